@@ -7,6 +7,8 @@ and streams.  There is no fallback: if libnq.so is missing, every call raises.
     import torch, block_quantized_weight_nq_amd as nq
     y = nq.dequantize_packed("gguf:q4_k", payload_u8_cuda, [4096, 4096], torch.bfloat16)
 """
+import collections
+import contextlib
 import ctypes
 import os
 
@@ -25,9 +27,12 @@ EXPORTS = ["nq_format_count", "nq_format_by_id", "nq_format_query", "nq_validate
            "nq_validate_fp8_row", "nq_dequantize_fp8_row", "nq_validate_grouped_absmax",
            "nq_quantize_grouped_absmax", "nq_validate_quantize_q8_1", "nq_quantize_q8_1",
            "nq_validate_gemv_q8_1", "nq_gemv_q8_1", "nq_validate_gemm_q8_1", "nq_gemm_q8_1_workspace", "nq_gemm_q8_1", "nq_gemm_q8_1_noalloc",
+           "nq_kv_tables", "nq_kv_store", "nq_kv_load", "nq_kv_attention_workspace", "nq_kv_attention",
            "nq_status_string"]
 GEMV_MAX_M = 8
 GQ_SCHEMES = {"q4_g64_fp16": (0, 64), "q5_g64_fp16": (1, 64), "q6_g64_fp16": (2, 64), "q8_g32_fp16": (3, 32)}
+KV_CODES = {"q8": 0, "e4m3": 1}
+KV_DIMS, KV_BLOCKS = (64, 128, 256), (16, 32, 64, 128)
 FP8_ROW_KINDS = {"fp8_e4m3fn_row_bf16": 0, "fp8_e4m3fn_row_fp16": 1}
 
 
@@ -52,6 +57,23 @@ class TensorDesc(ctypes.Structure):
     """nq_tensor: one tensor of nq_dequantize_packed_many."""
     _fields_ = [("format", ctypes.c_int32), ("rank", ctypes.c_int32), ("shape", ctypes.POINTER(ctypes.c_int64)),
                 ("payload", ctypes.c_void_p), ("nbytes", ctypes.c_uint64), ("out", ctypes.c_void_p)]
+
+
+class KvCacheDesc(ctypes.Structure):
+    """nq_kv_cache."""
+    _fields_ = [("code", ctypes.c_int32), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("block", ctypes.c_int32), ("blocks", ctypes.c_int64), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class KvAttentionArgs(ctypes.Structure):
+    """nq_kv_attention_args."""
+    _fields_ = [("q", ctypes.c_void_p), ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("tokens", ctypes.c_int64), ("q_heads", ctypes.c_int64), ("requests", ctypes.c_int64),
+                ("token_start", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("table_width", ctypes.c_int64), ("table_stride", ctypes.c_int64), ("window", ctypes.c_int64),
+                ("max_new", ctypes.c_int64), ("max_length", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 _LIB = None
@@ -100,6 +122,18 @@ def _lib():
                                    c.c_int64, c.c_void_p, c.c_void_p, c.c_uint64, c.c_void_p]
         L.nq_gemm_q8_1_noalloc.argtypes = [c.c_int32, c.c_void_p, c.c_uint64, c.c_int64, c.c_int64, c.c_void_p,
                                             c.c_int64, c.c_void_p, c.c_void_p]
+        L.nq_kv_tables.argtypes = [c.c_void_p, c.c_void_p, c.c_int64, c.c_void_p, c.c_int64, c.c_int64, c.c_void_p,
+                                   c.c_int64, c.c_void_p, c.c_int32, c.c_int64, c.c_void_p, c.c_void_p, c.c_void_p,
+                                   c.c_void_p, c.c_void_p, c.c_void_p]
+        L.nq_kv_store.argtypes = [c.POINTER(KvCacheDesc), c.c_void_p, c.c_int64, c.c_int64, c.c_void_p, c.c_int64,
+                                  c.c_int64, c.c_int64, c.c_int32, c.c_void_p, c.c_void_p, c.c_int64, c.c_void_p,
+                                  c.c_void_p]
+        L.nq_kv_load.argtypes = [c.POINTER(KvCacheDesc), c.c_void_p, c.c_int64, c.c_int32, c.c_void_p, c.c_void_p,
+                                 c.c_void_p]
+        L.nq_kv_attention_workspace.argtypes = [c.POINTER(KvCacheDesc), c.POINTER(KvAttentionArgs),
+                                                c.POINTER(c.c_uint64)]
+        L.nq_kv_attention.argtypes = [c.POINTER(KvCacheDesc), c.POINTER(KvAttentionArgs), c.c_void_p, c.c_uint64,
+                                      c.c_void_p]
         L.nq_status_string.argtypes = [c.c_int]
         L.nq_status_string.restype = c.c_char_p
         _LIB = L
@@ -520,3 +554,195 @@ def dequantize_packed(fmt, payload, shape, out_dtype=None, out=None, stream=None
     if st != NQ_OK:
         raise NqError(st, f"{fmt} {list(shape)}")
     return out
+
+
+class KvCache:
+    """A pool of blocks of an 8-bit key/value cache (one layer).
+
+    k: codes [blocks, heads, block, dim], v: [blocks, heads, dim, block], both torch.int8 ("q8") or both
+    torch.float8_e4m3fn ("e4m3"); k_scale, v_scale: float32 [blocks, heads].  Contiguous CUDA tensors that the
+    caller owns and that the calls below update in place.  KvCache.empty() allocates a pool.
+    """
+
+    def __init__(self, k, v, k_scale, v_scale):
+        import torch
+        codes = {torch.int8: "q8", torch.float8_e4m3fn: "e4m3"}
+        if k.dtype not in codes or v.dtype != k.dtype:
+            raise ValueError("k and v must both be torch.int8 or both torch.float8_e4m3fn")
+        if k.dim() != 4 or v.dim() != 4:
+            raise ValueError("k must be [blocks, heads, block, dim] and v [blocks, heads, dim, block]")
+        blocks, heads, block, dim = k.shape
+        if tuple(v.shape) != (blocks, heads, dim, block):
+            raise ValueError("k must be [blocks, heads, block, dim] and v [blocks, heads, dim, block]")
+        if dim not in KV_DIMS or block not in KV_BLOCKS or blocks < 1 or heads < 1:
+            raise ValueError(f"dim must be one of {KV_DIMS}, block one of {KV_BLOCKS}, blocks and heads at least 1")
+        for s in (k_scale, v_scale):
+            if s.dtype != torch.float32 or tuple(s.shape) != (blocks, heads):
+                raise ValueError("scales must be float32 [blocks, heads]")
+        for t in (k, v, k_scale, v_scale):
+            if not t.is_cuda or t.device != k.device or not t.is_contiguous():
+                raise ValueError("cache tensors must be contiguous CUDA tensors of one device")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.blocks, self.heads, self.block, self.dim, self.code = blocks, heads, block, dim, codes[k.dtype]
+        self.device = k.device
+        self._desc = KvCacheDesc(KV_CODES[self.code], heads, dim, block, blocks, k.data_ptr(), v.data_ptr(),
+                                 k_scale.data_ptr(), v_scale.data_ptr())
+        self._ref = ctypes.byref(self._desc)
+
+    @classmethod
+    def empty(cls, blocks, heads, block, dim, code="q8", device="cuda"):
+        """A pool with uninitialized contents (the calls never read what was not stored)."""
+        import torch
+        dtype = {"q8": torch.int8, "e4m3": torch.float8_e4m3fn}[code]
+        new = lambda shape, dt: torch.empty(shape, dtype=dt, device=device)  # noqa: E731
+        return cls(new((blocks, heads, block, dim), dtype), new((blocks, heads, dim, block), dtype),
+                   new((blocks, heads), torch.float32), new((blocks, heads), torch.float32))
+
+
+KvStep = collections.namedtuple("KvStep", "lengths token_start slots free_state status")
+
+
+def _on(stream, device):
+    """(stream, context to allocate in): new tensors belong to the stream that the work runs on."""
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream(device), contextlib.nullcontext()
+    return stream, torch.cuda.stream(stream)
+
+
+def _device_ints(device, dtype, **tensors):
+    for name, t in tensors.items():
+        if t.dtype != dtype or not t.is_cuda or t.device != device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor on {device}")
+
+
+def _block_table(table, requests, device, dtype):
+    if table.dim() != 2 or table.shape[0] != requests or table.dtype != dtype or table.device != device or \
+            table.shape[1] < 1 or table.stride(1) != 1:
+        raise ValueError(f"table must be {dtype} [{requests}, width] on {device}, each row contiguous")
+
+
+def kv_tables(lengths, added, table, ring, free_state, block, tokens, stream=None):
+    """Block tables, slots and token starts of one serving step, on the GPU.
+
+    lengths, added: int32 [requests], the tokens a request holds and its new ones (-1: it ends); table: int32
+    [requests, width]; ring: int32 [ring size], the free blocks from free_state = int32 [head, count]; tokens:
+    room for the step's new tokens.  table and ring are updated in place.  Returns KvStep(lengths, token_start
+    [requests + 1], slots int64 [tokens], free_state, status int32 [1]); nothing changes if status is not 0 (1: too
+    few free blocks, 2: a bad length, 4: more than `tokens` new tokens, 8: the ring cannot hold the blocks).
+    """
+    import torch
+    device = lengths.device
+    n = lengths.numel()
+    _device_ints(device, torch.int32, lengths=lengths, added=added, ring=ring, free_state=free_state)
+    _block_table(table, n, device, torch.int32)
+    if added.numel() != n or free_state.numel() != 2:
+        raise ValueError("added must have one entry for each request and free_state two")
+    stream, ctx = _on(stream, device)
+    with ctx:
+        words = torch.empty(2 * n + 4, dtype=torch.int32, device=device)
+        slots = torch.empty(int(tokens), dtype=torch.int64, device=device)
+    p = words.data_ptr()
+    st = _lib().nq_kv_tables(lengths.data_ptr(), added.data_ptr(), n, table.data_ptr(), table.shape[1],
+                             table.stride(0), ring.data_ptr(), ring.numel(), free_state.data_ptr(), block, tokens, p,
+                             p + 4 * n, slots.data_ptr(), p + 8 * n + 4, p + 8 * n + 12, stream.cuda_stream)
+    if st != NQ_OK:
+        raise NqError(st, f"{n} requests, table {list(table.shape)}, block {block}, {tokens} tokens")
+    return KvStep(words[:n], words[n:2 * n + 1], slots, words[2 * n + 1:2 * n + 3], words[2 * n + 3:])
+
+
+def _heads_of(name, x, cache, heads=None):
+    if x.dim() != 3 or x.shape[2] != cache.dim or (heads and x.shape[1] != heads) or x.device != cache.device or \
+            (x.numel() and x.stride(2) != 1):
+        raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {cache.dim}] on {cache.device}, "
+                         "channels contiguous")
+
+
+def kv_store(cache, k, v, slots, token_start, stream=None):
+    """Quantize new keys and values ([tokens, heads, dim], float32, float16 or bfloat16, any token and head strides)
+    into their blocks.  slots: int64 [tokens], token_start: int32 [requests + 1] (as kv_tables returns them).
+    Returns status int32 [1]: 1 a value is not finite (NaN is stored as 0, infinities saturate), 2 a slot outside
+    the pool or out of order (that block's tokens are not stored)."""
+    import torch
+    _heads_of("k", k, cache, cache.heads)
+    _heads_of("v", v, cache, cache.heads)
+    if v.dtype != k.dtype or v.shape[0] != k.shape[0]:
+        raise ValueError("k and v must have one type and one number of tokens")
+    _device_ints(cache.device, torch.int64, slots=slots)
+    _device_ints(cache.device, torch.int32, token_start=token_start)
+    n = k.shape[0]
+    if slots.numel() < n or token_start.numel() < 2:
+        raise ValueError("slots needs one entry for each token and token_start one for each request and one more")
+    stream, ctx = _on(stream, cache.device)
+    with ctx:
+        status = torch.empty(1, dtype=torch.int32, device=cache.device)
+    st = _lib().nq_kv_store(cache._ref, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
+                            v.stride(1), n, _dtype_code(k.dtype), slots.data_ptr(), token_start.data_ptr(),
+                            token_start.numel() - 1, status.data_ptr(), stream.cuda_stream)
+    if st != NQ_OK:
+        raise NqError(st, f"k {list(k.shape)} {k.dtype}")
+    return status
+
+
+def kv_load(cache, ids, out_dtype=None, stream=None):
+    """Keys and values of whole blocks (ids: int32 [n]), each [n, block, heads, dim] in out_dtype (default float32)."""
+    import torch
+    _device_ints(cache.device, torch.int32, ids=ids)
+    out_dtype = out_dtype or torch.float32
+    code = _dtype_code(out_dtype)
+    shape = (ids.numel(), cache.block, cache.heads, cache.dim)
+    stream, ctx = _on(stream, cache.device)
+    with ctx:
+        k = torch.empty(shape, dtype=out_dtype, device=cache.device)
+        v = torch.empty(shape, dtype=out_dtype, device=cache.device)
+    st = _lib().nq_kv_load(cache._ref, ids.data_ptr(), ids.numel(), code, k.data_ptr(), v.data_ptr(),
+                           stream.cuda_stream)
+    if st != NQ_OK:
+        raise NqError(st, f"{ids.numel()} blocks as {out_dtype}")
+    return k, v
+
+
+def kv_attention(cache, q, token_start, lengths, table, scale=None, window=0, max_new=None, max_length=None,
+                 return_lse=False, stream=None):
+    """Causal attention of new tokens over a cache that already holds their keys and values.
+
+    q: [tokens, q_heads, dim] (float32, float16 or bfloat16; any token and head strides), q_heads a multiple of
+    cache.heads; token_start: int32 [requests + 1]; lengths: int32 [requests], new tokens included; table: int32
+    [requests, width].  scale: default dim ** -0.5; window: keys a token sees at most, 0 for all.  max_new and
+    max_length bound a request's new tokens and length (default: `tokens` and what the table can name); tight
+    bounds save launches of idle workgroups.  Returns out in q's type and shape, and with return_lse also the
+    natural logarithms of the sums, float32 [tokens, q_heads].
+    """
+    import torch
+    _heads_of("q", q, cache)
+    n, q_heads, dim = q.shape
+    requests = lengths.numel()
+    _device_ints(cache.device, torch.int32, token_start=token_start, lengths=lengths)
+    _block_table(table, requests, cache.device, torch.int32)
+    if token_start.numel() != requests + 1:
+        raise ValueError("token_start must have one entry more than lengths")
+    if max_new is None:
+        max_new = max(1, n)
+    if max_length is None:
+        max_length = table.shape[1] * cache.block
+    code = _dtype_code(q.dtype)
+    stream, ctx = _on(stream, cache.device)
+    with ctx:
+        out = torch.empty((n, q_heads, dim), dtype=q.dtype, device=cache.device)
+        lse = torch.empty((n, q_heads), dtype=torch.float32, device=cache.device) if return_lse else None
+        args = KvAttentionArgs(q.data_ptr(), q.stride(0), q.stride(1), n, q_heads, requests, token_start.data_ptr(),
+                               lengths.data_ptr(), table.data_ptr(), table.shape[1], table.stride(0), window, max_new,
+                               max_length, out.data_ptr(), lse.data_ptr() if return_lse else None, code,
+                               dim ** -0.5 if scale is None else scale)
+        ref, need, lib = ctypes.byref(args), ctypes.c_uint64(), _lib()
+        st = lib.nq_kv_attention_workspace(cache._ref, ref, ctypes.byref(need))
+        ws = None
+        if st == NQ_OK:
+            if need.value:
+                ws = torch.empty(need.value, dtype=torch.uint8, device=cache.device)
+            st = lib.nq_kv_attention(cache._ref, ref, ws.data_ptr() if need.value else None, need.value,
+                                     stream.cuda_stream)
+    if st != NQ_OK:
+        raise NqError(st, f"q {list(q.shape)} {q.dtype}, {requests} requests, table {list(table.shape)}, "
+                          f"window {window}, max_new {max_new}, max_length {max_length}")
+    return (out, lse) if return_lse else out

@@ -13,9 +13,9 @@ include/nq.h.  Flags that matter for exactness:
 * ``-Xclang -target-feature -Xclang -packed-fp32-ops`` is passed as given (the
   build never emits packed-fp32 VALU instructions).
 
-The matrix-core product units (k_gemm_*.hip) also take
+The matrix-core units (k_gemm_*.hip, k_kv_attn_*.hip) also take
 ``-mllvm -amdgpu-mfma-vgpr-form=1``: MFMA results land in VGPRs, so the
-binary32 scaling reads them without an AGPR copy per value.
+binary32 scaling and the softmax read them without an AGPR copy per value.
 """
 import concurrent.futures
 import os
@@ -32,8 +32,9 @@ KERNEL_SOURCES = ["k_simple.hip", "k_kquant.hip", "k_iq.hip", "k_fp4.hip", "k_te
                   "k_gqenc.hip", "k_q8_1.hip", "k_gemv_simple.hip", "k_gemv_kquant.hip", "k_gemv_iq.hip",
                   "k_gemv_fp4t.hip", "k_gemm_simple.hip", "k_gemm_kquant.hip", "k_gemm_iq.hip",
                   "k_gemm_fp4t.hip", "k_many_simple.hip", "k_many_kquant.hip", "k_many_iq.hip", "k_many_fp4.hip",
-                  "k_many_ternary.hip", "k_measure.hip"]
-HOST_SOURCES = ["nq_abi.cpp", "nq_noalloc.hip"]
+                  "k_many_ternary.hip", "k_measure.hip", "k_kv_tables.hip", "k_kv_store.hip", "k_kv_attn_q8.hip",
+                  "k_kv_attn_e4m3.hip"]
+HOST_SOURCES = ["nq_abi.cpp", "nq_noalloc.hip", "nq_kv_abi.cpp"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-ffp-contract=off",
           "-fno-fast-math", "-Wall", "-Wno-unused-function"]
@@ -61,7 +62,7 @@ SAN_HOST = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=unde
 
 def _compile(src, is_kernel, build_dir=BUILD, defines=(), sanitize=False):
     obj = os.path.join(build_dir, os.path.splitext(src)[0] + ".o")
-    extra = MFMA_UNITS if src.startswith("k_gemm_") else []
+    extra = MFMA_UNITS if src.startswith(("k_gemm_", "k_kv_attn_")) else []
     if sanitize and src in HOST_SOURCES:
         extra = extra + SAN_HOST
     cmd = [_hipcc(), *COMMON, *DEVICE, *extra, *[f"-D{d}" for d in defines], "-x", "hip", "-c",

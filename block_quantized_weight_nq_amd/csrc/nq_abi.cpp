@@ -89,6 +89,10 @@ uint32_t resident_workgroups() { return compute_units() * NQ_RESIDENT_PER_CU; }
 
 }  // namespace
 
+namespace nq {
+uint32_t device_compute_units() { return compute_units(); }
+}  // namespace nq
+
 NQ_API int nq_format_count(void) { return nq::NUM_FORMATS; }
 
 NQ_API int nq_format_by_id(int32_t id, nq_format_info *out) {
@@ -514,7 +518,7 @@ NQ_API const char *nq_status_string(int status) {
     case NQ_ERR_HIP: return "HIP launch failed";
     case NQ_ERR_BAD_DIVISORS: return "divisors must be in [1, 2^30] and divide the row count";
     case NQ_ERR_MISALIGNED: return "a pointer is not aligned as the call requires";
-    case NQ_ERR_SCRATCH: return "the shape needs more workspace than the static scratch holds; use nq_gemm_q8_1";
+    case NQ_ERR_SCRATCH: return "the call needs more workspace than it has (the static scratch, or the one passed)";
     default: return "unknown status";
     }
 }

@@ -1,0 +1,179 @@
+// nq_kv.h -- the 8-bit key/value cache: layouts, host-checkable index rules and launch arguments.
+//
+// A cache is a pool of blocks of T tokens (T = 16, 32, 64 or 128).  A block
+// holds, for each of H key/value heads, T x D key codes ([T][D], a token's
+// codes contiguous) and D x T value codes ([D][T], a channel's tokens
+// contiguous), one binary32 scale for its keys and one for its values.  A
+// code c stands for RN32(c * scale); c is a signed byte in -127..127 or an
+// E4M3FN word.  The two layouts are the ones the attention's matrix
+// instructions read without a transpose: scores contract over the channels of
+// a key, outputs over the tokens of a channel.
+//
+// The functions marked NQ_HD decide which bytes a kernel touches; a host
+// build runs them to check every address against the buffers.
+#pragma once
+
+#include "nq_decode.h"
+
+namespace nq {
+
+constexpr int KV_Q8 = 0, KV_E4M3 = 1;
+constexpr float KV_TINY = 1.17549435082228750797e-38f;  // 2^-126, the least scale
+
+// Status bits the kernels set.
+constexpr uint32_t KV_ST_NOT_FINITE = 1u, KV_ST_BAD_SLOT = 2u;                     // store
+constexpr uint32_t KV_ST_NO_BLOCKS = 1u, KV_ST_BAD_LENGTH = 2u, KV_ST_TOKENS = 4u, KV_ST_RING = 8u;  // tables
+
+struct KvPool {
+    uint8_t *k, *v;
+    float *ks, *vs;
+    int64_t blocks;
+    uint32_t heads, dim, bsh;  // T = 1 << bsh
+};
+
+// Byte offset of (block, head) in either code pool.
+NQ_HD int64_t kv_tile_at(const KvPool &c, int64_t block, uint32_t head) {
+    return (block * (int64_t)c.heads + (int64_t)head) * (int64_t)((uint64_t)c.dim << c.bsh);
+}
+
+// ---------------------------------------------------------------------------
+// Store: which tokens a workgroup writes
+// ---------------------------------------------------------------------------
+// A request's tokens are consecutive positions, so the blocks they fall into
+// follow from the offset of its first token.  n tokens touch at most
+// floor(n / T) + 2 blocks, so request r owns the units floor(s_r / T) + 2 r
+// up to those of request r + 1: the launch needs no host copy of the starts.
+NQ_HD int64_t kv_unit_first(int64_t start, int64_t r, uint32_t bsh) { return (start >> bsh) + 2 * r; }
+
+// Tokens [lo, hi) of unit j of a request whose tokens are [s0, s1) and whose
+// first one sits at offset off0 of its block.
+NQ_HD void kv_unit_tokens(int64_t s0, int64_t s1, int64_t j, int64_t off0, uint32_t bsh, int64_t *lo, int64_t *hi) {
+    const int64_t T = (int64_t)1 << bsh;
+    const int64_t a = s0 + j * T - off0, b = a + T;
+    *lo = a > s0 ? a : s0;
+    *hi = b < s1 ? b : s1;
+}
+
+// ---------------------------------------------------------------------------
+// Attention: which keys a row tile reads
+// ---------------------------------------------------------------------------
+// The rows of a request and key head are its new tokens times the query heads
+// that share the key head, token-major; a tile is ROWS of them.
+struct KvTile {
+    int rows;         // rows of the request (all tiles)
+    int base;         // position of the request's first new token (negative if it has fewer keys than new tokens)
+    int live;         // keys the request has
+    int first, last;  // the tile's first and last new token
+    int kb;           // first key that some row sees
+    int kbeg, kend;   // keys the tile reads: kbeg is kb rounded down to a multiple of 64
+    int nsplit;       // pieces of `chunk` keys, at least 1
+};
+
+NQ_HD KvTile kv_tile(int added, int length, int cap, int group, int tile, int ROWS, int window, int chunk) {
+    KvTile t;
+    t.rows = added * group;
+    t.base = length - added;
+    t.live = length < cap ? length : cap;
+    if (t.live < 0) t.live = 0;
+    const int row0 = tile * ROWS;
+    const int rowl = (row0 + ROWS < t.rows ? row0 + ROWS : t.rows) - 1;
+    t.first = row0 / group;
+    t.last = rowl / group;
+    int kend = t.base + t.last + 1;
+    if (kend > t.live) kend = t.live;
+    t.kend = kend < 0 ? 0 : kend;
+    int kb = window > 0 ? t.base + t.first - window + 1 : 0;
+    if (kb > t.kend) kb = t.kend;
+    t.kb = kb < 0 ? 0 : kb;
+    t.kbeg = t.kb & ~63;
+    t.nsplit = (t.kend - t.kbeg + chunk - 1) / chunk;
+    if (t.nsplit < 1) t.nsplit = 1;
+    return t;
+}
+
+// Block of key position `key` (a multiple of 16 or inside such a run), or -1
+// where the tile must not look: past its keys, before its window, or where
+// the table names no block of the pool.
+template <class Table>
+NQ_HD int kv_page(const Table &table, int key, const KvTile &t, uint32_t bsh, int64_t blocks) {
+    const int idx = key >> bsh;
+    if (key >= t.kend || ((idx + 1) << bsh) <= t.kb) return -1;
+    const int p = table(idx);
+    return p >= 0 && (int64_t)p < blocks ? p : -1;
+}
+
+// Byte offsets of a key's codes and of a channel's codes from token `key` on,
+// in the block `page` that kv_page named (block 0 stands in for -1: what is
+// read there is masked).
+NQ_HD int64_t kv_k_at(const KvPool &c, int page, uint32_t head, int key) {
+    return kv_tile_at(c, page < 0 ? 0 : page, head) + (int64_t)(key & ((1 << c.bsh) - 1)) * c.dim;
+}
+NQ_HD int64_t kv_v_at(const KvPool &c, int page, uint32_t head, int channel, int key) {
+    return kv_tile_at(c, page < 0 ? 0 : page, head) + ((int64_t)channel << c.bsh) + (key & ((1 << c.bsh) - 1));
+}
+
+// ---------------------------------------------------------------------------
+// Launch arguments
+// ---------------------------------------------------------------------------
+struct KvTablesLaunch {
+    const int32_t *lengths, *added;
+    int32_t *table, *ring;
+    const int32_t *state;
+    int32_t *lengths_out, *starts;
+    int64_t *slots;
+    int32_t *state_out;
+    uint32_t *status;
+    int64_t table_stride, tokens;
+    int32_t requests, width, ring_size;
+    uint32_t bsh;
+};
+int launch_kv_tables(const KvTablesLaunch &L, hipStream_t s);
+
+struct KvStoreLaunch {
+    KvPool c;
+    const void *x[2];           // new keys, new values
+    int64_t ts[2], hs[2];       // their token and head strides in elements
+    const int64_t *slots;
+    const int32_t *starts;
+    uint32_t *status;
+    int64_t tokens;
+    int32_t requests, code, in_dtype;
+};
+int launch_kv_store(const KvStoreLaunch &L, hipStream_t s);
+
+struct KvLoadLaunch {
+    KvPool c;
+    const int32_t *ids;
+    void *out[2];
+    int64_t n;
+    int32_t code, out_dtype;
+};
+int launch_kv_load(const KvLoadLaunch &L, hipStream_t s);
+
+struct KvAttnLaunch {
+    KvPool c;
+    const void *q;
+    int64_t q_ts, q_hs;  // token and head strides of q in elements
+    const int32_t *starts, *lengths, *table;
+    int64_t table_stride;
+    void *out;           // [tokens, q_heads, dim], contiguous
+    float *lse;          // [tokens, q_heads] or NULL
+    float *part;         // normalized outputs of the pieces, [tokens, q_heads, max_splits, dim]
+    float *part_lse;     // their base-2 logarithms of the sums, [tokens, q_heads, max_splits]
+    int32_t tokens, requests, q_heads, group;
+    int32_t cap;         // keys a request can have: max_length, and what its table row can name
+    int32_t max_new, window, chunk, max_splits, tiles;
+    int32_t code, dtype;
+    float scale;
+};
+
+struct KvAttnPlan {
+    int rows;            // rows of a tile
+    int tiles;           // tiles of a request and key head
+    int chunk;           // keys of a piece
+    int max_splits;      // most pieces of a tile
+};
+KvAttnPlan kv_attn_plan(const KvAttnLaunch &L, uint32_t cus);
+int launch_kv_attn(const KvAttnLaunch &L, hipStream_t s);
+
+}  // namespace nq

@@ -1,0 +1,482 @@
+// nq_kv_attn.h -- attention over the 8-bit key/value cache.
+//
+// For a new token at position p of its request, query head h and key head
+// h / group, over the keys j <= p of the request (and j > p - window):
+//   s_j = scale * ks_j * sum_c q_c kc_jc,  out = sum_j softmax(s)_j * vs_j * vc_j,
+//   lse = ln sum_j exp(s_j),
+// with ks, vs the block scales and kc, vc the codes.  A row that sees no key
+// gives out = 0 and lse = -inf.
+//
+// Arithmetic.  A code is exact in binary16, so the products run on
+// the binary16 matrix instructions with binary32 accumulation:
+//   * a query row is multiplied by a power of two that brings its largest
+//     element to [2^14, 2^15): binary16 and bfloat16 queries are then exact
+//     (bfloat16's smaller elements down to 2^-39 of the largest); a binary32
+//     query is the sum of two binary16 terms, exact to 2^-24 of an element;
+//   * exp(s_j - m) vs_j / vref, at most 1, times 2^14 is rounded to binary16
+//     (2^-11 of its value), or to two terms for binary32 queries (2^-22).
+//     Weights too small for that precision (below 2^-28 of 1, or 2^-17 in two
+//     terms; a wave sees whether its tile has any) are multiplied up and
+//     added by products of their own: a channel in which the dominant keys
+//     are 0 keeps the relative precision of what is left;
+//   * maxima, sums, outputs and the block scales stay in binary32, the
+//     running maximum m in base-2 logarithms.
+// vref is the largest value scale met so far; like m, it is a factor of the
+// running output and is corrected when it grows.
+#pragma once
+
+#include "nq_kv_codes.h"
+
+namespace nq {
+
+constexpr float KV_LOG2E = 1.44269504088896340736f, KV_LN2 = 0.69314718055994530942f;
+constexpr float KV_PSCALE = 16384.0f;  // 2^14
+
+// Weights (times 2^14) below LEAST lose precision in binary16 (in the second
+// term, for two); UP brings the next level to just below 2^14.
+template <int TERMS>
+struct KvLevel {
+    static constexpr float LEAST = TERMS == 1 ? 0x1p-14f : 0x1p-3f;
+    static constexpr float UP = TERMS == 1 ? 0x1p28f : 0x1p17f;
+};
+
+struct KvAttnArgs {
+    KvAttnLaunch L;
+};
+
+// 2^x, v_exp_f32 (1 ulp; results below 2^-126 are 0)
+__device__ __forceinline__ float kv_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The power of two that brings amax to [2^14, 2^15) (1 where amax is 0, infinite or NaN).
+__device__ __forceinline__ float kv_row_scale(float amax) {
+    const uint32_t e = (__builtin_bit_cast(uint32_t, amax) >> 23) & 0xFFu;
+    if (e == 255u || amax == 0.0f) return 1.0f;
+    const int s = 127 + 14 + 127 - (int)e;  // e = 0: a subnormal row stays below 2^14
+    return bits_f32((uint32_t)(s > 250 ? 250 : s) << 23);
+}
+
+__device__ __forceinline__ float kv_xor_max(float x, int d) { return fmaxf(x, __shfl_xor(x, d, 64)); }
+__device__ __forceinline__ float kv_xor_add(float x, int d) { return x + __shfl_xor(x, d, 64); }
+
+// Rows of a request's table, as kv_page reads them.
+struct KvTableRow {
+    const int32_t *row;
+    __device__ __forceinline__ int operator()(int i) const { return row[i]; }
+};
+
+// A request's token range and length, made safe: starts inside [0, tokens].
+struct KvReq {
+    int s0, s1, len;
+};
+__device__ __forceinline__ KvReq kv_request(const KvAttnLaunch &a, int r) {
+    KvReq q;
+    q.s0 = a.starts[r];
+    q.s1 = a.starts[r + 1];
+    q.len = a.lengths[r];
+    q.s0 = q.s0 < 0 ? 0 : q.s0 > a.tokens ? a.tokens : q.s0;
+    q.s1 = q.s1 < q.s0 ? q.s0 : q.s1 > a.tokens ? a.tokens : q.s1;
+    if (q.s1 - q.s0 > a.max_new) q.s1 = q.s0 + a.max_new;
+    if (q.len < 0) q.len = 0;
+    return q;
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: one wave per run of keys
+// ---------------------------------------------------------------------------
+// A tile is 16 rows (the matrix instruction's width).  A workgroup has four
+// waves; wave w takes the key tiles w, w + 4, ... of its piece, keeps its own
+// maximum, sum and output, and the four are joined at the end.  Codes go from
+// memory to registers in the operands' own order, 16 bytes a lane: nothing is
+// staged, so nothing waits but the loads.  Per KT keys (64; 32 for 256
+// channels) with lane = 16 g + r:
+//   scores  A = keys [16][32 channels]: row r of key tile t is key KT/4 * (r/4)
+//           + 4 t + r%4, channels 64 a + 16 g + 8 b ..+7 for step 2 a + b;
+//           the result gives lane (r = query row, g) the keys KT/4 * g + 4 t + i;
+//   output  A = values [16 channels][32 keys]: channel 16 dt + r, keys
+//           KT/4 * g + 8 b ..+7: just those of the lane's own scores, so the
+//           probabilities are the B operand where they are.
+// The keys of a lane lie in one block, so its scales are two registers.
+template <int CODE, int DIM, int IN, int TERMS>
+struct KvDec {
+    static constexpr int KT = DIM > 128 ? 32 : 64;  // keys of a tile
+    static constexpr int KPG = KT / 4;              // keys of a lane
+    static constexpr int NT = KT / 16;              // score tiles
+    static constexpr int NA = DIM / 64;             // 16-byte loads of a key
+    static constexpr int ND = DIM / 16;             // output tiles
+    static constexpr int NB = KT / 32;              // steps of the output product
+    static constexpr int OS = DIM + 4;              // row stride of the joined output in LDS
+    static constexpr int LDS_FLOATS = 4 * 16 * OS + 2 * 64 + 4;
+};
+
+template <int CODE, int DIM, int IN, int TERMS>
+__global__ __launch_bounds__(256, 2) void k_kv_attn_dec(KvAttnArgs args) {
+    using C = KvDec<CODE, DIM, IN, TERMS>;
+    constexpr int KT = C::KT, KPG = C::KPG, NT = C::NT, NA = C::NA, ND = C::ND, NB = C::NB;
+    extern __shared__ float lds[];
+    const KvAttnLaunch &a = args.L;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
+    const uint32_t head = blockIdx.x % a.c.heads;
+    const int tile = (int)(blockIdx.x / a.c.heads), split = (int)blockIdx.y, req = (int)blockIdx.z;
+    const int group = a.group;
+
+    if (req == a.requests) {  // tokens of no request: zeros
+        if (split != 0) return;
+        int s = a.starts[a.requests];
+        s = s < 0 ? 0 : s;
+        for (int64_t tok = (int64_t)s + tile; tok < a.tokens; tok += a.tiles)
+            for (int i = tid; i < group * DIM; i += 256) {
+                const int64_t row = tok * a.q_heads + (int64_t)head * group + i / DIM;
+                if constexpr (IN == 0)
+                    ((float *)a.out)[row * DIM + i % DIM] = 0.0f;
+                else
+                    ((uint16_t *)a.out)[row * DIM + i % DIM] = 0;
+                if (a.lse && i % DIM == 0) a.lse[row] = -__builtin_inff();
+            }
+        return;
+    }
+    const KvReq q = kv_request(a, req);
+    if (tile * 16 >= (q.s1 - q.s0) * group) return;
+    const KvTile t = kv_tile(q.s1 - q.s0, q.len, a.cap, group, tile, 16, a.window, a.chunk);
+    if (split >= t.nsplit) return;
+    const int k0 = t.kbeg + split * a.chunk;
+    const int k1 = t.kend - k0 > a.chunk ? k0 + a.chunk : t.kend;
+
+    // this lane's query row (as the column of the score tiles)
+    const int row = tile * 16 + r, tok = row / group;
+    const bool has = row < t.rows;
+    const int p = t.base + tok;
+    const int hi = has ? (p + 1 < t.live ? p + 1 : t.live) : 0;
+    const int lo = a.window > 0 && p - a.window + 1 > 0 ? p - a.window + 1 : 0;
+    const int all_hi = t.base + t.first + 1 < t.live ? t.base + t.first + 1 : t.live;
+    const int all_lo = a.window > 0 ? t.base + t.last - a.window + 1 : 0;
+    kv_h8 Q[TERMS][2 * NA];
+    float qscale;
+    {
+        float f[NA][16];
+        float amax = 0.0f;
+        const int64_t at = (int64_t)(q.s0 + (has ? tok : 0)) * a.q_ts + ((int64_t)head * group + (has ? row % group : 0)) * a.q_hs;
+#pragma unroll
+        for (int i = 0; i < NA; i++)
+#pragma unroll
+            for (int k = 0; k < 16; k++) {
+                f[i][k] = has ? kv_read<IN>(a.q, at + 64 * i + 16 * g + k) : 0.0f;
+                amax = fmaxf(amax, fabsf(f[i][k]));
+            }
+        amax = kv_xor_max(kv_xor_max(amax, 16), 32);
+        const float up = kv_row_scale(amax);
+        qscale = a.scale * KV_LOG2E / up;
+#pragma unroll
+        for (int i = 0; i < NA; i++)
+#pragma unroll
+            for (int k = 0; k < 16; k++) {
+                const float x = f[i][k] * up;
+                const _Float16 h = (_Float16)x;
+                Q[0][2 * i + (k >> 3)][k & 7] = h;
+                if constexpr (TERMS == 2) Q[1][2 * i + (k >> 3)][k & 7] = (_Float16)(x - (float)h);
+            }
+    }
+
+    const KvTableRow table = {a.table + (int64_t)req * a.table_stride};
+    const uint32_t bsh = a.c.bsh;
+    const int kr = KPG * (r >> 2) + (r & 3);  // key of row r in score tile 0
+
+    kv_u4 K[NT][NA];
+    kv_u2 V[ND][NB];
+    kv_f4 O[ND];
+#pragma unroll
+    for (int d = 0; d < ND; d++) O[d] = kv_f4{0, 0, 0, 0};
+    float m = -__builtin_inff(), l = 0.0f, vref = KV_TINY;
+
+    auto load_k = [&](int key0) {
+        const int pg = kv_page(table, key0 + KPG * (r >> 2), t, bsh, a.c.blocks);
+        const uint8_t *src = a.c.k + kv_k_at(a.c, pg, head, key0 + kr) + 16 * g;
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int i = 0; i < NA; i++) K[n][i] = *(const kv_u4 *)(src + 4 * n * DIM + 64 * i);
+    };
+
+    int key0 = k0 + wave * KT;
+    if (key0 < k1) load_k(key0);
+    for (; key0 < k1; key0 += 4 * KT) {
+        // values and scales of the lane's own keys
+        const int kv0 = key0 + KPG * g;
+        const int pg = kv_page(table, kv0, t, bsh, a.c.blocks);
+        const int64_t sc_at = (int64_t)(pg < 0 ? 0 : pg) * a.c.heads + head;
+        float ks = a.c.ks[sc_at], vs = a.c.vs[sc_at];
+        if (pg < 0) ks = vs = 0.0f;
+        {
+            const uint8_t *src = a.c.v + kv_v_at(a.c, pg, head, r, kv0);
+#pragma unroll
+            for (int d = 0; d < ND; d++) {
+                if constexpr (NB == 2) {
+                    const kv_u4 w = *(const kv_u4 *)(src + ((int64_t)d << (bsh + 4)));
+                    V[d][0] = kv_u2{w[0], w[1]};
+                    V[d][NB - 1] = kv_u2{w[2], w[3]};
+                } else {
+                    V[d][0] = *(const kv_u2 *)(src + ((int64_t)d << (bsh + 4)));
+                }
+            }
+        }
+        kv_f4 S[NT];
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            S[n] = kv_f4{0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < NA; i++)
+#pragma unroll
+                for (int b = 0; b < 2; b++) {
+                    const kv_h8 kk = kv_codes8_f16<CODE>(kv_u2{K[n][i][2 * b], K[n][i][2 * b + 1]});
+#pragma unroll
+                    for (int e = 0; e < TERMS; e++)
+                        S[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kk, Q[e][2 * i + b], S[n], 0, 0, 0);
+                }
+        }
+        if (key0 + 4 * KT < k1) load_k(key0 + 4 * KT);
+
+        const float cf = qscale * ks;
+        const bool dead = pg < 0;
+        const bool edge = key0 < all_lo || key0 + KT > all_hi || __ballot(dead) != 0;
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) S[n][i] *= cf;
+        if (edge) {
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int key = kv0 + 4 * n + i;
+                    if (dead || key < lo || key >= hi) S[n][i] = -__builtin_inff();
+                }
+            // codes of places that hold no key may be anything: E4M3's NaN among them
+#pragma unroll
+            for (int d = 0; d < ND; d++)
+#pragma unroll
+                for (int b = 0; b < NB; b++)
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        uint32_t keep = 0;
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            const int key = kv0 + 8 * b + 4 * h + i;
+                            if (!dead && key >= t.kb && key < t.kend) keep |= 0xFFu << (8 * i);
+                        }
+                        V[d][b][h] &= keep;
+                    }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) top = fmaxf(top, S[n][i]);
+        top = kv_xor_max(kv_xor_max(top, 16), 32);
+        const float m1 = fmaxf(m, top), safe = m1 == -__builtin_inff() ? 0.0f : m1;
+        const float vr1 = fmaxf(vref, kv_xor_max(kv_xor_max(fabsf(vs), 16), 32));
+        const float alpha = kv_exp2(m - safe), beta = alpha * (vref / vr1);
+        const float pv = vs / vr1 * KV_PSCALE;
+        m = m1;
+        vref = vr1;
+        l *= alpha;
+        float x[NT][4], least = KV_PSCALE;
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float e = kv_exp2(S[n][i] - safe);
+                l += e;
+                x[n][i] = e * pv;
+                least = fminf(least, fabsf(x[n][i]));
+            }
+#pragma unroll
+        for (int d = 0; d < ND; d++) O[d] *= beta;
+        // O += values * weights, or for the small weights values * (weights * UP^k) / UP^k
+        auto add = [&](const float (&w)[NT][4], float back) {
+            kv_h8 P[TERMS][NB];
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const _Float16 h = (_Float16)w[n][i];
+                    P[0][n >> 1][4 * (n & 1) + i] = h;
+                    if constexpr (TERMS == 2) P[1][n >> 1][4 * (n & 1) + i] = (_Float16)(w[n][i] - (float)h);
+                }
+#pragma unroll
+            for (int d = 0; d < ND; d++) {
+                kv_f4 acc = back == 1.0f ? O[d] : kv_f4{0, 0, 0, 0};
+#pragma unroll
+                for (int b = 0; b < NB; b++) {
+                    const kv_h8 vv = kv_codes8_f16<CODE>(V[d][b]);
+#pragma unroll
+                    for (int e = 0; e < TERMS; e++)
+                        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, P[e][b], acc, 0, 0, 0);
+                }
+                if (back == 1.0f)
+                    O[d] = acc;
+                else
+                    O[d] += acc * back;
+            }
+        };
+        if (__ballot(least < KvLevel<TERMS>::LEAST)) {
+            float w[NT][4], back = 1.0f;
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    w[n][i] = fabsf(x[n][i]) < KvLevel<TERMS>::LEAST ? x[n][i] : 0.0f;
+                    x[n][i] -= w[n][i];
+                }
+            for (;;) {
+                float most = 0.0f, now[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; n++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        w[n][i] *= KvLevel<TERMS>::UP;
+                        most = fmaxf(most, fabsf(w[n][i]));
+                        now[n][i] = fabsf(w[n][i]) < KvLevel<TERMS>::LEAST ? 0.0f : w[n][i];
+                        w[n][i] -= now[n][i];
+                    }
+                back *= 1.0f / KvLevel<TERMS>::UP;
+                if (!__ballot(most > 0.0f)) break;  // most < 2^-149 * UP^k: at most 9 rounds
+                add(now, back);
+            }
+        }
+        add(x, 1.0f);
+    }
+    l = kv_xor_add(kv_xor_add(l, 16), 32);
+
+    // Join the four waves.
+    float *so = lds + wave * 16 * C::OS, *sm = lds + 4 * 16 * C::OS, *sl = sm + 64, *sv = sl + 64;
+#pragma unroll
+    for (int d = 0; d < ND; d++) *(kv_f4 *)(so + r * C::OS + 16 * d + 4 * g) = O[d];
+    if (g == 0) {
+        sm[wave * 16 + r] = m;
+        sl[wave * 16 + r] = l;
+    }
+    if (lane == 0) sv[wave] = vref;
+    __syncthreads();
+    const int orow = tid >> 4, c0 = (tid & 15) * ND;
+    if (tile * 16 + orow >= t.rows) return;
+    float mm = -__builtin_inff();
+#pragma unroll
+    for (int w = 0; w < 4; w++) mm = fmaxf(mm, sm[w * 16 + orow]);
+    const float safe = mm == -__builtin_inff() ? 0.0f : mm;
+    float sum = 0.0f, fw[4];
+#pragma unroll
+    for (int w = 0; w < 4; w++) {
+        const float e = kv_exp2(sm[w * 16 + orow] - safe);
+        sum += e * sl[w * 16 + orow];
+        fw[w] = e;
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int w = 0; w < 4; w++) fw[w] = fw[w] * inv * (sv[w] * (1.0f / KV_PSCALE));
+    const float lse2 = sum == 0.0f ? -__builtin_inff() : safe + __builtin_amdgcn_logf(sum);
+    const int otok = (tile * 16 + orow) / group, oh = (int)head * group + (tile * 16 + orow) % group;
+    const int64_t oat = (int64_t)(q.s0 + otok) * a.q_heads + oh;
+    float res[ND];
+#pragma unroll
+    for (int i = 0; i < ND; i++) {
+        res[i] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 4; w++) res[i] += lds[w * 16 * C::OS + orow * C::OS + c0 + i] * fw[w];
+    }
+    if (t.nsplit == 1) {
+#pragma unroll
+        for (int i = 0; i < ND; i += 4) {
+            const float f[4] = {res[i], res[i + 1], res[i + 2], res[i + 3]};
+            kv_write4<IN>(a.out, oat * DIM + c0 + i, f);
+        }
+        if (a.lse && c0 == 0) a.lse[oat] = lse2 * KV_LN2;
+    } else {
+        float *part = a.part + (oat * a.max_splits + split) * DIM + c0;
+#pragma unroll
+        for (int i = 0; i < ND; i++) part[i] = res[i];
+        if (c0 == 0) a.part_lse[oat * a.max_splits + split] = lse2;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Joining the pieces of a row
+// ---------------------------------------------------------------------------
+// One workgroup per new token and query head that has more than one piece:
+// out = sum_s 2^(lse_s - max) out_s / sum_s 2^(lse_s - max).
+template <int DIM, int IN>
+__global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs args, int ROWS) {
+    __shared__ float so[4][DIM], ssum[4];
+    const KvAttnLaunch &a = args.L;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int h = (int)blockIdx.y, tok = (int)blockIdx.x, req = (int)blockIdx.z;
+    const KvReq q = kv_request(a, req);
+    if (tok >= q.s1 - q.s0) return;
+    const int row = tok * a.group + h % a.group;
+    const KvTile t = kv_tile(q.s1 - q.s0, q.len, a.cap, a.group, row / ROWS, ROWS, a.window, a.chunk);
+    if (t.nsplit == 1) return;
+    const int64_t at = (int64_t)(q.s0 + tok) * a.q_heads + h;
+    const float *pl = a.part_lse + at * a.max_splits;
+    const float *po = a.part + at * a.max_splits * DIM;
+    float mm = -__builtin_inff();
+    for (int s = lane; s < t.nsplit; s += 64) mm = fmaxf(mm, pl[s]);
+    for (int d = 1; d < 64; d <<= 1) mm = kv_xor_max(mm, d);
+    const float safe = mm == -__builtin_inff() ? 0.0f : mm;
+    constexpr int PL = DIM / 64;
+    float o[PL], sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PL; i++) o[i] = 0.0f;
+    for (int s = wave; s < t.nsplit; s += 4) {
+        const float w = kv_exp2(pl[s] - safe);
+        sum += w;
+#pragma unroll
+        for (int i = 0; i < PL; i++) o[i] += w * po[(int64_t)s * DIM + lane + 64 * i];
+    }
+#pragma unroll
+    for (int i = 0; i < PL; i++) so[wave][lane + 64 * i] = o[i];
+    if (lane == 0) ssum[wave] = sum;
+    __syncthreads();
+    sum = ssum[0] + ssum[1] + ssum[2] + ssum[3];
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    if (tid < DIM / 4) {
+        float f[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int c = 4 * tid + i;
+            f[i] = (so[0][c] + so[1][c] + so[2][c] + so[3][c]) * inv;
+        }
+        kv_write4<IN>(a.out, at * DIM + 4 * tid, f);
+    }
+    if (tid == 0 && a.lse) a.lse[at] = (sum == 0.0f ? -__builtin_inff() : safe + __builtin_amdgcn_logf(sum)) * KV_LN2;
+}
+
+template <int CODE, int DIM, int IN>
+int launch_kv_attn_dim(const KvAttnLaunch &L, hipStream_t s) {
+    constexpr int TERMS = IN == 0 ? 2 : 1;
+    KvAttnArgs a{L};
+    const dim3 grid(L.c.heads * (uint32_t)L.tiles, (uint32_t)L.max_splits, (uint32_t)L.requests + 1);
+    constexpr uint32_t lds = KvDec<CODE, DIM, IN, TERMS>::LDS_FLOATS * 4;
+    hipLaunchKernelGGL((k_kv_attn_dec<CODE, DIM, IN, TERMS>), grid, dim3(256), lds, s, a);
+    if (hipGetLastError() != hipSuccess) return 9;  // NQ_ERR_HIP
+    if (L.max_splits > 1) {
+        const dim3 jgrid((uint32_t)L.max_new, (uint32_t)L.q_heads, (uint32_t)L.requests);
+        hipLaunchKernelGGL((k_kv_attn_join<DIM, IN>), jgrid, dim3(256), 0, s, a, 16);
+        if (hipGetLastError() != hipSuccess) return 9;  // NQ_ERR_HIP
+    }
+    return 0;
+}
+
+template <int CODE>
+int launch_kv_attn_code(const KvAttnLaunch &L, hipStream_t s) {
+    switch ((L.c.dim == 64 ? 0 : L.c.dim == 128 ? 3 : 6) + L.dtype) {
+    case 0: return launch_kv_attn_dim<CODE, 64, 0>(L, s);
+    case 1: return launch_kv_attn_dim<CODE, 64, 1>(L, s);
+    case 2: return launch_kv_attn_dim<CODE, 64, 2>(L, s);
+    case 3: return launch_kv_attn_dim<CODE, 128, 0>(L, s);
+    case 4: return launch_kv_attn_dim<CODE, 128, 1>(L, s);
+    case 5: return launch_kv_attn_dim<CODE, 128, 2>(L, s);
+    case 6: return launch_kv_attn_dim<CODE, 256, 0>(L, s);
+    case 7: return launch_kv_attn_dim<CODE, 256, 1>(L, s);
+    default: return launch_kv_attn_dim<CODE, 256, 2>(L, s);
+    }
+}
+
+}  // namespace nq

@@ -42,7 +42,8 @@ typedef enum {
     NQ_ERR_HIP = 9,               /* the HIP runtime reported an error at launch */
     NQ_ERR_BAD_DIVISORS = 10,     /* stacked nvfp4: divisors < 1, above 2^30, or not dividing the rows */
     NQ_ERR_MISALIGNED = 11,       /* a pointer lacks the alignment the call requires */
-    NQ_ERR_SCRATCH = 12           /* nq_gemm_q8_1_noalloc: the shape needs more than NQ_GEMM_SCRATCH_BYTES */
+    NQ_ERR_SCRATCH = 12           /* more workspace needed: than NQ_GEMM_SCRATCH_BYTES (nq_gemm_q8_1_noalloc),
+                                     or than was passed (nq_kv_attention) */
 } nq_status;
 
 /* Output types: the page's FLOAT, FLOAT16, BFLOAT16 and DOUBLE. */
@@ -348,6 +349,129 @@ int nq_gemm_q8_1(int32_t format, const void *weight, uint64_t nbytes, int64_t N,
 #define NQ_GEMM_SCRATCH_BYTES (32u << 20)
 int nq_gemm_q8_1_noalloc(int32_t format, const void *weight, uint64_t nbytes, int64_t N, int64_t K, const void *xq,
                          int64_t M, float *y, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * 8-bit key/value cache
+ * ---------------------------------------------------------------------------
+ * A pool of blocks of `block` tokens holds the keys and values of one layer
+ * in 8 bits.  Block b and head h have
+ *   k[((b*heads + h)*block + t)*dim + c]   the code of channel c of token t,
+ *   v[((b*heads + h)*dim + c)*block + t]   likewise, a channel's tokens
+ *                                          contiguous,
+ *   k_scale[b*heads + h], v_scale[...]     one binary32 scale each;
+ * a code stands for RN32(code * scale).  NQ_KV_Q8 codes are signed bytes
+ * (-127..127), NQ_KV_E4M3 codes E4M3FN words (at most 448).  dim is 64, 128
+ * or 256, block 16, 32, 64 or 128, 1 <= heads <= 65535 and 1 <= blocks <
+ * 2^31; k and v are 16-byte aligned, the scales 4-byte.  The caller owns
+ * every buffer.  What a pool holds where no token was stored does not matter.
+ *
+ * Every call checks the cache first: NULL cache or buffers (NQ_ERR_NULL_ARG),
+ * code (NQ_ERR_UNKNOWN_FORMAT), dim, block, heads and blocks (NQ_ERR_BAD_DIM),
+ * alignment (NQ_ERR_MISALIGNED).  Data types are NQ_F32, NQ_F16 and NQ_BF16
+ * (NQ_ERR_BAD_DTYPE), counts are at most 2^30 and strides below 2^60
+ * (NQ_ERR_OVERFLOW).  Lengths, tables and slots are device memory and are
+ * checked by the kernels: no value of theirs makes a kernel read or write
+ * outside the buffers that the arguments describe. */
+typedef enum { NQ_KV_Q8 = 0, NQ_KV_E4M3 = 1 } nq_kv_code;
+
+typedef struct {
+    int32_t code;  /* nq_kv_code */
+    int32_t heads, dim, block;
+    int64_t blocks;
+    void *k, *v;
+    float *k_scale, *v_scale;
+} nq_kv_cache;
+
+/* nq_kv_tables: the block tables, slots and token starts of a step.
+ * Request r holds lengths[r] tokens and gets added[r] >= 0 more, or ends
+ * (-1).  Its table row names held = ceil(length / block) blocks; the blocks
+ * it needs beyond come, in request order, from the head of a ring of free
+ * blocks (ring[ring_size]; free_state = {head, count}), and those of ended
+ * requests go, in request order, to its tail.  Written: the table and ring
+ * (in place), lengths_out[r] (0 for an ended request), token_start[r] (the
+ * sum of added tokens before r; requests + 1 of them), slots[i] = block id *
+ * block + offset for each of the step's tokens and -1 for i past them,
+ * free_state_out and status.
+ * status bits: 1 too few free blocks, 2 a negative length, an added count
+ * below -1 or a request longer than its table row, 4 more new tokens than
+ * `tokens`, 8 a head, count or returned blocks that the ring cannot hold.
+ * With any bit set the table and ring stay as they are, lengths_out and
+ * free_state_out repeat the input, token_start is 0 and every slot -1.
+ * requests < 2^20 and table_stride >= table_width (NQ_ERR_BAD_DIM); arrays
+ * are 4-byte aligned, slots 8-byte.  Outputs must not overlap inputs. */
+int nq_kv_tables(const int32_t *lengths, const int32_t *added, int64_t requests, int32_t *table,
+                 int64_t table_width, int64_t table_stride, int32_t *ring, int64_t ring_size,
+                 const int32_t *free_state, int32_t block, int64_t tokens, int32_t *lengths_out,
+                 int32_t *token_start, int64_t *slots, int32_t *free_state_out, uint32_t *status,
+                 hipStream_t stream);
+
+/* nq_kv_store: new keys and values into their blocks.  Element (i, h, c) of k
+ * is k[i*k_token_stride + h*k_head_stride + c], likewise v; tokens
+ * token_start[r] to token_start[r+1] belong to request r and are consecutive
+ * positions (slots as nq_kv_tables writes them: blocks fill from offset 0
+ * and belong to one request).  For a block, head and kind whose first new
+ * token has offset f:
+ *   s' = max(f > 0 ? s : 0, RN32(amax / qmax), 2^-126), amax over the finite
+ *        new values, qmax 127 or 448;
+ *   new codes are the nearest (ties to even, saturated) to RN32(x * RN32(1 /
+ *   s')), 0 for NaN; where s' > s, codes before f become the nearest to
+ *   RN32(code * RN32(s / s')).
+ * status is cleared on the stream, then ORed with 1 for a non-finite value
+ * and 2 for slots outside the pool or not consecutive: those tokens of that
+ * block are not stored.  Tokens past token_start[requests] are ignored. */
+int nq_kv_store(const nq_kv_cache *cache, const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                const void *v, int64_t v_token_stride, int64_t v_head_stride, int64_t tokens, int32_t in_dtype,
+                const int64_t *slots, const int32_t *token_start, int64_t requests, uint32_t *status,
+                hipStream_t stream);
+
+/* nq_kv_load: the values of n whole blocks, k_out and v_out [n, block, heads,
+ * dim], rounded once to out_dtype.  An id outside the pool gives zeros.
+ * Outputs are 16-byte aligned. */
+int nq_kv_load(const nq_kv_cache *cache, const int32_t *ids, int64_t n, int32_t out_dtype, void *k_out,
+               void *v_out, hipStream_t stream);
+
+/* nq_kv_attention: causal attention of each request's new tokens over its
+ * keys and values.  Request r has lengths[r] tokens, the new ones included:
+ * query i of it (token token_start[r] + i of q) has position lengths[r] -
+ * added + i, added = token_start[r+1] - token_start[r], and sees the keys up
+ * to that position, at most `window` of them (0: all).  Query head h uses
+ * key head h / (q_heads / heads).  With s_j = scale * q . k_j,
+ *   out = sum_j exp(s_j) v_j / sum_j exp(s_j),  lse = ln sum_j exp(s_j),
+ * and 0 and -inf for a row that sees no key.  A table entry outside the pool
+ * hides its keys.  out is [tokens, q_heads, dim] in q's type, 16-byte
+ * aligned; lse (binary32, [tokens, q_heads]) may be NULL.  Tokens past
+ * token_start[requests] get 0 and -inf.
+ * max_new and max_length bound the new tokens and the length of every
+ * request (rows past them are not computed; keys past them are not seen).
+ * They and the counts alone set the launch and the workspace, so a captured
+ * graph stays valid for other lengths within them.
+ * Products are binary16 with binary32 accumulation; queries in binary32 and
+ * their probabilities are taken in two binary16 terms (about 2^-23).  The
+ * order of sums is fixed by the shapes: repeated calls give identical bits.
+ * Checks beyond the cache's: 1 <= requests <= 65534, q_heads a multiple of
+ * heads, max_new, max_length, table_width >= 1, window >= 0, scale finite
+ * (NQ_ERR_BAD_DIM); q_heads <= 65535 and tokens * q_heads <= 2^30
+ * (NQ_ERR_OVERFLOW).  nq_kv_attention_workspace gives the bytes of device
+ * memory (16-byte aligned, not used by another call until this one's work is
+ * done) that the call needs, 0 for many; fewer are refused (NQ_ERR_SCRATCH). */
+typedef struct {
+    const void *q;
+    int64_t q_token_stride, q_head_stride; /* in elements; channels are contiguous */
+    int64_t tokens, q_heads, requests;
+    const int32_t *token_start; /* requests + 1 */
+    const int32_t *lengths;
+    const int32_t *table; /* [requests, table_width], rows table_stride apart */
+    int64_t table_width, table_stride;
+    int64_t window, max_new, max_length;
+    void *out;
+    float *lse;
+    int32_t dtype; /* of q and out */
+    float scale;
+} nq_kv_attention_args;
+
+int nq_kv_attention_workspace(const nq_kv_cache *cache, const nq_kv_attention_args *args, uint64_t *bytes);
+int nq_kv_attention(const nq_kv_cache *cache, const nq_kv_attention_args *args, void *workspace,
+                    uint64_t workspace_bytes, hipStream_t stream);
 
 /* Static description of a status code (the nq_status values above; other
  * values give "unknown status").  The pages define no status codes: these
