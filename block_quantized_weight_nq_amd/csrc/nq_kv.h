@@ -164,6 +164,7 @@ struct KvAttnLaunch {
     int32_t cap;         // keys a request can have: max_length, and what its table row can name
     int32_t max_new, window, chunk, max_splits, tiles;
     int32_t code, dtype;
+    bool q_vec;          // rows of q start on 16-byte boundaries
     float scale;
 };
 

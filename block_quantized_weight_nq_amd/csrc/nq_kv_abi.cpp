@@ -236,6 +236,8 @@ NQ_API int nq_kv_attention(const nq_kv_cache *cache, const nq_kv_attention_args 
     if (need > 0 && (!workspace || workspace_bytes < need)) return NQ_ERR_SCRATCH;
     if (args->tokens == 0) return NQ_OK;
     L.q = args->q;
+    L.q_vec = (uintptr_t)args->q % 16 == 0 && args->q_token_stride * (int64_t)esz % 16 == 0 &&
+              args->q_head_stride * (int64_t)esz % 16 == 0;
     L.starts = args->token_start;
     L.lengths = args->lengths;
     L.table = args->table;

@@ -142,10 +142,9 @@ __global__ __launch_bounds__(256, 2) void k_kv_attn_dec(KvAttnArgs args) {
     const int k1 = t.kend - k0 > a.chunk ? k0 + a.chunk : t.kend;
 
     // this lane's query row (as the column of the score tiles)
-    const int row = tile * 16 + r, tok = row / group;
-    const bool has = row < t.rows;
+    const int row = tile * 16 + r < t.rows ? tile * 16 + r : t.rows - 1, tok = row / group;
     const int p = t.base + tok;
-    const int hi = has ? (p + 1 < t.live ? p + 1 : t.live) : 0;
+    const int hi = p + 1 < t.live ? p + 1 : t.live;
     const int lo = a.window > 0 && p - a.window + 1 > 0 ? p - a.window + 1 : 0;
     const int all_hi = t.base + t.first + 1 < t.live ? t.base + t.first + 1 : t.live;
     const int all_lo = a.window > 0 ? t.base + t.last - a.window + 1 : 0;
@@ -154,14 +153,17 @@ __global__ __launch_bounds__(256, 2) void k_kv_attn_dec(KvAttnArgs args) {
     {
         float f[NA][16];
         float amax = 0.0f;
-        const int64_t at = (int64_t)(q.s0 + (has ? tok : 0)) * a.q_ts + ((int64_t)head * group + (has ? row % group : 0)) * a.q_hs;
+        const int64_t at = (int64_t)(q.s0 + tok) * a.q_ts + ((int64_t)head * group + row % group) * a.q_hs;
+        // the tile's last row stands in for the rows past it: nothing of theirs is written
 #pragma unroll
-        for (int i = 0; i < NA; i++)
+        for (int i = 0; i < NA; i++) {
+            if (a.q_vec)
+                kv_read16<IN, true>(a.q, at + 64 * i + 16 * g, f[i]);
+            else
+                kv_read16<IN, false>(a.q, at + 64 * i + 16 * g, f[i]);
 #pragma unroll
-            for (int k = 0; k < 16; k++) {
-                f[i][k] = has ? kv_read<IN>(a.q, at + 64 * i + 16 * g + k) : 0.0f;
-                amax = fmaxf(amax, fabsf(f[i][k]));
-            }
+            for (int k = 0; k < 16; k++) amax = fmaxf(amax, fabsf(f[i][k]));
+        }
         amax = kv_xor_max(kv_xor_max(amax, 16), 32);
         const float up = kv_row_scale(amax);
         qscale = a.scale * KV_LOG2E / up;
@@ -288,61 +290,53 @@ __global__ __launch_bounds__(256, 2) void k_kv_attn_dec(KvAttnArgs args) {
                 x[n][i] = e * pv;
                 least = fminf(least, fabsf(x[n][i]));
             }
+        // O = O * fo + values * weights * ft: all weights at once, or level by level where some are small
+        float fo = beta, ft = 1.0f;
+        for (bool slow = __ballot(least < KvLevel<TERMS>::LEAST) != 0;;) {
+            float rest[NT][4];
+            bool more = false;
+            if (slow) {
 #pragma unroll
-        for (int d = 0; d < ND; d++) O[d] *= beta;
-        // O += values * weights, or for the small weights values * (weights * UP^k) / UP^k
-        auto add = [&](const float (&w)[NT][4], float back) {
+                for (int n = 0; n < NT; n++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        rest[n][i] = fabsf(x[n][i]) < KvLevel<TERMS>::LEAST ? x[n][i] : 0.0f;
+                        more |= rest[n][i] != 0.0f;
+                        x[n][i] -= rest[n][i];
+                    }
+            }
             kv_h8 P[TERMS][NB];
 #pragma unroll
             for (int n = 0; n < NT; n++)
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    const _Float16 h = (_Float16)w[n][i];
+                    const _Float16 h = (_Float16)x[n][i];
                     P[0][n >> 1][4 * (n & 1) + i] = h;
-                    if constexpr (TERMS == 2) P[1][n >> 1][4 * (n & 1) + i] = (_Float16)(w[n][i] - (float)h);
+                    if constexpr (TERMS == 2) P[1][n >> 1][4 * (n & 1) + i] = (_Float16)(x[n][i] - (float)h);
                 }
 #pragma unroll
             for (int d = 0; d < ND; d++) {
-                kv_f4 acc = back == 1.0f ? O[d] : kv_f4{0, 0, 0, 0};
+                kv_f4 acc = {0, 0, 0, 0};
 #pragma unroll
                 for (int b = 0; b < NB; b++) {
+                    // keeps the conversion in this loop: hoisted, the values would hold twice the registers
+                    asm volatile("" : "+v"(V[d][b]));
                     const kv_h8 vv = kv_codes8_f16<CODE>(V[d][b]);
 #pragma unroll
                     for (int e = 0; e < TERMS; e++)
                         acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, P[e][b], acc, 0, 0, 0);
                 }
-                if (back == 1.0f)
-                    O[d] = acc;
-                else
-                    O[d] += acc * back;
+#pragma unroll
+                for (int i = 0; i < 4; i++) O[d][i] = __builtin_fmaf(O[d][i], fo, acc[i] * ft);
             }
-        };
-        if (__ballot(least < KvLevel<TERMS>::LEAST)) {
-            float w[NT][4], back = 1.0f;
+            if (!slow || !__ballot(more)) break;  // weights are multiples of 2^-149: at most 10 rounds
+            fo = 1.0f;
+            ft *= 1.0f / KvLevel<TERMS>::UP;
 #pragma unroll
             for (int n = 0; n < NT; n++)
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    w[n][i] = fabsf(x[n][i]) < KvLevel<TERMS>::LEAST ? x[n][i] : 0.0f;
-                    x[n][i] -= w[n][i];
-                }
-            for (;;) {
-                float most = 0.0f, now[NT][4];
-#pragma unroll
-                for (int n = 0; n < NT; n++)
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        w[n][i] *= KvLevel<TERMS>::UP;
-                        most = fmaxf(most, fabsf(w[n][i]));
-                        now[n][i] = fabsf(w[n][i]) < KvLevel<TERMS>::LEAST ? 0.0f : w[n][i];
-                        w[n][i] -= now[n][i];
-                    }
-                back *= 1.0f / KvLevel<TERMS>::UP;
-                if (!__ballot(most > 0.0f)) break;  // most < 2^-149 * UP^k: at most 9 rounds
-                add(now, back);
-            }
+                for (int i = 0; i < 4; i++) x[n][i] = rest[n][i] * KvLevel<TERMS>::UP;
         }
-        add(x, 1.0f);
     }
     l = kv_xor_add(kv_xor_add(l, 16), 32);
 

@@ -101,6 +101,32 @@ __device__ __forceinline__ void kv_read4(const void *x, int64_t i, float (&f)[4]
     }
 }
 
+// Sixteen consecutive elements; VEC: the address is a multiple of 16 bytes.
+template <int IN, bool VEC>
+__device__ __forceinline__ void kv_read16(const void *x, int64_t i, float (&f)[16]) {
+    if constexpr (!VEC) {
+#pragma unroll
+        for (int j = 0; j < 16; j++) f[j] = kv_read<IN>(x, i + j);
+    } else if constexpr (IN == 0) {
+#pragma unroll
+        for (int v = 0; v < 4; v++) {
+            const kv_f4 w = *(const kv_f4 *)((const float *)x + i + 4 * v);
+#pragma unroll
+            for (int j = 0; j < 4; j++) f[4 * v + j] = w[j];
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < 2; v++) {
+            const kv_u4 w = *(const kv_u4 *)((const uint16_t *)x + i + 8 * v);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const uint32_t h = (w[j >> 1] >> (16 * (j & 1))) & 0xFFFFu;
+                f[8 * v + j] = IN == 1 ? f16(h) : bits_f32(h << 16);
+            }
+        }
+    }
+}
+
 // Four consecutive elements of type OT, rounded to nearest even; the address is a multiple of their bytes.
 template <int OT>
 __device__ __forceinline__ void kv_write4(void *y, int64_t i, const float (&f)[4]) {
