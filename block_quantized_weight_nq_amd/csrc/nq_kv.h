@@ -162,19 +162,19 @@ struct KvAttnLaunch {
     float *part_lse;     // their base-2 logarithms of the sums, [tokens, q_heads, max_splits]
     int32_t tokens, requests, q_heads, group;
     int32_t cap;         // keys a request can have: max_length, and what its table row can name
-    int32_t max_new, window, chunk, max_splits, tiles;
+    int32_t max_new, window;
     int32_t code, dtype;
     bool q_vec;          // rows of q start on 16-byte boundaries
     float scale;
+    // the plan
+    int32_t few;         // requests of at most this many rows go to the few-rows kernel
+    int32_t waves;       // of a many-rows workgroup, 32 rows each; 0 without such a launch
+    int32_t tiles, tiles_few;    // tiles of a request and key head, at most
+    int32_t chunk, chunk_few;    // keys of a piece
+    int32_t splits, splits_few;  // pieces of a tile, at most
+    int32_t max_splits;          // the larger of them: the stride of the pieces
 };
-
-struct KvAttnPlan {
-    int rows;            // rows of a tile
-    int tiles;           // tiles of a request and key head
-    int chunk;           // keys of a piece
-    int max_splits;      // most pieces of a tile
-};
-KvAttnPlan kv_attn_plan(const KvAttnLaunch &L, uint32_t cus);
+void kv_attn_plan(KvAttnLaunch &L, uint32_t cus);
 int launch_kv_attn(const KvAttnLaunch &L, hipStream_t s);
 
 }  // namespace nq

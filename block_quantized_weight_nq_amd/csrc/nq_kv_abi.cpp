@@ -14,32 +14,52 @@ int launch_kv_attn_e4m3(const KvAttnLaunch &L, hipStream_t s);
 // wait for the stream), so every request gets the workgroups of the longest
 // one and those past its own end return at once.
 //
-// A piece is `chunk` keys.  Several pieces a row let few rows fill the card;
-// each costs a partial output.  512 keys keep the slowest workgroup short
-// where lengths differ, and calls with enough tiles take one piece.
-KvAttnPlan kv_attn_plan(const KvAttnLaunch &L, uint32_t cus) {
-    KvAttnPlan p;
-    p.rows = 16;
+// Requests of at most `few` rows go to the kernel for few rows, the others to
+// the one for many.  A piece is `chunk` keys: several pieces a row let few
+// rows fill the card, each costs a partial output.  For few rows 512 keys keep
+// the slowest workgroup short where lengths differ; many rows are cut only
+// where the tiles leave compute units idle.
+void kv_attn_plan(KvAttnLaunch &L, uint32_t cus) {
     const int64_t rows = (int64_t)L.max_new * L.group;
-    p.tiles = (int)((rows + p.rows - 1) / p.rows);
-    int64_t span = L.cap;
-    if (L.window > 0) {
-        const int64_t seen = (int64_t)L.window + p.rows / L.group + 2 + 63;
-        if (seen < span) span = seen;
+    auto span_of = [&](int64_t tile_rows) {
+        const int64_t seen = (int64_t)L.window + tile_rows / L.group + 2 + 63;
+        const int64_t span = L.window > 0 && seen < L.cap ? seen : L.cap;
+        return span < 1 ? 1 : span;
+    };
+    auto cut = [](int64_t span, int64_t pieces, int64_t least, int32_t *chunk, int32_t *splits) {
+        if (pieces > 65535) pieces = 65535;
+        int64_t c = ((span + pieces - 1) / pieces + 255) / 256 * 256;
+        if (c < least) c = least;
+        *chunk = (int32_t)c;
+        *splits = (int32_t)((span + c - 1) / c);
+    };
+    L.few = 32;
+    L.waves = 0;
+    L.tiles = L.splits = 0;
+    L.chunk = 256;
+    if (L.dtype == 0) L.few = 1 << 30;  // two terms leave no registers for 32 rows a wave
+    if (rows > L.few) {
+        L.waves = L.c.dim == 128 && rows > 128 ? 8 : 4;
+        const int64_t tr = 32 * L.waves;
+        const int64_t tiles = (rows + tr - 1) / tr;
+        L.tiles = (int32_t)tiles;
+        // tiles that have rows, at most
+        int64_t busy = (int64_t)L.tokens * L.group / tr + L.requests;
+        if (busy > L.requests * tiles) busy = L.requests * tiles;
+        busy *= L.c.heads;
+        const int64_t want = L.waves == 8 ? cus : 2 * cus;
+        cut(span_of(tr), busy >= want ? 1 : (want + busy - 1) / busy, 512, &L.chunk, &L.splits);
     }
-    if (span < 1) span = 1;
-    // tiles that have rows, at most
-    int64_t busy = (int64_t)L.tokens * L.group / p.rows + L.requests;
-    if (busy > (int64_t)L.requests * p.tiles) busy = (int64_t)L.requests * p.tiles;
+    const int64_t few_rows = rows < L.few ? rows : L.few;
+    L.tiles_few = (int32_t)((few_rows + 15) / 16);
+    const int64_t span = span_of(16);
+    int64_t busy = (int64_t)L.tokens * L.group / 16 + L.requests;
+    if (busy > (int64_t)L.requests * L.tiles_few) busy = (int64_t)L.requests * L.tiles_few;
     busy *= L.c.heads;
-    const int64_t want = 8ll * cus;
-    int64_t pieces = p.tiles > 4 ? (busy >= want ? 1 : (want + busy - 1) / (busy > 0 ? busy : 1)) : (span + 511) / 512;
-    int64_t chunk = (span + pieces - 1) / pieces;
-    chunk = (chunk + 255) / 256 * 256;
-    if ((span + chunk - 1) / chunk > 65535) chunk = (span / 65535 + 256) / 256 * 256;
-    p.chunk = (int)chunk;
-    p.max_splits = (int)((span + chunk - 1) / chunk);
-    return p;
+    // many tiles (prompts in binary32) fill the card by themselves
+    const int64_t pieces = L.tiles_few > 4 ? (busy >= 8ll * cus ? 1 : (8ll * cus + busy - 1) / busy) : (span + 511) / 512;
+    cut(span, pieces, 256, &L.chunk_few, &L.splits_few);
+    L.max_splits = L.splits > L.splits_few ? L.splits : L.splits_few;
 }
 }  // namespace nq
 
@@ -103,11 +123,8 @@ int check_attention(const nq_kv_cache *cache, const nq_kv_attention_args *x, nq:
     L->code = cache->code;
     L->dtype = x->dtype;
     L->scale = x->scale;
-    const nq::KvAttnPlan p = nq::kv_attn_plan(*L, nq::device_compute_units());
-    if ((int64_t)p.tiles * cache->heads >= (1ll << 31)) return NQ_ERR_OVERFLOW;
-    L->tiles = p.tiles;
-    L->chunk = p.chunk;
-    L->max_splits = p.max_splits;
+    if (((int64_t)L->max_new * L->group / 16 + 1) * cache->heads >= (1ll << 31)) return NQ_ERR_OVERFLOW;
+    nq::kv_attn_plan(*L, nq::device_compute_units());
     return NQ_OK;
 }
 

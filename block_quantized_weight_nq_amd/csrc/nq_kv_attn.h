@@ -123,7 +123,7 @@ __global__ __launch_bounds__(256, 2) void k_kv_attn_dec(KvAttnArgs args) {
         if (split != 0) return;
         int s = a.starts[a.requests];
         s = s < 0 ? 0 : s;
-        for (int64_t tok = (int64_t)s + tile; tok < a.tokens; tok += a.tiles)
+        for (int64_t tok = (int64_t)s + tile; tok < a.tokens; tok += a.tiles_few)
             for (int i = tid; i < group * DIM; i += 256) {
                 const int64_t row = tok * a.q_heads + (int64_t)head * group + i / DIM;
                 if constexpr (IN == 0)
@@ -135,11 +135,12 @@ __global__ __launch_bounds__(256, 2) void k_kv_attn_dec(KvAttnArgs args) {
         return;
     }
     const KvReq q = kv_request(a, req);
-    if (tile * 16 >= (q.s1 - q.s0) * group) return;
-    const KvTile t = kv_tile(q.s1 - q.s0, q.len, a.cap, group, tile, 16, a.window, a.chunk);
+    const int rows = (q.s1 - q.s0) * group;
+    if (rows > a.few || tile * 16 >= rows) return;
+    const KvTile t = kv_tile(q.s1 - q.s0, q.len, a.cap, group, tile, 16, a.window, a.chunk_few);
     if (split >= t.nsplit) return;
-    const int k0 = t.kbeg + split * a.chunk;
-    const int k1 = t.kend - k0 > a.chunk ? k0 + a.chunk : t.kend;
+    const int k0 = t.kbeg + split * a.chunk_few;
+    const int k1 = t.kend - k0 > a.chunk_few ? k0 + a.chunk_few : t.kend;
 
     // this lane's query row (as the column of the score tiles)
     const int row = tile * 16 + r < t.rows ? tile * 16 + r : t.rows - 1, tok = row / group;
@@ -397,7 +398,7 @@ __global__ __launch_bounds__(256, 2) void k_kv_attn_dec(KvAttnArgs args) {
 // One workgroup per new token and query head that has more than one piece:
 // out = sum_s 2^(lse_s - max) out_s / sum_s 2^(lse_s - max).
 template <int DIM, int IN>
-__global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs args, int ROWS) {
+__global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs args) {
     __shared__ float so[4][DIM], ssum[4];
     const KvAttnLaunch &a = args.L;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -405,7 +406,9 @@ __global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs args, int ROWS)
     const KvReq q = kv_request(a, req);
     if (tok >= q.s1 - q.s0) return;
     const int row = tok * a.group + h % a.group;
-    const KvTile t = kv_tile(q.s1 - q.s0, q.len, a.cap, a.group, row / ROWS, ROWS, a.window, a.chunk);
+    const bool few = (q.s1 - q.s0) * a.group <= a.few;
+    const int ROWS = few ? 16 : 32 * a.waves;
+    const KvTile t = kv_tile(q.s1 - q.s0, q.len, a.cap, a.group, row / ROWS, ROWS, a.window, few ? a.chunk_few : a.chunk);
     if (t.nsplit == 1) return;
     const int64_t at = (int64_t)(q.s0 + tok) * a.q_heads + h;
     const float *pl = a.part_lse + at * a.max_splits;
@@ -440,37 +443,6 @@ __global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs args, int ROWS)
         kv_write4<IN>(a.out, at * DIM + 4 * tid, f);
     }
     if (tid == 0 && a.lse) a.lse[at] = (sum == 0.0f ? -__builtin_inff() : safe + __builtin_amdgcn_logf(sum)) * KV_LN2;
-}
-
-template <int CODE, int DIM, int IN>
-int launch_kv_attn_dim(const KvAttnLaunch &L, hipStream_t s) {
-    constexpr int TERMS = IN == 0 ? 2 : 1;
-    KvAttnArgs a{L};
-    const dim3 grid(L.c.heads * (uint32_t)L.tiles, (uint32_t)L.max_splits, (uint32_t)L.requests + 1);
-    constexpr uint32_t lds = KvDec<CODE, DIM, IN, TERMS>::LDS_FLOATS * 4;
-    hipLaunchKernelGGL((k_kv_attn_dec<CODE, DIM, IN, TERMS>), grid, dim3(256), lds, s, a);
-    if (hipGetLastError() != hipSuccess) return 9;  // NQ_ERR_HIP
-    if (L.max_splits > 1) {
-        const dim3 jgrid((uint32_t)L.max_new, (uint32_t)L.q_heads, (uint32_t)L.requests);
-        hipLaunchKernelGGL((k_kv_attn_join<DIM, IN>), jgrid, dim3(256), 0, s, a, 16);
-        if (hipGetLastError() != hipSuccess) return 9;  // NQ_ERR_HIP
-    }
-    return 0;
-}
-
-template <int CODE>
-int launch_kv_attn_code(const KvAttnLaunch &L, hipStream_t s) {
-    switch ((L.c.dim == 64 ? 0 : L.c.dim == 128 ? 3 : 6) + L.dtype) {
-    case 0: return launch_kv_attn_dim<CODE, 64, 0>(L, s);
-    case 1: return launch_kv_attn_dim<CODE, 64, 1>(L, s);
-    case 2: return launch_kv_attn_dim<CODE, 64, 2>(L, s);
-    case 3: return launch_kv_attn_dim<CODE, 128, 0>(L, s);
-    case 4: return launch_kv_attn_dim<CODE, 128, 1>(L, s);
-    case 5: return launch_kv_attn_dim<CODE, 128, 2>(L, s);
-    case 6: return launch_kv_attn_dim<CODE, 256, 0>(L, s);
-    case 7: return launch_kv_attn_dim<CODE, 256, 1>(L, s);
-    default: return launch_kv_attn_dim<CODE, 256, 2>(L, s);
-    }
 }
 
 }  // namespace nq
