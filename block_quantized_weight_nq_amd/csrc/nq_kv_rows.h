@@ -296,8 +296,11 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void k_kv_attn_rows(KvA
                     const float x = fabsf(S[g >> 1][8 * (g & 1) + i]);
                     most = fmaxf(most, x < KvLevel<1>::LEAST ? x : 0.0f);
                 }
-            const uint32_t e = __builtin_bit_cast(uint32_t, kv_max_halves(most)) >> 23;  // most < 2^-14: e < 113
-            up = bits_f32((e > 70u ? 127u + 13u + 127u - e : 197u) << 23);  // at most 2^70: |O| < 2^53 stays finite
+            // |O| <= 2^14 * 448 * 2 max(l): up stops where their product would pass 2^127
+            const int e = (int)(__builtin_bit_cast(uint32_t, kv_max_halves(most)) >> 23) - 127;
+            const int el = (int)(__builtin_bit_cast(uint32_t, kv_max_halves(l)) >> 23) - 127;
+            const int room = el > 0 ? 100 - el : 100;
+            up = bits_f32((uint32_t)(127 + (13 - e < room ? 13 - e : room)) << 23);
 #pragma unroll
             for (int g = 0; g < 4; g++)
 #pragma unroll
