@@ -8,9 +8,9 @@ and streams.  There is no fallback: if libnq.so is missing, every call raises.
     y = nq.dequantize_packed("gguf:q4_k", payload_u8_cuda, [4096, 4096], torch.bfloat16)
 """
 import collections
-import contextlib
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libnq.so")
@@ -130,10 +130,9 @@ def _lib():
                                   c.c_void_p]
         L.nq_kv_load.argtypes = [c.POINTER(KvCacheDesc), c.c_void_p, c.c_int64, c.c_int32, c.c_void_p, c.c_void_p,
                                  c.c_void_p]
-        L.nq_kv_attention_workspace.argtypes = [c.POINTER(KvCacheDesc), c.POINTER(KvAttentionArgs),
-                                                c.POINTER(c.c_uint64)]
-        L.nq_kv_attention.argtypes = [c.POINTER(KvCacheDesc), c.POINTER(KvAttentionArgs), c.c_void_p, c.c_uint64,
-                                      c.c_void_p]
+        # (the arguments: a KvAttentionArgs by reference, or its bytes)
+        L.nq_kv_attention_workspace.argtypes = [c.POINTER(KvCacheDesc), c.c_void_p, c.POINTER(c.c_uint64)]
+        L.nq_kv_attention.argtypes = [c.POINTER(KvCacheDesc), c.c_void_p, c.c_void_p, c.c_uint64, c.c_void_p]
         L.nq_status_string.argtypes = [c.c_int]
         L.nq_status_string.restype = c.c_char_p
         _LIB = L
@@ -584,7 +583,8 @@ class KvCache:
                 raise ValueError("cache tensors must be contiguous CUDA tensors of one device")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.blocks, self.heads, self.block, self.dim, self.code = blocks, heads, block, dim, codes[k.dtype]
-        self.device = k.device
+        self.device, self.index = k.device, k.get_device()
+        self._workspaces = {}
         self._desc = KvCacheDesc(KV_CODES[self.code], heads, dim, block, blocks, k.data_ptr(), v.data_ptr(),
                                  k_scale.data_ptr(), v_scale.data_ptr())
         self._ref = ctypes.byref(self._desc)
@@ -601,25 +601,37 @@ class KvCache:
 
 KvStep = collections.namedtuple("KvStep", "lengths token_start slots free_state status")
 
-
-def _on(stream, device):
-    """(stream, context to allocate in): new tensors belong to the stream that the work runs on."""
-    import torch
-    if stream is None:
-        return torch.cuda.current_stream(device), contextlib.nullcontext()
-    return stream, torch.cuda.stream(stream)
+# A serving step makes these calls once a layer, at a few microseconds each: they take the raw stream, compare device
+# indices, and pass nq_kv_attention_args as packed bytes (the fields of KvAttentionArgs, in its layout).
+_ATTENTION_ARGS = struct.Struct("@PqqqqqPPPqqqqqPPif")
+assert _ATTENTION_ARGS.size == ctypes.sizeof(KvAttentionArgs)
 
 
-def _device_ints(device, dtype, **tensors):
-    for name, t in tensors.items():
-        if t.dtype != dtype or not t.is_cuda or t.device != device or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor on {device}")
+_TYPES = {}  # torch dtypes and the raw-stream query, filled by the first call
 
 
-def _block_table(table, requests, device, dtype):
-    if table.dim() != 2 or table.shape[0] != requests or table.dtype != dtype or table.device != device or \
+def _types():
+    if not _TYPES:
+        import torch
+        _TYPES.update(i32=torch.int32, i64=torch.int64, f32=torch.float32, u8=torch.uint8, on=torch.cuda.stream,
+                      handle=torch._C._cuda_getCurrentRawStream, codes={torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+    return _TYPES
+
+
+def _kv_dtype(dtype):
+    code = _TYPES["codes"].get(dtype)
+    return _dtype_code(dtype) if code is None else code
+
+
+def _device_ints(index, dtype, name, t):
+    if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on CUDA device {index}")
+
+
+def _block_table(table, requests, index, dtype):
+    if table.dtype is not dtype or table.get_device() != index or table.dim() != 2 or table.shape[0] != requests or \
             table.shape[1] < 1 or table.stride(1) != 1:
-        raise ValueError(f"table must be {dtype} [{requests}, width] on {device}, each row contiguous")
+        raise ValueError(f"table must be {dtype} [{requests}, width] on CUDA device {index}, each row contiguous")
 
 
 def kv_tables(lengths, added, table, ring, free_state, block, tokens, stream=None):
@@ -631,29 +643,38 @@ def kv_tables(lengths, added, table, ring, free_state, block, tokens, stream=Non
     [requests + 1], slots int64 [tokens], free_state, status int32 [1]); nothing changes if status is not 0 (1: too
     few free blocks, 2: a bad length, 4: more than `tokens` new tokens, 8: the ring cannot hold the blocks).
     """
-    import torch
-    device = lengths.device
+    t = _types()
+    if stream is not None:  # outputs belong to the stream that the work runs on
+        with t["on"](stream):
+            return kv_tables(lengths, added, table, ring, free_state, block, tokens)
+    i32 = t["i32"]
+    if not lengths.is_cuda:
+        raise ValueError("lengths must be a CUDA tensor")
+    index = lengths.get_device()
     n = lengths.numel()
-    _device_ints(device, torch.int32, lengths=lengths, added=added, ring=ring, free_state=free_state)
-    _block_table(table, n, device, torch.int32)
+    _device_ints(index, i32, "lengths", lengths)
+    _device_ints(index, i32, "added", added)
+    _device_ints(index, i32, "ring", ring)
+    _device_ints(index, i32, "free_state", free_state)
+    _block_table(table, n, index, i32)
     if added.numel() != n or free_state.numel() != 2:
         raise ValueError("added must have one entry for each request and free_state two")
-    stream, ctx = _on(stream, device)
-    with ctx:
-        words = torch.empty(2 * n + 4, dtype=torch.int32, device=device)
-        slots = torch.empty(int(tokens), dtype=torch.int64, device=device)
+    words = lengths.new_empty(2 * n + 4)
+    slots = lengths.new_empty(max(0, tokens), dtype=t["i64"])
     p = words.data_ptr()
     st = _lib().nq_kv_tables(lengths.data_ptr(), added.data_ptr(), n, table.data_ptr(), table.shape[1],
                              table.stride(0), ring.data_ptr(), ring.numel(), free_state.data_ptr(), block, tokens, p,
-                             p + 4 * n, slots.data_ptr(), p + 8 * n + 4, p + 8 * n + 12, stream.cuda_stream)
+                             p + 4 * n, slots.data_ptr(), p + 8 * n + 4, p + 8 * n + 12, t["handle"](index))
     if st != NQ_OK:
         raise NqError(st, f"{n} requests, table {list(table.shape)}, block {block}, {tokens} tokens")
-    return KvStep(words[:n], words[n:2 * n + 1], slots, words[2 * n + 1:2 * n + 3], words[2 * n + 3:])
+    new_lengths, token_start, state, status = words.split_with_sizes((n, n + 1, 2, 1))
+    return KvStep(new_lengths, token_start, slots, state, status)
 
 
 def _heads_of(name, x, cache, heads=None):
-    if x.dim() != 3 or x.shape[2] != cache.dim or (heads and x.shape[1] != heads) or x.device != cache.device or \
-            (x.numel() and x.stride(2) != 1):
+    shape = x.shape
+    if len(shape) != 3 or shape[2] != cache.dim or (heads and shape[1] != heads) or x.get_device() != cache.index or \
+            (x.stride(2) != 1 and x.numel()):
         raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {cache.dim}] on {cache.device}, "
                          "channels contiguous")
 
@@ -663,22 +684,24 @@ def kv_store(cache, k, v, slots, token_start, stream=None):
     into their blocks.  slots: int64 [tokens], token_start: int32 [requests + 1] (as kv_tables returns them).
     Returns status int32 [1]: 1 a value is not finite (NaN is stored as 0, infinities saturate), 2 a slot outside
     the pool or out of order (that block's tokens are not stored)."""
-    import torch
+    t = _types()
+    if stream is not None:
+        with t["on"](stream):
+            return kv_store(cache, k, v, slots, token_start)
     _heads_of("k", k, cache, cache.heads)
     _heads_of("v", v, cache, cache.heads)
-    if v.dtype != k.dtype or v.shape[0] != k.shape[0]:
-        raise ValueError("k and v must have one type and one number of tokens")
-    _device_ints(cache.device, torch.int64, slots=slots)
-    _device_ints(cache.device, torch.int32, token_start=token_start)
     n = k.shape[0]
+    if v.dtype is not k.dtype or v.shape[0] != n:
+        raise ValueError("k and v must have one type and one number of tokens")
+    _device_ints(cache.index, t["i64"], "slots", slots)
+    _device_ints(cache.index, t["i32"], "token_start", token_start)
     if slots.numel() < n or token_start.numel() < 2:
         raise ValueError("slots needs one entry for each token and token_start one for each request and one more")
-    stream, ctx = _on(stream, cache.device)
-    with ctx:
-        status = torch.empty(1, dtype=torch.int32, device=cache.device)
-    st = _lib().nq_kv_store(cache._ref, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
-                            v.stride(1), n, _dtype_code(k.dtype), slots.data_ptr(), token_start.data_ptr(),
-                            token_start.numel() - 1, status.data_ptr(), stream.cuda_stream)
+    status = token_start.new_empty(1)
+    ks, vs = k.stride(), v.stride()
+    st = _lib().nq_kv_store(cache._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], n,
+                            _kv_dtype(k.dtype), slots.data_ptr(), token_start.data_ptr(), token_start.numel() - 1,
+                            status.data_ptr(), t["handle"](cache.index))
     if st != NQ_OK:
         raise NqError(st, f"k {list(k.shape)} {k.dtype}")
     return status
@@ -686,19 +709,21 @@ def kv_store(cache, k, v, slots, token_start, stream=None):
 
 def kv_load(cache, ids, out_dtype=None, stream=None):
     """Keys and values of whole blocks (ids: int32 [n]), each [n, block, heads, dim] in out_dtype (default float32)."""
-    import torch
-    _device_ints(cache.device, torch.int32, ids=ids)
-    out_dtype = out_dtype or torch.float32
-    code = _dtype_code(out_dtype)
-    shape = (ids.numel(), cache.block, cache.heads, cache.dim)
-    stream, ctx = _on(stream, cache.device)
-    with ctx:
-        k = torch.empty(shape, dtype=out_dtype, device=cache.device)
-        v = torch.empty(shape, dtype=out_dtype, device=cache.device)
-    st = _lib().nq_kv_load(cache._ref, ids.data_ptr(), ids.numel(), code, k.data_ptr(), v.data_ptr(),
-                           stream.cuda_stream)
+    t = _types()
+    if stream is not None:
+        with t["on"](stream):
+            return kv_load(cache, ids, out_dtype)
+    _device_ints(cache.index, t["i32"], "ids", ids)
+    out_dtype = out_dtype or t["f32"]
+    code = _kv_dtype(out_dtype)
+    n = ids.numel()
+    shape = (n, cache.block, cache.heads, cache.dim)
+    k = ids.new_empty(shape, dtype=out_dtype)
+    v = ids.new_empty(shape, dtype=out_dtype)
+    st = _lib().nq_kv_load(cache._ref, ids.data_ptr(), n, code, k.data_ptr(), v.data_ptr(),
+                           t["handle"](cache.index))
     if st != NQ_OK:
-        raise NqError(st, f"{ids.numel()} blocks as {out_dtype}")
+        raise NqError(st, f"{n} blocks as {out_dtype}")
     return k, v
 
 
@@ -713,35 +738,46 @@ def kv_attention(cache, q, token_start, lengths, table, scale=None, window=0, ma
     bounds save launches of idle workgroups.  Returns out in q's type and shape, and with return_lse also the
     natural logarithms of the sums, float32 [tokens, q_heads].
     """
-    import torch
+    t = _types()
+    if stream is not None:
+        with t["on"](stream):
+            return kv_attention(cache, q, token_start, lengths, table, scale, window, max_new, max_length, return_lse)
     _heads_of("q", q, cache)
     n, q_heads, dim = q.shape
-    requests = lengths.numel()
-    _device_ints(cache.device, torch.int32, token_start=token_start, lengths=lengths)
-    _block_table(table, requests, cache.device, torch.int32)
+    requests, width, index, i32 = lengths.numel(), table.shape[-1], cache.index, t["i32"]
+    _device_ints(index, i32, "token_start", token_start)
+    _device_ints(index, i32, "lengths", lengths)
+    _block_table(table, requests, index, i32)
     if token_start.numel() != requests + 1:
         raise ValueError("token_start must have one entry more than lengths")
     if max_new is None:
         max_new = max(1, n)
     if max_length is None:
-        max_length = table.shape[1] * cache.block
-    code = _dtype_code(q.dtype)
-    stream, ctx = _on(stream, cache.device)
-    with ctx:
-        out = torch.empty((n, q_heads, dim), dtype=q.dtype, device=cache.device)
-        lse = torch.empty((n, q_heads), dtype=torch.float32, device=cache.device) if return_lse else None
-        args = KvAttentionArgs(q.data_ptr(), q.stride(0), q.stride(1), n, q_heads, requests, token_start.data_ptr(),
-                               lengths.data_ptr(), table.data_ptr(), table.shape[1], table.stride(0), window, max_new,
-                               max_length, out.data_ptr(), lse.data_ptr() if return_lse else None, code,
-                               dim ** -0.5 if scale is None else scale)
-        ref, need, lib = ctypes.byref(args), ctypes.c_uint64(), _lib()
-        st = lib.nq_kv_attention_workspace(cache._ref, ref, ctypes.byref(need))
-        ws = None
+        max_length = width * cache.block
+    if scale is None:
+        scale = dim ** -0.5
+    code = _kv_dtype(q.dtype)
+    lib, ref, strides = _lib(), cache._ref, q.stride()
+    out = q.new_empty((n, q_heads, dim))
+    lse = q.new_empty((n, q_heads), dtype=t["f32"]) if return_lse else None
+    args = _ATTENTION_ARGS.pack(q.data_ptr(), strides[0], strides[1], n, q_heads, requests, token_start.data_ptr(),
+                                lengths.data_ptr(), table.data_ptr(), width, table.stride(0), window, max_new,
+                                max_length, out.data_ptr(), lse.data_ptr() if return_lse else 0, code, scale)
+    # the workspace is a function of the sizes alone: asked for once for each
+    sizes = (n, q_heads, requests, width, window, max_new, max_length, code)
+    need = cache._workspaces.get(sizes)
+    st = NQ_OK
+    if need is None:
+        asked = ctypes.c_uint64()
+        st = lib.nq_kv_attention_workspace(ref, args, asked)
+        need = asked.value
         if st == NQ_OK:
-            if need.value:
-                ws = torch.empty(need.value, dtype=torch.uint8, device=cache.device)
-            st = lib.nq_kv_attention(cache._ref, ref, ws.data_ptr() if need.value else None, need.value,
-                                     stream.cuda_stream)
+            if len(cache._workspaces) >= 1024:
+                cache._workspaces.clear()
+            cache._workspaces[sizes] = need
+    if st == NQ_OK:
+        ws = q.new_empty(need, dtype=t["u8"]) if need else None
+        st = lib.nq_kv_attention(ref, args, ws.data_ptr() if need else None, need, t["handle"](index))
     if st != NQ_OK:
         raise NqError(st, f"q {list(q.shape)} {q.dtype}, {requests} requests, table {list(table.shape)}, "
                           f"window {window}, max_new {max_new}, max_length {max_length}")
