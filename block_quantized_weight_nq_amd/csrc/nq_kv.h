@@ -91,15 +91,18 @@ NQ_HD KvTile kv_tile(int added, int length, int cap, int group, int tile, int RO
     return t;
 }
 
-// Block of key position `key` (a multiple of 16 or inside such a run), or -1
-// where the tile must not look: past its keys, before its window, or where
-// the table names no block of the pool.
-template <class Table>
-NQ_HD int kv_page(const Table &table, int key, const KvTile &t, uint32_t bsh, int64_t blocks) {
-    const int idx = key >> bsh;
-    if (key >= t.kend || ((idx + 1) << bsh) <= t.kb) return -1;
-    const int p = table(idx);
-    return p >= 0 && (int64_t)p < blocks ? p : -1;
+// The table entry that names the block of key position `key`, kept inside the
+// entries of the tile's keys, and the block it names, or -1 where the tile
+// must not look: past its keys, before its window, or where the table names no
+// block of the pool.  Two steps, so that a kernel can have entries on their
+// way while it works on others.
+NQ_HD int kv_entry(int key, const KvTile &t, uint32_t bsh) {
+    const int last = (t.kend - 1) >> bsh, i = key >> bsh;
+    return i < last ? i : last < 0 ? 0 : last;
+}
+NQ_HD int kv_named(int entry, int key, const KvTile &t, uint32_t bsh, int64_t blocks) {
+    if (key >= t.kend || (((key >> bsh) + 1) << bsh) <= t.kb) return -1;
+    return entry >= 0 && (int64_t)entry < blocks ? entry : -1;
 }
 
 // Byte offsets of a key's codes and of a channel's codes from token `key` on,

@@ -39,7 +39,7 @@ void kv_attn_plan(KvAttnLaunch &L, uint32_t cus) {
     L.chunk = 256;
     if (L.dtype == 0) L.few = 1 << 30;  // two terms leave no registers for 32 rows a wave
     if (rows > L.few) {
-        L.waves = L.c.dim == 128 && rows > 128 ? 8 : 4;
+        L.waves = L.c.dim == 128 ? 8 : 4;
         const int64_t tr = 32 * L.waves;
         const int64_t tiles = (rows + tr - 1) / tr;
         L.tiles = (int32_t)tiles;
@@ -47,7 +47,7 @@ void kv_attn_plan(KvAttnLaunch &L, uint32_t cus) {
         int64_t busy = (int64_t)L.tokens * L.group / tr + L.requests;
         if (busy > L.requests * tiles) busy = L.requests * tiles;
         busy *= L.c.heads;
-        const int64_t want = L.waves == 8 ? cus : 2 * cus;
+        const int64_t want = L.c.dim == 64 ? 2 * cus : cus;  // workgroups that the card holds
         cut(span_of(tr), busy >= want ? 1 : (want + busy - 1) / busy, 512, &L.chunk, &L.splits);
     }
     const int64_t few_rows = rows < L.few ? rows : L.few;

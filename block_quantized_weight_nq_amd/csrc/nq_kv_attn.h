@@ -58,7 +58,7 @@ __device__ __forceinline__ float kv_row_scale(float amax) {
 __device__ __forceinline__ float kv_xor_max(float x, int d) { return fmaxf(x, __shfl_xor(x, d, 64)); }
 __device__ __forceinline__ float kv_xor_add(float x, int d) { return x + __shfl_xor(x, d, 64); }
 
-// Rows of a request's table, as kv_page reads them.
+// A request's row of the table.
 struct KvTableRow {
     const int32_t *row;
     __device__ __forceinline__ int operator()(int i) const { return row[i]; }
@@ -190,8 +190,14 @@ __global__ __launch_bounds__(256, 2) void k_kv_attn_dec(KvAttnArgs args) {
     for (int d = 0; d < ND; d++) O[d] = kv_f4{0, 0, 0, 0};
     float m = -__builtin_inff(), l = 0.0f, vref = KV_TINY;
 
+    // Table entries are read a tile ahead of the codes that they lead to.
+    int ek = 0, ev = 0;
+    auto find = [&](int key0) {
+        ek = table(kv_entry(key0 + KPG * (r >> 2), t, bsh));
+        ev = table(kv_entry(key0 + KPG * g, t, bsh));
+    };
     auto load_k = [&](int key0) {
-        const int pg = kv_page(table, key0 + KPG * (r >> 2), t, bsh, a.c.blocks);
+        const int pg = kv_named(ek, key0 + KPG * (r >> 2), t, bsh, a.c.blocks);
         const uint8_t *src = a.c.k + kv_k_at(a.c, pg, head, key0 + kr) + 16 * g;
 #pragma unroll
         for (int n = 0; n < NT; n++)
@@ -199,12 +205,17 @@ __global__ __launch_bounds__(256, 2) void k_kv_attn_dec(KvAttnArgs args) {
             for (int i = 0; i < NA; i++) K[n][i] = *(const kv_u4 *)(src + 4 * n * DIM + 64 * i);
     };
 
-    int key0 = k0 + wave * KT;
-    if (key0 < k1) load_k(key0);
+    int key0 = k0 + wave * KT, at_v = 0;
+    if (key0 < k1) {
+        find(key0);
+        load_k(key0);
+        at_v = ev;
+        find(key0 + 4 * KT);
+    }
     for (; key0 < k1; key0 += 4 * KT) {
         // values and scales of the lane's own keys
         const int kv0 = key0 + KPG * g;
-        const int pg = kv_page(table, kv0, t, bsh, a.c.blocks);
+        const int pg = kv_named(at_v, kv0, t, bsh, a.c.blocks);
         const int64_t sc_at = (int64_t)(pg < 0 ? 0 : pg) * a.c.heads + head;
         float ks = a.c.ks[sc_at], vs = a.c.vs[sc_at];
         if (pg < 0) ks = vs = 0.0f;
@@ -236,6 +247,8 @@ __global__ __launch_bounds__(256, 2) void k_kv_attn_dec(KvAttnArgs args) {
                 }
         }
         if (key0 + 4 * KT < k1) load_k(key0 + 4 * KT);
+        at_v = ev;
+        find(key0 + 8 * KT);
 
         const float cf = qscale * ks;
         const bool dead = pg < 0;

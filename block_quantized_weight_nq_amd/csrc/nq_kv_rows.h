@@ -1,11 +1,10 @@
 // nq_kv_rows.h -- attention over the 8-bit key/value cache for many rows (prompts, chunks of prompts) of 16-bit queries.
 //
 // The formulas and the arithmetic are nq_kv_attn.h's.  With many rows the
-// matrix instructions bound the work, so a key's codes are converted to
-// binary16 once for 32 * NW rows: a workgroup of NW waves stages 64 keys at a
-// time in LDS (two buffers, one barrier a tile; the codes of the next tile
-// but one are on their way to registers), and each wave holds 32 rows: their
-// queries and outputs stay in registers.  With lane = 32 h + r:
+// matrix instructions and the softmax bound the work, so a key's codes are
+// converted to binary16 once for 32 * NW rows: a workgroup of NW waves stages
+// 64 keys at a time in LDS, and each wave holds 32 rows, whose queries and
+// outputs stay in registers.  With lane = 32 h + r:
 //   scores  A = keys [32][16 channels], B = the queries: the result gives lane
 //           (r = query row, h) the keys 32 kt + 8 j + 4 h + i;
 //   output  A = values [32 channels][16 keys], B = the weights, which are
@@ -13,6 +12,13 @@
 //           0-3 8-11 4-7 12-15, so that a lane's eight are contiguous.
 // Rows of the LDS tiles are padded by 16 bytes: 16 lanes' reads then fall into
 // different banks.
+//
+// A wave alone issues a vector instruction every 8 cycles or so, and a SIMD
+// has only two of these waves, so each wave mixes its own work: the scores of
+// tile i + 1 are multiplied while the weights of tile i are formed, and the
+// codes of the tiles after are converted while its output is multiplied.
+// Keys are staged two tiles ahead and values one, in two buffers each; one
+// barrier a tile.
 #pragma once
 
 #include "nq_kv_attn.h"
@@ -23,15 +29,21 @@ typedef float kv_f16x __attribute__((ext_vector_type(16)));
 
 template <int DIM, int NW>
 struct KvRows {
-    static constexpr int KT = 64, ROWS = 32 * NW, TB = 64 * NW;
-    static constexpr int UNITS = KT * DIM / 16;             // 16-byte pieces of a tile's keys, and of its values
-    static constexpr int NL = UNITS / TB;                   // a thread's
+    static constexpr int KT = 64, ROWS = 32 * NW;
+    static constexpr int PER = NW / 4;                      // waves that stage 16 keys
+    static constexpr int KL = 1024 / DIM;                   // keys of a 1 KB piece
+    static constexpr int NL = 16 / (PER * KL);              // a wave's pieces of the keys, and of the values
     static constexpr int KS = DIM + 8, VS = KT + 8;         // row strides in LDS, binary16 elements
     static constexpr int K_ELEMS = KT * KS, V_ELEMS = DIM * VS;
-    static constexpr int BUF = K_ELEMS + V_ELEMS;           // elements of a buffer
-    static constexpr int LDS_BYTES = 2 * BUF * 2 + 2 * 8 * 4;
-    static_assert(NL >= 1 && NL * TB == UNITS, "every thread stages the same number of pieces");
+    static constexpr int SC = 20;                           // floats of a buffer's scales, below
+    static constexpr int LDS_BYTES = 2 * (K_ELEMS + V_ELEMS) * 2 + 2 * SC * 4;
+    static_assert(NL >= 1 && NL * PER * KL == 16 && NL * PER * 64 == DIM, "the waves share 16 keys evenly");
 };
+
+// Weights are times 2^14: a row's maximum in use may lag behind by 2^KV_LAG
+// before its output is multiplied down (binary16 holds up to 2^16).
+constexpr float KV_ROWS_PSCALE = 16384.0f, KV_LAG = 1.5f;
+constexpr float KV_VREF_MIN = 0x1p-100f;
 
 // Codes of keys outside [lo, hi), or of no block, become 0: what lies there may be E4M3's NaN.
 __device__ __forceinline__ void kv_mask16(kv_u4 &w, int key, int lo, int hi, bool dead) {
@@ -52,17 +64,60 @@ __device__ __forceinline__ float kv_max_halves(float x) {
     return fmaxf(__builtin_bit_cast(float, (uint32_t)p[0]), __builtin_bit_cast(float, (uint32_t)p[1]));
 }
 
+// A lane's half of its query row (the 16-channel steps' channels 8 h..+7, at element `at` of q) as binary16 with the
+// row's power of two; returns what a product with a key's codes is multiplied by, times the scale and log2(e).
+template <int IN, int NS>
+__device__ __forceinline__ float kv_load_rows(const KvAttnLaunch &a, int64_t at, kv_h8 (&Q)[NS]) {
+    float amax = 0.0f;
+    float f[NS][8];
+#pragma unroll
+    for (int s = 0; s < NS; s++) {
+        if (a.q_vec) {
+            kv_read4<IN, true>(a.q, at + 16 * s, *(float(*)[4])&f[s][0]);
+            kv_read4<IN, true>(a.q, at + 16 * s + 4, *(float(*)[4])&f[s][4]);
+        } else {
+            kv_read4<IN, false>(a.q, at + 16 * s, *(float(*)[4])&f[s][0]);
+            kv_read4<IN, false>(a.q, at + 16 * s + 4, *(float(*)[4])&f[s][4]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i++) amax = fmaxf(amax, fabsf(f[s][i]));
+    }
+    const float up = kv_row_scale(kv_max_halves(amax));
+#pragma unroll
+    for (int s = 0; s < NS; s++)
+#pragma unroll
+        for (int i = 0; i < 8; i++) Q[s][i] = (_Float16)(f[s][i] * up);
+    return a.scale * KV_LOG2E / up;
+}
+
+// The scales of 16 keys for the weights (their place in the kernels' sc).
+__device__ __forceinline__ void kv_put_scales(float *s, float ks, float vs, bool dead) {
+    const bool odd = !(ks > 0.0f && vs > 0.0f && vs < __builtin_inff());
+    s[0] = dead ? 1.0f : ks;  // a block that is not there: its keys are masked, any scale will do
+    s[4] = dead ? KV_VREF_MIN : vs;
+    s[8] = __builtin_amdgcn_logf(dead ? KV_VREF_MIN : vs);
+    s[12] = __builtin_amdgcn_rcpf(dead ? KV_VREF_MIN : vs);  // 1 ulp
+    ((int *)s)[16] = dead ? 3 : odd ? 2 : 0;
+}
+
+
+// Scheduling of a block: matrix instructions with their LDS reads, spread over the block's vector instructions.
+#define KV_MIX_SCORES
+#define KV_MIX_OUTPUT
 template <int CODE, int DIM, int IN, int NW>
 __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void k_kv_attn_rows(KvAttnArgs args) {
     using C = KvRows<DIM, NW>;
-    constexpr int KT = C::KT, NL = C::NL, KS = C::KS, VS = C::VS, TB = C::TB;
+    constexpr int KT = C::KT, NL = C::NL, KS = C::KS, VS = C::VS, SC = C::SC, KL = C::KL;
     constexpr int NS = DIM / 16;  // channel steps of a score
     constexpr int ND = DIM / 32;  // output tiles
     extern __shared__ __align__(16) uint8_t lds_raw[];
-    _Float16 *const buf = (_Float16 *)lds_raw;
-    float *const sc = (float *)(lds_raw + 2 * C::BUF * 2);  // [2][8]: key scales, value scales of 16 keys
+    _Float16 *const kbuf = (_Float16 *)lds_raw, *const vbuf = kbuf + 2 * C::K_ELEMS;
+    // of 16 keys each: [0-3] key scales, [4-7] value scales, [8-11] their base-2 logarithms, [12-15] their
+    // inverses, [16-19] flags: 1 no block, 2 a scale that is not positive
+    float *const sc = (float *)(vbuf + 2 * C::V_ELEMS);
     const KvAttnLaunch &a = args.L;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 31, h = lane >> 5;
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t head = blockIdx.x % a.c.heads;
     const int tile = a.tiles - 1 - (int)(blockIdx.x / a.c.heads);  // the longest rows first
     const int split = (int)blockIdx.y, req = (int)blockIdx.z, group = a.group;
@@ -87,137 +142,110 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void k_kv_attn_rows(KvA
     const int all_lo = a.window > 0 ? t.base + w1 - a.window + 1 : 0;
 
     kv_h8 Q[NS];
-    float qscale;
-    {
-        const int64_t at = (int64_t)(q.s0 + tok) * a.q_ts + ((int64_t)head * group + row % group) * a.q_hs + 8 * h;
-        float amax = 0.0f;
-        float f[NS][8];
-#pragma unroll
-        for (int s = 0; s < NS; s++) {
-            if (a.q_vec) {
-                kv_read4<IN, true>(a.q, at + 16 * s, *(float(*)[4])&f[s][0]);
-                kv_read4<IN, true>(a.q, at + 16 * s + 4, *(float(*)[4])&f[s][4]);
-            } else {
-                kv_read4<IN, false>(a.q, at + 16 * s, *(float(*)[4])&f[s][0]);
-                kv_read4<IN, false>(a.q, at + 16 * s + 4, *(float(*)[4])&f[s][4]);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; i++) amax = fmaxf(amax, fabsf(f[s][i]));
-        }
-        amax = kv_max_halves(amax);
-        const float up = kv_row_scale(amax);
-        qscale = a.scale * KV_LOG2E / up;
-#pragma unroll
-        for (int s = 0; s < NS; s++)
-#pragma unroll
-            for (int i = 0; i < 8; i++) Q[s][i] = (_Float16)(f[s][i] * up);
-    }
+    const float qscale = kv_load_rows<IN, NS>(a, (int64_t)(q.s0 + tok) * a.q_ts + ((int64_t)head * group + row % group) * a.q_hs + 8 * h, Q);
 
-    // Staging: a thread's pieces of a tile's keys (16 channels of a key) and values (16 keys of a channel).
-    const KvTableRow table = {a.table + (int64_t)req * a.table_stride};
-    const uint32_t bsh = a.c.bsh;
+    // Staging: all pieces of a wave lie in the same 16 keys, so a tile takes it one table entry.  A piece of the keys
+    // is 1 KB in a row (KL keys), one of the values 16 keys of 64 channels.  What lies past the last tile is fetched
+    // and staged as if it were there (from block 0): nothing reads it.
+    const int sub = wave / C::PER, part = wave % C::PER;
+    const int32_t *const table = a.table + (int64_t)req * a.table_stride;
+    const uint32_t bsh = a.c.bsh, tmask = (1u << bsh) - 1, tile_bytes = (uint32_t)DIM << bsh;
+    const uint8_t *const kbase = a.c.k + (uint64_t)head * tile_bytes + (part * NL * KL) * DIM + 16 * lane;
+    const uint8_t *const vbase = a.c.v + (uint64_t)head * tile_bytes + (((uint32_t)(64 * part * NL + lane)) << bsh);
+    const uint32_t block_bytes = a.c.heads * tile_bytes;  // at most 2^16 * 2^15
+    _Float16 *const kput = kbuf + (16 * sub + part * NL * KL + lane / (DIM / 16)) * KS + 16 * (lane % (DIM / 16));
+    _Float16 *const vput = vbuf + (64 * part * NL + lane) * VS + 16 * sub;
     kv_u4 rk[NL], rv[NL];
-    int pk[NL], pv[NL];  // blocks of the pieces
+    int entry = 0, page = -1, was = -1;  // the table entry on its way, the block of the keys and of the values fetched last
     float rks = 0.0f, rvs = 0.0f;
-    auto find = [&](int key0) {
+    // Vector loads, though the address is the wave's: scalar ones share the LDS reads' counter and complete out of
+    // order, so that every wait for an LDS read would wait for memory.
+    int none = 0;
+    asm volatile("" : "+v"(none));
+    auto find = [&](int key0) { entry = table[kv_entry(key0 + 16 * sub, t, bsh) + none]; };
+    auto fetch_k = [&](int key0) {
+        page = kv_named(__builtin_amdgcn_readfirstlane(entry), key0 + 16 * sub, t, bsh, a.c.blocks);
+        const uint8_t *const src = kbase + (uint64_t)(uint32_t)(page < 0 ? 0 : page) * block_bytes + (((key0 + 16 * sub) & tmask) * DIM);
 #pragma unroll
-        for (int n = 0; n < NL; n++) {
-            const int u = tid + n * TB;
-            pk[n] = kv_page(table, key0 + u / (DIM / 16), t, bsh, a.c.blocks);
-            pv[n] = kv_page(table, key0 + 16 * (u & 3), t, bsh, a.c.blocks);
+        for (int n = 0; n < NL; n++) rk[n] = *(const kv_u4 *)(src + n * 1024);
+    };
+    auto fetch_v = [&](int key0, int block) {
+        was = block;
+        const uint32_t at = block < 0 ? 0 : (uint32_t)block;
+        const uint8_t *const src = vbase + (uint64_t)at * block_bytes + ((key0 + 16 * sub) & tmask);
+#pragma unroll
+        for (int n = 0; n < NL; n++) rv[n] = *(const kv_u4 *)(src + ((uint32_t)(64 * n) << bsh));
+        if (part == 0) {
+            const uint64_t s = (uint64_t)at * a.c.heads + head + none;
+            rks = a.c.ks[s];
+            rvs = a.c.vs[s];
         }
     };
-    auto fetch = [&](int key0) {
+    auto clean_v = [&](int key0) {  // signed bytes are finite whatever they are, and their weights 0
+        if constexpr (CODE == KV_E4M3)
+#pragma unroll
+            for (int n = 0; n < NL; n++) kv_mask16(rv[n], key0 + 16 * sub, t.kb, t.kend, was < 0);
+    };
+    auto stage_k = [&](int b) {
 #pragma unroll
         for (int n = 0; n < NL; n++) {
-            const int u = tid + n * TB;
-            rk[n] = *(const kv_u4 *)(a.c.k + kv_k_at(a.c, pk[n], head, key0 + u / (DIM / 16)) + 16 * (u % (DIM / 16)));
-            rv[n] = *(const kv_u4 *)(a.c.v + kv_v_at(a.c, pv[n], head, u >> 2, key0 + 16 * (u & 3)));
-        }
-        if (tid < 4) {
-            const int64_t at = (int64_t)(pv[0] < 0 ? 0 : pv[0]) * a.c.heads + head;
-            rks = a.c.ks[at];
-            rvs = a.c.vs[at];
+            _Float16 *const d = kput + b * C::K_ELEMS + n * KL * KS;
+            *(kv_h8 *)d = kv_codes8_f16<CODE>(kv_u2{rk[n][0], rk[n][1]});
+            *(kv_h8 *)(d + 8) = kv_codes8_f16<CODE>(kv_u2{rk[n][2], rk[n][3]});
         }
     };
-    // dead: the pieces' blocks when they were fetched
-    auto stage = [&](int key0, int b, const int (&was)[NL]) {
-        _Float16 *const K = buf + b * C::BUF, *const V = K + C::K_ELEMS;
+    auto stage_v = [&](int b) {
 #pragma unroll
         for (int n = 0; n < NL; n++) {
-            const int u = tid + n * TB;
-            _Float16 *const dk = K + (u / (DIM / 16)) * KS + 16 * (u % (DIM / 16));
-            *(kv_h8 *)dk = kv_codes8_f16<CODE>(kv_u2{rk[n][0], rk[n][1]});
-            *(kv_h8 *)(dk + 8) = kv_codes8_f16<CODE>(kv_u2{rk[n][2], rk[n][3]});
-            kv_mask16(rv[n], key0 + 16 * (u & 3), t.kb, t.kend, was[n] < 0);
-            _Float16 *const dv = V + (u >> 2) * VS + 16 * (u & 3);
-            *(kv_h8 *)dv = kv_codes8_f16<CODE>(kv_u2{rv[n][0], rv[n][2]});
-            *(kv_h8 *)(dv + 8) = kv_codes8_f16<CODE>(kv_u2{rv[n][1], rv[n][3]});
+            _Float16 *const d = vput + b * C::V_ELEMS + 64 * n * VS;
+            *(kv_h8 *)d = kv_codes8_f16<CODE>(kv_u2{rv[n][0], rv[n][2]});
+            *(kv_h8 *)(d + 8) = kv_codes8_f16<CODE>(kv_u2{rv[n][1], rv[n][3]});
         }
-        if (tid < 4) {
-            // a block that is not there: its keys are masked, any scale will do
-            sc[8 * b + tid] = was[0] < 0 ? 0.0f : rks;
-            sc[8 * b + 4 + tid] = was[0] < 0 ? 0.0f : rvs;
-        }
+    };
+    auto stage_scales = [&](int b) {
+        if (part == 0 && lane == 0) kv_put_scales(sc + SC * b + sub, rks, rvs, was < 0);
     };
 
+    // O and l are in units of 2^14 / vref: O sums x codes and l sums x / vs, x = 2^(score - m) vs 2^14 / vref.
     kv_f16x O[ND];
 #pragma unroll
     for (int d = 0; d < ND; d++)
 #pragma unroll
         for (int i = 0; i < 16; i++) O[d][i] = 0.0f;
-    float m = -__builtin_inff(), l = 0.0f, vref = KV_TINY;
+    float m = -__builtin_inff(), l = 0.0f;
+    float vref = KV_VREF_MIN, unit = KV_ROWS_PSCALE / KV_VREF_MIN, lunit = 114.0f;  // and log2(unit)
 
-    int was[NL];
-    if (k0 < k1) {
-        find(k0);
-        fetch(k0);
+    auto scores = [&](int b, kv_f16x (&S)[2]) {
+        const _Float16 *const K = kbuf + b * C::K_ELEMS + r * KS + 8 * h;
 #pragma unroll
-        for (int n = 0; n < NL; n++) was[n] = pv[n];
-        find(k0 + KT);
-        stage(k0, 0, was);
-        if (k0 + KT < k1) fetch(k0 + KT);
-#pragma unroll
-        for (int n = 0; n < NL; n++) was[n] = pv[n];
-        find(k0 + 2 * KT);
-    }
-    __syncthreads();
-    int b = 0;
-    for (int key0 = k0; key0 < k1; key0 += KT, b ^= 1) {
-        const _Float16 *const K = buf + b * C::BUF, *const V = K + C::K_ELEMS;
-        kv_f16x S[2];
-#pragma unroll
-        for (int kt = 0; kt < 2; kt++) {
+        for (int kt = 0; kt < 2; kt++)
 #pragma unroll
             for (int i = 0; i < 16; i++) S[kt][i] = 0.0f;
+        // two sums in turn: a matrix instruction does not wait for the one before it
 #pragma unroll
-            for (int s = 0; s < NS; s++) {
-                const kv_h8 kk = *(const kv_h8 *)(K + (32 * kt + r) * KS + 16 * s + 8 * h);
-                S[kt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kk, Q[s], S[kt], 0, 0, 0);
-            }
-        }
-        float ks[4], vs[4];
+        for (int s = 0; s < NS; s++)
 #pragma unroll
-        for (int g = 0; g < 4; g++) {
-            ks[g] = sc[8 * b + g];
-            vs[g] = sc[8 * b + 4 + g];
-        }
-        if (key0 + KT < k1) {
-            stage(key0 + KT, b ^ 1, was);
-            if (key0 + 2 * KT < k1) fetch(key0 + 2 * KT);
-#pragma unroll
-            for (int n = 0; n < NL; n++) was[n] = pv[n];
-            find(key0 + 3 * KT);
-        }
-        // scores in base-2 logarithms
+            for (int kt = 0; kt < 2; kt++)
+                S[kt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const kv_h8 *)(K + 32 * kt * KS + 16 * s), Q[s], S[kt], 0, 0, 0);
+    };
+
+    // Tile i (keys from key0 on): its scores are in S; next gets those of tile i + 1.  b = i mod 2.
+    auto step = [&](int key0, int b, kv_f16x (&S)[2], kv_f16x (&next)[2]) {
+        const float *const s4 = sc + SC * b;
+        const kv_f4 ks = *(const kv_f4 *)s4, vs = *(const kv_f4 *)(s4 + 4), lv = *(const kv_f4 *)(s4 + 8);
+        const kv_f4 iv = *(const kv_f4 *)(s4 + 12);
+        const kv_u4 fl = *(const kv_u4 *)(s4 + 16);
+        const int flags = __builtin_amdgcn_readfirstlane((int)(fl[0] | fl[1] | fl[2] | fl[3]));
+        const float most = fmaxf(fmaxf(fabsf(vs[0]), fabsf(vs[1])), fmaxf(fabsf(vs[2]), fabsf(vs[3])));
+        const float fewest = fminf(fminf(vs[0], vs[1]), fminf(vs[2], vs[3]));
+        const float vr1 = fmaxf(vref, most);
+        // scores in base-2 logarithms are S * cf.  Scales that are not positive, and value scales far below vref
+        // (whose weights would leave binary32's range where l divides by the scale), take the plain order.
+        const bool odd = (flags & 2) || !(a.scale > 0.0f) || __ballot(fewest * 0x1p20f < vr1);
         float cf[4];
-        bool odd = false;
 #pragma unroll
-        for (int g = 0; g < 4; g++) {
-            cf[g] = qscale * ks[g];
-            odd |= !(cf[g] > 0.0f);
-        }
-        if (__ballot(odd)) {  // negative, zero or NaN scales, blocks that are not there
+        for (int g = 0; g < 4; g++) cf[g] = qscale * ks[g];
+        if (odd) {
 #pragma unroll
             for (int g = 0; g < 4; g++) {
 #pragma unroll
@@ -225,13 +253,10 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void k_kv_attn_rows(KvA
                 cf[g] = 1.0f;
             }
         }
-        bool gone = false;
-#pragma unroll
-        for (int g = 0; g < 4; g++) gone |= ks[g] == 0.0f && vs[g] == 0.0f;
-        if (key0 < all_lo || key0 + KT > all_hi || __ballot(gone)) {
+        if (key0 < all_lo || key0 + KT > all_hi || (flags & 1)) {
 #pragma unroll
             for (int g = 0; g < 4; g++) {
-                const bool dead = kv_page(table, key0 + 16 * g, t, bsh, a.c.blocks) < 0;
+                const bool dead = fl[g] & 1;
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
                     const int key = key0 + 16 * g + 8 * (i >> 2) + 4 * h + (i & 3);
@@ -239,106 +264,145 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void k_kv_attn_rows(KvA
                 }
             }
         }
-        float top = -__builtin_inff(), vr1 = vref;
+        float top = -__builtin_inff(), low[4];
 #pragma unroll
         for (int g = 0; g < 4; g++) {
-            float x = S[g >> 1][8 * (g & 1)];
+            float high = S[g >> 1][8 * (g & 1)];
+            low[g] = high;
 #pragma unroll
-            for (int i = 1; i < 8; i++) x = fmaxf(x, S[g >> 1][8 * (g & 1) + i]);
-            top = fmaxf(top, x * cf[g]);
-            vr1 = fmaxf(vr1, fabsf(vs[g]));
+            for (int i = 1; i < 8; i++) {
+                high = fmaxf(high, S[g >> 1][8 * (g & 1) + i]);
+                low[g] = fminf(low[g], S[g >> 1][8 * (g & 1) + i]);
+            }
+            top = fmaxf(top, high * cf[g]);
         }
         top = kv_max_halves(top);
-        const float m1 = fmaxf(m, top), safe = m1 == -__builtin_inff() ? 0.0f : m1;
-        float fo = 1.0f;
-        if (__ballot(m1 > m || vr1 > vref)) {
-            const float alpha = kv_exp2(m - safe);
-            l *= alpha;
-            fo = alpha * (vref / vr1);
+        // the maximum in use may be lower than the true one by KV_LAG
+        if (__ballot(top > m + KV_LAG || vr1 > vref)) {
+            const float m1 = fmaxf(m, top);
+            const float fo = kv_exp2(m - (m1 == -__builtin_inff() ? 0.0f : m1)) * (vref / vr1);
+            l *= fo;
 #pragma unroll
             for (int d = 0; d < ND; d++)
 #pragma unroll
                 for (int i = 0; i < 16; i++) O[d][i] *= fo;
             m = m1;
             vref = vr1;
+            unit = KV_ROWS_PSCALE / vref;
+            lunit = __builtin_amdgcn_logf(unit);
         }
-        float least = KV_PSCALE;
-        const float unit = KV_PSCALE / vref;
+        const float safe = m == -__builtin_inff() ? 0.0f : m;
+        clean_v(key0 + KT);
+        const _Float16 *const V = vbuf + b * C::V_ELEMS + r * VS + 8 * h;
+        kv_h8 P[4];
+        float at[4], least = 0.0f;  // and the logarithm of the smallest weight
 #pragma unroll
         for (int g = 0; g < 4; g++) {
-            const float w = vs[g] * unit;
-            float sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const float e = kv_exp2(__builtin_fmaf(S[g >> 1][8 * (g & 1) + i], cf[g], -safe));
-                const float x = e * w;
-                sum += e;
-                S[g >> 1][8 * (g & 1) + i] = x;
-                least = fminf(least, fabsf(x));
-            }
-            l += sum;
+            at[g] = lv[g] + lunit - safe;
+            least = fminf(least, __builtin_fmaf(low[g], cf[g], at[g]));
         }
-        // O += values * weights.  Where some weights are small, those once more by themselves, multiplied by the
-        // power of two that brings the row's largest of them to [2^13, 2^14).
-        const bool slow = __ballot(least < KvLevel<1>::LEAST) != 0;
-        float up = 1.0f;
-        kv_h8 P[4], P2[4];
+        if (!odd && !__ballot(!(least >= -14.0f))) {
+            scores(b ^ 1, next);
+#pragma unroll
+            for (int g = 0; g < 4; g++) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const float x = kv_exp2(__builtin_fmaf(S[g >> 1][8 * (g & 1) + i], cf[g], at[g]));
+                    sum += x;
+                    P[g][i] = (_Float16)x;
+                }
+                l = __builtin_fmaf(sum, iv[g], l);
+            }
+            KV_MIX_SCORES
+        } else {
+            asm volatile("" ::: "memory");
+            // Any scales; small weights by themselves, times the power of two that brings the row's largest of them
+            // in 16 keys to [2^13, 2^14).
+#pragma unroll
+            for (int g = 0; g < 4; g++) {
+                const float w = vs[g] * unit;
+                float x[8], sum = 0.0f, big = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const float e = kv_exp2(__builtin_fmaf(S[g >> 1][8 * (g & 1) + i], cf[g], -safe));
+                    x[i] = e * w;
+                    sum += e;
+                    P[g][i] = (_Float16)x[i];
+                    big = fmaxf(big, fabsf(x[i]) < KvLevel<1>::LEAST ? fabsf(x[i]) : 0.0f);
+                }
+                l = __builtin_fmaf(sum, unit, l);
+                if (__ballot(big > 0.0f)) {
+                    const int e = (int)(__builtin_bit_cast(uint32_t, kv_max_halves(big)) >> 23) - 127;
+                    const float up = bits_f32((uint32_t)(127 + (13 - e < 120 ? 13 - e : 120)) << 23), down = 1.0f / up;
+                    kv_h8 W;
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        const bool is = fabsf(x[i]) < KvLevel<1>::LEAST;
+                        W[i] = (_Float16)(is ? x[i] * up : 0.0f);
+                        P[g][i] = is ? (_Float16)0.0f : P[g][i];
+                    }
+#pragma unroll
+                    for (int d = 0; d < ND; d++) {
+                        kv_f16x acc;
+#pragma unroll
+                        for (int i = 0; i < 16; i++) acc[i] = 0.0f;
+                        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const kv_h8 *)(V + 32 * d * VS + 16 * g), W, acc, 0, 0, 0);
+#pragma unroll
+                        for (int i = 0; i < 16; i++) O[d][i] = __builtin_fmaf(acc[i], down, O[d][i]);
+                    }
+                }
+                asm volatile("" ::: "memory");  // the values are read again, not held meanwhile
+            }
+            scores(b ^ 1, next);
+        }
 #pragma unroll
         for (int g = 0; g < 4; g++)
 #pragma unroll
-            for (int i = 0; i < 8; i++) P[g][i] = (_Float16)S[g >> 1][8 * (g & 1) + i];
-        if (slow) {
-            float most = 0.0f;
-#pragma unroll
-            for (int g = 0; g < 4; g++)
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const float x = fabsf(S[g >> 1][8 * (g & 1) + i]);
-                    most = fmaxf(most, x < KvLevel<1>::LEAST ? x : 0.0f);
-                }
-            // |O| <= 2^14 * 448 * 2 max(l): up stops where their product would pass 2^127
-            const int e = (int)(__builtin_bit_cast(uint32_t, kv_max_halves(most)) >> 23) - 127;
-            const int el = (int)(__builtin_bit_cast(uint32_t, kv_max_halves(l)) >> 23) - 127;
-            const int room = el > 0 ? 100 - el : 100;
-            up = bits_f32((uint32_t)(127 + (13 - e < room ? 13 - e : room)) << 23);
-#pragma unroll
-            for (int g = 0; g < 4; g++)
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const float x = S[g >> 1][8 * (g & 1) + i];
-                    const bool small = fabsf(x) < KvLevel<1>::LEAST;
-                    P[g][i] = small ? (_Float16)0.0f : P[g][i];
-                    P2[g][i] = (_Float16)(small ? x * up : 0.0f);
-                }
-        }
-#pragma unroll
-        for (int d = 0; d < ND; d++)
-#pragma unroll
-            for (int g = 0; g < 4; g++) {
-                const kv_h8 vv = *(const kv_h8 *)(V + (32 * d + r) * VS + 16 * g + 8 * h);
-                O[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv, P[g], O[d], 0, 0, 0);
-            }
-        if (slow) {
-#pragma unroll
-            for (int d = 0; d < ND; d++) {
-#pragma unroll
-                for (int i = 0; i < 16; i++) O[d][i] *= up;
-#pragma unroll
-                for (int g = 0; g < 4; g++) {
-                    const kv_h8 vv = *(const kv_h8 *)(V + (32 * d + r) * VS + 16 * g + 8 * h);
-                    O[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv, P2[g], O[d], 0, 0, 0);
-                }
-#pragma unroll
-                for (int i = 0; i < 16; i++) O[d][i] *= 1.0f / up;
-            }
-        }
+            for (int d = 0; d < ND; d++)
+                O[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const kv_h8 *)(V + 32 * d * VS + 16 * g), P[g], O[d], 0, 0, 0);
+        stage_k(b);
+        stage_v(b ^ 1);
+        KV_MIX_OUTPUT
+        stage_scales(b ^ 1);
+        const int block = page;  // of the keys of tile i + 2
+        fetch_k(key0 + 3 * KT);
+        fetch_v(key0 + 2 * KT, block);
+        find(key0 + 4 * KT);
         __syncthreads();
+    };
+
+    const int nt = (k1 - k0 + KT - 1) / KT;
+    if (nt > 0) {
+        // keys of tiles 0 and 1 and values of tile 0 into LDS; those of tiles 2 and 1 on their way
+        find(k0);
+        fetch_k(k0);
+        find(k0 + KT);
+        fetch_v(k0, page);
+        stage_k(0);
+        clean_v(k0);
+        stage_v(0);
+        stage_scales(0);
+        fetch_k(k0 + KT);
+        find(k0 + 2 * KT);
+        fetch_v(k0 + KT, page);
+        stage_k(1);
+        fetch_k(k0 + 2 * KT);
+        find(k0 + 3 * KT);
+        __syncthreads();
+        kv_f16x S0[2], S1[2];
+        scores(0, S0);
+        __syncthreads();  // tile 0 is read before tile 2 is staged in its place
+        for (int i = 0; i < nt; i += 2) {
+            step(k0 + i * KT, 0, S0, S1);
+            if (i + 1 < nt) step(k0 + (i + 1) * KT, 1, S1, S0);
+        }
     }
 
     l += __shfl_xor(l, 32, 64);
     if (row_at >= t.rows) return;
-    const float inv = l == 0.0f ? 0.0f : vref * (1.0f / KV_PSCALE) / l;
-    const float lse2 = l == 0.0f ? -__builtin_inff() : (m == -__builtin_inff() ? 0.0f : m) + __builtin_amdgcn_logf(l);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float lse2 = l == 0.0f ? -__builtin_inff() : (m == -__builtin_inff() ? 0.0f : m) + __builtin_amdgcn_logf(l / unit);
     const int64_t oat = (int64_t)(q.s0 + tok) * a.q_heads + (int64_t)head * group + row % group;
     const int64_t pat = oat * a.max_splits + split;
 #pragma unroll
@@ -369,15 +433,10 @@ int launch_kv_attn_dim(const KvAttnLaunch &L, hipStream_t s) {
     KvAttnArgs a{L};
     if constexpr (TERMS == 1) {
         const dim3 grid(L.c.heads * (uint32_t)L.tiles, (uint32_t)L.splits, (uint32_t)L.requests);
-        if (L.waves == 4) {
-            hipLaunchKernelGGL((k_kv_attn_rows<CODE, DIM, IN, 4>), grid, dim3(256), (KvRows<DIM, 4>::LDS_BYTES), s, a);
+        if (L.waves > 0) {
+            constexpr int NW = DIM == 128 ? 8 : 4;
+            hipLaunchKernelGGL((k_kv_attn_rows<CODE, DIM, IN, NW>), grid, dim3(64 * NW), (KvRows<DIM, NW>::LDS_BYTES), s, a);
             if (hipGetLastError() != hipSuccess) return 9;  // NQ_ERR_HIP
-        }
-        if constexpr (DIM == 128) {
-            if (L.waves == 8) {
-                hipLaunchKernelGGL((k_kv_attn_rows<CODE, DIM, IN, 8>), grid, dim3(512), (KvRows<DIM, 8>::LDS_BYTES), s, a);
-                if (hipGetLastError() != hipSuccess) return 9;  // NQ_ERR_HIP
-            }
         }
     }
     const dim3 grid(L.c.heads * (uint32_t)L.tiles_few, (uint32_t)L.splits_few, (uint32_t)L.requests + 1);

@@ -22,6 +22,10 @@ struct HostTable {
         return row[i];
     }
 };
+
+int page_of(const HostTable &tab, int key, const nq::KvTile &t, int bsh, int64_t blocks) {
+    return nq::kv_named(tab(nq::kv_entry(key, t, (uint32_t)bsh)), key, t, (uint32_t)bsh, blocks);
+}
 }  // namespace
 
 // How often each token is stored: the units of a store launch over starts
@@ -72,12 +76,12 @@ EMU_API long nq_kv_emu_attention(int added, int length, int cap, int group, int 
                     for (int lane = 0; lane < 64; lane++)
                         for (int head = 0; head < heads; head += heads > 1 ? heads - 1 : 1) {
                             const int r = lane & 15, g = lane >> 4;
-                            const int kp = nq::kv_page(tab, key0 + KPG * (r >> 2), t, (uint32_t)bsh, blocks);
+                            const int kp = page_of(tab, key0 + KPG * (r >> 2), t, bsh, blocks);
                             const int64_t k = nq::kv_k_at(c, kp, (uint32_t)head, key0 + KPG * (r >> 2) + (r & 3)) + 16 * g;
                             const int64_t kl = k + 4 * (KT / 16 - 1) * dim + 64 * (dim / 64 - 1) + 16;
                             bad += k < 0 || kl > pool;
                             const int kv0 = key0 + KPG * g;
-                            const int vp = nq::kv_page(tab, kv0, t, (uint32_t)bsh, blocks);
+                            const int vp = page_of(tab, kv0, t, bsh, blocks);
                             const int64_t v = nq::kv_v_at(c, vp, (uint32_t)head, r, kv0);
                             bad += v < 0 || v + ((int64_t)(dim / 16 - 1) << (bsh + 4)) + KPG > pool;
                             bad += vp >= 0 && (kv0 & ((1 << bsh) - 1)) + KPG > (1 << bsh);
