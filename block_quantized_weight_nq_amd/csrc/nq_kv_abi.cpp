@@ -16,9 +16,12 @@ int launch_kv_attn_e4m3(const KvAttnLaunch &L, hipStream_t s);
 //
 // Requests of at most `few` rows go to the kernel for few rows, the others to
 // the one for many.  A piece is `chunk` keys: several pieces a row let few
-// rows fill the card, each costs a partial output.  For few rows 512 keys keep
-// the slowest workgroup short where lengths differ; many rows are cut only
-// where the tiles leave compute units idle.
+// rows fill the card, each costs a workgroup's start and end and a partial
+// output.  Measured for few rows at pieces of 256, 512, 1024, 2048 and 4096
+// keys: 128 ragged requests of up to 8200 keys 127, 99, 86, 82 and 88 us; two
+// of 131001 and about 90000 keys 153, 114, 97, 95 and 92 us; 32 requests
+// with 5 tokens and a window of 2049 keys 37, 33, 32, 38 and 33 us.  Many rows
+// are cut only where the tiles leave compute units idle.
 void kv_attn_plan(KvAttnLaunch &L, uint32_t cus) {
     const int64_t rows = (int64_t)L.max_new * L.group;
     auto span_of = [&](int64_t tile_rows) {
@@ -28,7 +31,7 @@ void kv_attn_plan(KvAttnLaunch &L, uint32_t cus) {
     };
     auto cut = [](int64_t span, int64_t pieces, int64_t least, int32_t *chunk, int32_t *splits) {
         if (pieces > 65535) pieces = 65535;
-        int64_t c = ((span + pieces - 1) / pieces + 255) / 256 * 256;
+        int64_t c = ((span + pieces - 1) / pieces + 63) / 64 * 64;
         if (c < least) c = least;
         *chunk = (int32_t)c;
         *splits = (int32_t)((span + c - 1) / c);
@@ -56,9 +59,10 @@ void kv_attn_plan(KvAttnLaunch &L, uint32_t cus) {
     int64_t busy = (int64_t)L.tokens * L.group / 16 + L.requests;
     if (busy > (int64_t)L.requests * L.tiles_few) busy = (int64_t)L.requests * L.tiles_few;
     busy *= L.c.heads;
-    // many tiles (prompts in binary32) fill the card by themselves
-    const int64_t pieces = L.tiles_few > 4 ? (busy >= 8ll * cus ? 1 : (8ll * cus + busy - 1) / busy) : (span + 511) / 512;
-    cut(span, pieces, 256, &L.chunk_few, &L.splits_few);
+    // six workgroups a compute unit, and no piece above 2048 keys where lengths differ
+    int64_t pieces = busy > 0 ? (6ll * cus + busy - 1) / busy : 1;
+    if (L.tiles_few <= 4 && pieces < (span + 2047) / 2048) pieces = (span + 2047) / 2048;
+    cut(span, pieces, 512, &L.chunk_few, &L.splits_few);
     L.max_splits = L.splits > L.splits_few ? L.splits : L.splits_few;
 }
 }  // namespace nq

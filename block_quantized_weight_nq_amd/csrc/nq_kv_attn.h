@@ -142,43 +142,13 @@ __global__ __launch_bounds__(256, 2) void k_kv_attn_dec(KvAttnArgs args) {
     const int k0 = t.kbeg + split * a.chunk_few;
     const int k1 = t.kend - k0 > a.chunk_few ? k0 + a.chunk_few : t.kend;
 
-    // this lane's query row (as the column of the score tiles)
+    // this lane's query row (as the column of the score tiles); the last row stands in for those past it
     const int row = tile * 16 + r < t.rows ? tile * 16 + r : t.rows - 1, tok = row / group;
     const int p = t.base + tok;
     const int hi = p + 1 < t.live ? p + 1 : t.live;
     const int lo = a.window > 0 && p - a.window + 1 > 0 ? p - a.window + 1 : 0;
     const int all_hi = t.base + t.first + 1 < t.live ? t.base + t.first + 1 : t.live;
     const int all_lo = a.window > 0 ? t.base + t.last - a.window + 1 : 0;
-    kv_h8 Q[TERMS][2 * NA];
-    float qscale;
-    {
-        float f[NA][16];
-        float amax = 0.0f;
-        const int64_t at = (int64_t)(q.s0 + tok) * a.q_ts + ((int64_t)head * group + row % group) * a.q_hs;
-        // the tile's last row stands in for the rows past it: nothing of theirs is written
-#pragma unroll
-        for (int i = 0; i < NA; i++) {
-            if (a.q_vec)
-                kv_read16<IN, true>(a.q, at + 64 * i + 16 * g, f[i]);
-            else
-                kv_read16<IN, false>(a.q, at + 64 * i + 16 * g, f[i]);
-#pragma unroll
-            for (int k = 0; k < 16; k++) amax = fmaxf(amax, fabsf(f[i][k]));
-        }
-        amax = kv_xor_max(kv_xor_max(amax, 16), 32);
-        const float up = kv_row_scale(amax);
-        qscale = a.scale * KV_LOG2E / up;
-#pragma unroll
-        for (int i = 0; i < NA; i++)
-#pragma unroll
-            for (int k = 0; k < 16; k++) {
-                const float x = f[i][k] * up;
-                const _Float16 h = (_Float16)x;
-                Q[0][2 * i + (k >> 3)][k & 7] = h;
-                if constexpr (TERMS == 2) Q[1][2 * i + (k >> 3)][k & 7] = (_Float16)(x - (float)h);
-            }
-    }
-
     const KvTableRow table = {a.table + (int64_t)req * a.table_stride};
     const uint32_t bsh = a.c.bsh;
     const int kr = KPG * (r >> 2) + (r & 3);  // key of row r in score tile 0
@@ -206,11 +176,42 @@ __global__ __launch_bounds__(256, 2) void k_kv_attn_dec(KvAttnArgs args) {
     };
 
     int key0 = k0 + wave * KT, at_v = 0;
+    if (key0 < k1) find(key0);
+    // the row's loads and the table's first, the keys' next, then the row's conversion
+    float f[NA][16];
+    const int64_t qat = (int64_t)(q.s0 + tok) * a.q_ts + ((int64_t)head * group + row % group) * a.q_hs;
+#pragma unroll
+    for (int i = 0; i < NA; i++) {
+        if (a.q_vec)
+            kv_read16<IN, true>(a.q, qat + 64 * i + 16 * g, f[i]);
+        else
+            kv_read16<IN, false>(a.q, qat + 64 * i + 16 * g, f[i]);
+    }
     if (key0 < k1) {
-        find(key0);
         load_k(key0);
         at_v = ev;
         find(key0 + 4 * KT);
+    }
+    kv_h8 Q[TERMS][2 * NA];
+    float qscale;
+    {
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NA; i++)
+#pragma unroll
+            for (int k = 0; k < 16; k++) amax = fmaxf(amax, fabsf(f[i][k]));
+        amax = kv_xor_max(kv_xor_max(amax, 16), 32);
+        const float up = kv_row_scale(amax);
+        qscale = a.scale * KV_LOG2E / up;
+#pragma unroll
+        for (int i = 0; i < NA; i++)
+#pragma unroll
+            for (int k = 0; k < 16; k++) {
+                const float x = f[i][k] * up;
+                const _Float16 h = (_Float16)x;
+                Q[0][2 * i + (k >> 3)][k & 7] = h;
+                if constexpr (TERMS == 2) Q[1][2 * i + (k >> 3)][k & 7] = (_Float16)(x - (float)h);
+            }
     }
     for (; key0 < k1; key0 += 4 * KT) {
         // values and scales of the lane's own keys
@@ -434,11 +435,23 @@ __global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs args) {
     float o[PL], sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < PL; i++) o[i] = 0.0f;
-    for (int s = wave; s < t.nsplit; s += 4) {
-        const float w = kv_exp2(pl[s] - safe);
-        sum += w;
+    for (int s0 = wave; s0 < t.nsplit; s0 += 32) {  // eight pieces of this wave on their way at a time
+        float w[8], x[8][PL];
 #pragma unroll
-        for (int i = 0; i < PL; i++) o[i] += w * po[(int64_t)s * DIM + lane + 64 * i];
+        for (int k = 0; k < 8; k++) {
+            const int s = s0 + 4 * k < t.nsplit ? s0 + 4 * k : t.nsplit - 1;
+            w[k] = pl[s];
+#pragma unroll
+            for (int i = 0; i < PL; i++) x[k][i] = po[(int64_t)s * DIM + lane + 64 * i];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            if (s0 + 4 * k >= t.nsplit) break;
+            const float e = kv_exp2(w[k] - safe);
+            sum += e;
+#pragma unroll
+            for (int i = 0; i < PL; i++) o[i] += e * x[k][i];
+        }
     }
 #pragma unroll
     for (int i = 0; i < PL; i++) so[wave][lane + 64 * i] = o[i];

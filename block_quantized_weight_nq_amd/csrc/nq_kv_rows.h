@@ -100,10 +100,6 @@ __device__ __forceinline__ void kv_put_scales(float *s, float ks, float vs, bool
     ((int *)s)[16] = dead ? 3 : odd ? 2 : 0;
 }
 
-
-// Scheduling of a block: matrix instructions with their LDS reads, spread over the block's vector instructions.
-#define KV_MIX_SCORES
-#define KV_MIX_OUTPUT
 template <int CODE, int DIM, int IN, int NW>
 __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void k_kv_attn_rows(KvAttnArgs args) {
     using C = KvRows<DIM, NW>;
@@ -314,7 +310,6 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void k_kv_attn_rows(KvA
                 }
                 l = __builtin_fmaf(sum, iv[g], l);
             }
-            KV_MIX_SCORES
         } else {
             asm volatile("" ::: "memory");
             // Any scales; small weights by themselves, times the power of two that brings the row's largest of them
@@ -363,7 +358,6 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void k_kv_attn_rows(KvA
                 O[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const kv_h8 *)(V + 32 * d * VS + 16 * g), P[g], O[d], 0, 0, 0);
         stage_k(b);
         stage_v(b ^ 1);
-        KV_MIX_OUTPUT
         stage_scales(b ^ 1);
         const int block = page;  // of the keys of tile i + 2
         fetch_k(key0 + 3 * KT);
