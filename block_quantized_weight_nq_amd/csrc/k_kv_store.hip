@@ -7,10 +7,13 @@
 // So a block that fills token by token keeps one scale, and its earlier codes
 // are rounded again only when a new token is larger than all before it.
 //
-// One workgroup per block, head and kind (keys or values); it reads its new
-// values twice (the second time from the cache: at most 64 KB in 16 bits).
-// The first pass finds amax, the second writes.  What bounds it is the
-// bytes of the new values for prompts, and latency for single tokens.
+// One workgroup per block, head and kind (keys or values).  A thread takes
+// tiles of four tokens by four channels: a dword of four codes is then a
+// token's four channels (keys) or a channel's four tokens (values) without a
+// transpose.  Its first two tiles stay in registers between the search for
+// amax and the writing, later ones (blocks of more than 8192 values) are read
+// again.  What bounds it: the bytes of the new values for prompts, and the
+// chain of dependent loads (starts, slot, values) for single tokens.
 #include "nq_kv_codes.h"
 
 namespace nq {
@@ -53,19 +56,27 @@ __global__ void k_kv_clear_status(uint32_t *status) { *status = 0u; }
 template <int CODE, int IN, bool VEC>
 __global__ __launch_bounds__(TB) void k_kv_store(KvStoreLaunch a) {
     __shared__ float wmax[TB / 64];
+    __shared__ int32_t found[3];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const uint32_t head = blockIdx.y, kind = blockIdx.z;
     const int64_t u = blockIdx.x, T = (int64_t)1 << a.c.bsh, n = a.tokens;
     const int D = (int)a.c.dim, bsh = (int)a.c.bsh;
 
-    // the request of this unit: the last one whose first unit is not past u
-    int r = -1;
-    for (int b = 0; b < a.requests; b += TB) {
-        const int i = b + tid;
-        r += __syncthreads_count(i < a.requests && kv_unit_first(a.starts[i], i, a.c.bsh) <= u);
+    // the request of this unit
+    if (tid == 0) found[0] = -1;
+    __syncthreads();
+    for (int i = tid; i < a.requests; i += TB) {
+        const int32_t s0 = a.starts[i], s1 = a.starts[i + 1];
+        if (kv_unit_first(s0, i, a.c.bsh) <= u && u < kv_unit_first(s1, i + 1, a.c.bsh)) {
+            found[0] = i;
+            found[1] = s0;
+            found[2] = s1;
+        }
     }
+    __syncthreads();
+    const int r = found[0];
     if (r < 0) return;
-    int64_t s0 = a.starts[r], s1 = a.starts[r + 1];
+    int64_t s0 = found[1], s1 = found[2];
     const int64_t j = u - kv_unit_first(s0, r, a.c.bsh);
     if (s1 > n) s1 = n;
     if (s0 < 0 || s0 >= s1) return;
@@ -74,88 +85,114 @@ __global__ __launch_bounds__(TB) void k_kv_store(KvStoreLaunch a) {
     int64_t lo, hi;
     kv_unit_tokens(s0, s1, j, slot0 & (T - 1), a.c.bsh, &lo, &hi);
     if (lo >= hi) return;
+    // the values are on their way while the slots are checked
+    const int cnt = (int)(hi - lo), first = lo > s0 ? 0 : (int)(slot0 & (T - 1)), last = first + cnt;
+    const void *x = a.x[kind];
+    const int64_t ts = a.ts[kind], x0 = (lo - first) * ts + head * a.hs[kind];
+    const int q4 = D / 4, g0 = first / 4, ng = (last + 3) / 4 - g0, tiles = ng * q4;
+    const auto place = [&](int i, int *g, int *c4) {  // lanes run along what the codes are contiguous in
+        *g = g0 + (kind == 0 ? i / q4 : i % ng);
+        *c4 = kind == 0 ? i % q4 : i / ng;
+    };
+    const auto read = [&](int g, int c4, float (&f)[4][4]) {  // [token][channel], 0 where there is no new token
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const int tok = 4 * g + k;
+            f[k][0] = f[k][1] = f[k][2] = f[k][3] = 0.0f;
+            if (tok >= first && tok < last) kv_read4<IN, VEC>(x, x0 + (int64_t)tok * ts + 4 * c4, f[k]);
+        }
+    };
+    float held[2][4][4], amax = 0.0f;
+    bool bad = false;
+#pragma unroll
+    for (int m = 0; m < 2; m++) {
+        int g, c4;
+        place(tid + m * TB < tiles ? tid + m * TB : 0, &g, &c4);
+        if (tid + m * TB < tiles) read(g, c4, held[m]);
+    }
     const int64_t slot = a.slots[lo];
-    bool wrong = slot < 0 || slot >= pool || (lo > s0 && (slot & (T - 1)) != 0);
-    const int cnt = (int)(hi - lo), first = (int)(slot & (T - 1));
+    bool wrong = slot < 0 || slot >= pool || (slot & (T - 1)) != first;
     if (tid < cnt) wrong |= a.slots[lo + tid] != slot + tid;
-    if (__syncthreads_or(wrong || first + cnt > (int)T)) {
+    if (__syncthreads_or(wrong)) {
         if (tid == 0) atomicOr(a.status, KV_ST_BAD_SLOT);
         return;
     }
     const int64_t block = slot >> bsh;
     uint8_t *codes = (kind ? a.c.v : a.c.k) + kv_tile_at(a.c, block, head);
     float *scale = (kind ? a.c.vs : a.c.ks) + block * a.c.heads + head;
-    const void *x = a.x[kind];
-    const int64_t ts = a.ts[kind], x0 = lo * ts + head * a.hs[kind];
-
-    const int q4 = D / 4, items = cnt * q4;  // four channels of one token
-    float amax = 0.0f;
-    bool bad = false;
-    for (int i = tid; i < items; i += TB) {
-        float f[4];
-        kv_read4<IN, VEC>(x, x0 + (int64_t)(i / q4) * ts + 4 * (i % q4), f);
-        amax = fmaxf(amax, amax4(f, &bad));
+    const float old = first > 0 ? *scale : 0.0f;
+#pragma unroll
+    for (int m = 0; m < 2; m++)
+        if (tid + m * TB < tiles)
+#pragma unroll
+            for (int k = 0; k < 4; k++) amax = fmaxf(amax, amax4(held[m][k], &bad));
+    for (int i = tid + 2 * TB; i < tiles; i += TB) {
+        int g, c4;
+        float f[4][4];
+        place(i, &g, &c4);
+        read(g, c4, f);
+#pragma unroll
+        for (int k = 0; k < 4; k++) amax = fmaxf(amax, amax4(f[k], &bad));
     }
     for (int d = 1; d < 64; d <<= 1) amax = fmaxf(amax, __shfl_xor(amax, d, 64));
     if (lane == 0) wmax[wave] = amax;
     if (__syncthreads_or(bad) && tid == 0) atomicOr(a.status, KV_ST_NOT_FINITE);
     for (int w = 0; w < TB / 64; w++) amax = fmaxf(amax, wmax[w]);
-    const float old = first > 0 ? *scale : 0.0f;
     const float now = fmaxf(fmaxf(old, amax / qmax<CODE>()), KV_TINY);
     const float inv = 1.0f / now, ratio = old / now;
     const bool grow = first > 0 && now > old;
-    __syncthreads();  // every thread has the old scale
-    if (tid == 0) *scale = now;
+    if (tid == 0) *scale = now;  // every thread has the old one: they have passed a barrier since
 
-    if (kind == 0) {
-        uint32_t *row = (uint32_t *)codes + first * q4;
-        for (int i = tid; i < items; i += TB) {
-            float f[4];
-            kv_read4<IN, VEC>(x, x0 + (int64_t)(i / q4) * ts + 4 * (i % q4), f);
+    const auto write = [&](int g, int c4, const float (&f)[4][4]) {
+        uint32_t is_new = 0;  // bytes of a dword of four tokens
 #pragma unroll
-            for (int k = 0; k < 4; k++) f[k] = (f[k] == f[k] ? f[k] : 0.0f) * inv;
-            row[i] = kv_f32_codes4<CODE>(f);
-        }
-        if (grow)
-            for (int i = tid; i < first * q4; i += TB) {
-                uint32_t *w = (uint32_t *)codes + i;
-                *w = rescale4<CODE>(*w, ratio);
+        for (int k = 0; k < 4; k++)
+            if (4 * g + k >= first && 4 * g + k < last) is_new |= 0xFFu << (8 * k);
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const float v = kind == 0 ? f[k][e] : f[e][k];
+                y[e] = (v == v ? v : 0.0f) * inv;
             }
-        return;
+            uint32_t w = kv_f32_codes4<CODE>(y);
+            if (kind == 0) {
+                if (is_new >> (8 * k) & 1u) ((uint32_t *)codes)[(4 * g + k) * q4 + c4] = w;
+            } else {
+                uint32_t *at = (uint32_t *)(codes + ((4 * c4 + k) << bsh) + 4 * g);
+                if (is_new != 0xFFFFFFFFu) {
+                    const uint32_t was = *at;
+                    uint32_t is_old = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        if (4 * g + e < first) is_old |= 0xFFu << (8 * e);
+                    const uint32_t kept = grow && is_old ? (rescale4<CODE>(was, ratio) & is_old) | (was & ~is_old) : was;
+                    w = (w & is_new) | (kept & ~is_new);
+                }
+                *at = w;
+            }
+        }
+    };
+#pragma unroll
+    for (int m = 0; m < 2; m++) {
+        int g, c4;
+        place(tid + m * TB < tiles ? tid + m * TB : 0, &g, &c4);
+        if (tid + m * TB < tiles) write(g, c4, held[m]);
     }
-    // Values: four channels of four tokens a thread, a dword of four tokens per channel.
-    const int last = first + cnt;
-    const int g0 = grow ? 0 : first / 4, g1 = (last + 3) / 4, ng = g1 - g0;
-    for (int i = tid; i < ng * q4; i += TB) {
-        const int g = g0 + i % ng, c4 = i / ng, t0 = 4 * g;
-        float f[4][4];  // [token][channel]
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-            if (t0 + k >= first && t0 + k < last)
-                kv_read4<IN, VEC>(x, x0 + (int64_t)(t0 + k - first) * ts + 4 * c4, f[k]);
-            else
-                f[k][0] = f[k][1] = f[k][2] = f[k][3] = 0.0f;
-        }
-        uint32_t is_new = 0, is_old = 0;  // byte masks
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-            if (t0 + k >= first && t0 + k < last) is_new |= 0xFFu << (8 * k);
-            if (t0 + k < first) is_old |= 0xFFu << (8 * k);
-        }
-#pragma unroll
-        for (int ch = 0; ch < 4; ch++) {
-            uint32_t *w = (uint32_t *)(codes + ((4 * c4 + ch) << bsh) + t0);
-            float g4[4];
-#pragma unroll
-            for (int k = 0; k < 4; k++) g4[k] = (f[k][ch] == f[k][ch] ? f[k][ch] : 0.0f) * inv;
-            uint32_t res = kv_f32_codes4<CODE>(g4);
-            if (is_new != 0xFFFFFFFFu) {
-                const uint32_t was = *w;
-                const uint32_t kept = grow && is_old ? (rescale4<CODE>(was, ratio) & is_old) | (was & ~is_old) : was;
-                res = (res & is_new) | (kept & ~is_new);
-            }
-            *w = res;
-        }
+    for (int i = tid + 2 * TB; i < tiles; i += TB) {
+        int g, c4;
+        float f[4][4];
+        place(i, &g, &c4);
+        read(g, c4, f);
+        write(g, c4, f);
+    }
+    if (!grow) return;
+    // codes before the first new token, four a dword; a dword of values that has a new token is done
+    const int old_dw = kind == 0 ? first * q4 : g0 * D;
+    for (int i = tid; i < old_dw; i += TB) {
+        uint32_t *w = (uint32_t *)codes + (kind == 0 ? i : (i / g0 << bsh) / 4 + i % g0);
+        *w = rescale4<CODE>(*w, ratio);
     }
 }
 
@@ -189,54 +226,74 @@ int launch_kv_store(const KvStoreLaunch &L, hipStream_t s) {
 }
 
 // Load: the values RN32(c * scale) of whole blocks, [n, T, heads, D] for keys
-// and for values.  A block that is not in the pool gives zeros.  One
-// workgroup per block, head and kind; value blocks turn through LDS.
+// and for values.  A block that is not in the pool gives zeros.  A workgroup
+// takes a block's kind and several heads, about 16 KB of codes; a thread writes
+// eight channels (16 bytes of a 16-bit type), and value blocks turn through LDS.
 template <int CODE, int OT>
 __global__ __launch_bounds__(TB) void k_kv_load(KvLoadLaunch a) {
-    extern __shared__ uint32_t tile[];  // [D][T / 4 + 1], an odd stride in dwords
+    extern __shared__ uint32_t tile[];  // [heads * D][T / 4 + 1], an odd stride in dwords
     const int tid = threadIdx.x;
-    const uint32_t head = blockIdx.y, kind = blockIdx.z;
-    const int D = (int)a.c.dim, T = 1 << a.c.bsh, q4 = D / 4;
+    const uint32_t kind = blockIdx.z;
+    const int D = (int)a.c.dim, T = 1 << a.c.bsh, q8 = D / 8;
+    const int h0 = (int)blockIdx.y * a.group, nh = h0 + a.group < (int)a.c.heads ? a.group : (int)a.c.heads - h0;
     const int64_t b = blockIdx.x;
     const int64_t block = a.ids[b];
     const bool live = block >= 0 && block < a.c.blocks;
-    const uint32_t *codes = (const uint32_t *)((kind ? a.c.v : a.c.k) + kv_tile_at(a.c, live ? block : 0, head));
-    const float scale = live ? (kind ? a.c.vs : a.c.ks)[block * a.c.heads + head] : 0.0f;
-    const int64_t row = (int64_t)a.c.heads * D;
-    const int64_t y0 = b * T * row + (int64_t)head * D;
+    const uint32_t *codes = (const uint32_t *)((kind ? a.c.v : a.c.k) + kv_tile_at(a.c, live ? block : 0, h0));
+    const float *scales = (kind ? a.c.vs : a.c.ks) + (live ? block : 0) * a.c.heads + h0;
+    const int64_t row = (int64_t)a.c.heads * D, y0 = b * T * row + (int64_t)h0 * D;
     void *y = a.out[kind];
+    const int per = nh * q8;  // eights of channels of a token
     if (kind == 0) {
-        for (int i = tid; i < T * q4; i += TB) {
-            float f[4];
-            kv_codes4_f32<CODE>(live ? codes[i] : 0u, f);
+        for (int i = tid; i < T * per; i += TB) {
+            const int t = i / per, c = i % per, h = c / q8;
+            const float s = live ? scales[h] : 0.0f;
+            const kv_u2 w = *(const kv_u2 *)(codes + (int64_t)(h * T + t) * (D / 4) + 2 * (c % q8));
 #pragma unroll
-            for (int k = 0; k < 4; k++) f[k] = f[k] * scale;
-            kv_write4<OT>(y, y0 + (i / q4) * row + 4 * (i % q4), f);
+            for (int e = 0; e < 2; e++) {
+                float f[4];
+                kv_codes4_f32<CODE>(live ? w[e] : 0u, f);
+#pragma unroll
+                for (int k = 0; k < 4; k++) f[k] = f[k] * s;
+                kv_write4<OT>(y, y0 + t * row + 8 * c + 4 * e, f);
+            }
         }
         return;
     }
-    const int tq = T / 4, stride = tq + 1;
-    for (int i = tid; i < D * tq; i += TB) tile[(i / tq) * stride + i % tq] = live ? codes[i] : 0u;
+    const int tq = T / 4, stride = tq + 1, all = nh * D * tq;
+    for (int i = 4 * tid; i < all; i += 4 * TB) {  // T is at least 16: four dwords of one channel
+        const kv_u4 w = *(const kv_u4 *)(codes + i);
+#pragma unroll
+        for (int k = 0; k < 4; k++) tile[i / tq * stride + i % tq + k] = live ? w[k] : 0u;
+    }
     __syncthreads();
-    for (int i = tid; i < tq * q4; i += TB) {
-        const int c4 = i % q4, g = i / q4;
-        float f[4][4];  // [channel][token]
+    for (int i = tid; i < tq * per; i += TB) {
+        const int c = i % per, g = i / per;
+        const float s = live ? scales[c / q8] : 0.0f;
+        float f[8][4];  // [channel][token]
 #pragma unroll
-        for (int ch = 0; ch < 4; ch++) kv_codes4_f32<CODE>(tile[(4 * c4 + ch) * stride + g], f[ch]);
+        for (int ch = 0; ch < 8; ch++) kv_codes4_f32<CODE>(tile[(8 * c + ch) * stride + g], f[ch]);
 #pragma unroll
-        for (int k = 0; k < 4; k++) {
-            float o[4];
+        for (int k = 0; k < 4; k++)
 #pragma unroll
-            for (int ch = 0; ch < 4; ch++) o[ch] = f[ch][k] * scale;
-            kv_write4<OT>(y, y0 + (4 * g + k) * row + 4 * c4, o);
-        }
+            for (int e = 0; e < 2; e++) {
+                float o[4];
+#pragma unroll
+                for (int ch = 0; ch < 4; ch++) o[ch] = f[4 * e + ch][k] * s;
+                kv_write4<OT>(y, y0 + (4 * g + k) * row + 8 * c + 4 * e, o);
+            }
     }
 }
 
 template <int CODE>
-static int load_code(const KvLoadLaunch &L, hipStream_t s) {
-    const dim3 grid((uint32_t)L.n, L.c.heads, 2);
-    const uint32_t lds = L.c.dim * ((1u << L.c.bsh) / 4 + 1) * 4;
+static int load_code(KvLoadLaunch L, hipStream_t s) {
+    // heads of a workgroup: 16 KB of codes, fewer where the blocks are too few for that (1024 workgroups)
+    const int64_t one = (int64_t)L.c.dim << L.c.bsh;
+    L.group = (int32_t)(one >= 16384 ? 1 : 16384 / one);
+    if (L.group > (int32_t)L.c.heads) L.group = (int32_t)L.c.heads;
+    while (L.group > 1 && 2 * L.n * ((L.c.heads + L.group - 1) / L.group) < 1024) L.group = (L.group + 1) / 2;
+    const dim3 grid((uint32_t)L.n, (L.c.heads + L.group - 1) / L.group, 2);
+    const uint32_t lds = (uint32_t)L.group * L.c.dim * ((1u << L.c.bsh) / 4 + 1) * 4;
     switch (L.out_dtype) {
     case 0: hipLaunchKernelGGL((k_kv_load<CODE, 0>), grid, dim3(TB), lds, s, L); break;
     case 1: hipLaunchKernelGGL((k_kv_load<CODE, 1>), grid, dim3(TB), lds, s, L); break;

@@ -21,7 +21,6 @@ namespace nq {
 
 namespace {
 
-constexpr int TB = 256;          // threads
 constexpr int TOK = 1024;        // tokens a workgroup's slots cover at a time
 constexpr uint32_t MAX_WG = 1024;  // workgroups of a launch
 
@@ -51,9 +50,12 @@ __device__ __forceinline__ int64_t up64(int64_t v, int d) { return __shfl_up(v, 
 
 }  // namespace
 
+// TB threads, each with its own requests: 256, or 1024 for more than 256 requests.
+template <int TB>
 __global__ __launch_bounds__(TB) void k_kv_tables(KvTablesLaunch a) {
     __shared__ Sums wsum[TB / 64];
-    __shared__ int32_t any_bad;
+    __shared__ int32_t any_bad, queued;
+    __shared__ int32_t m_req[TB], m_held[TB], m_count[TB], m_first[TB];
     __shared__ int32_t owner[TOK], o_req[TOK], o_start[TOK], o_took[TOK];
     __shared__ int32_t wtop[TB / 64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -125,39 +127,38 @@ __global__ __launch_bounds__(TB) void k_kv_tables(KvTablesLaunch a) {
 
     // 32-bit ring arithmetic: ring <= 2^30, first + j < count < 2^31 going in and < ring coming back.
     const int64_t tail = (head + count) % ring;
-    // Blocks in (pass 0) and out (pass 1): the requests of a thread's range
-    // one after the other, each by the whole wave.
+    // Blocks in (pass 0) and out (pass 1).  The workgroup's requests that have any queue up in LDS, one a thread at a
+    // time, and all threads move their blocks.
     auto move = [&](int pass) {
+        int64_t at = pass == 0 ? before.need : before.give;
         for (int k = 0; k < per; k++) {
+            if (tid == 0) queued = 0;
+            __syncthreads();
             const int r = r0 + k;
-            Req q = {0, 0, 0, 0, 0, false};
-            if (r < r1) q = request(a, r);
-            const bool mine_here = r < r1 && (uint32_t)r % G == blockIdx.x && (pass == 0 ? q.need > 0 : q.give > 0);
-            uint64_t todo = __ballot(mine_here);
-            const int64_t at = pass == 0 ? before.need : before.give;
-            while (todo) {
-                const int src = __builtin_ctzll(todo);
-                todo &= todo - 1;
-                const int rr = __shfl(r, src, 64);
-                const int64_t n = __shfl(pass == 0 ? q.need : q.give, src, 64);
-                const int64_t held = __shfl(q.held, src, 64);
-                const int64_t first = __shfl(at, src, 64);
-                int32_t *row = a.table + (int64_t)rr * a.table_stride;
-                for (int64_t j = lane; j < n; j += 64) {
+            if (r < r1) {
+                const Req q = request(a, r);
+                const int64_t n = pass == 0 ? q.need : q.give;
+                if (n > 0 && (uint32_t)r % G == blockIdx.x) {
+                    const int i = atomicAdd(&queued, 1);
+                    m_req[i] = r;
+                    m_held[i] = (int32_t)q.held;
+                    m_count[i] = (int32_t)n;
+                    m_first[i] = (int32_t)at;
+                }
+                at += n;
+            }
+            __syncthreads();
+            for (int i = 0; i < queued; i++) {
+                int32_t *row = a.table + (int64_t)m_req[i] * a.table_stride;
+                const int held = m_held[i], n = m_count[i], first = m_first[i];
+                for (int j = tid; j < n; j += TB) {
                     if (pass == 0)
                         row[held + j] = a.ring[(uint32_t)(head + first + j) % (uint32_t)ring];
                     else
                         a.ring[(uint32_t)(tail + first + j) % (uint32_t)ring] = row[j];
                 }
             }
-            before.need += q.need;
-            before.give += q.give;
-        }
-        for (int k = 0; k < per; k++) {
-            if (r0 + k >= r1) break;
-            const Req q = request(a, r0 + k);
-            before.need -= q.need;
-            before.give -= q.give;
+            __syncthreads();
         }
     };
     move(0);
@@ -226,7 +227,10 @@ __global__ __launch_bounds__(TB) void k_kv_tables(KvTablesLaunch a) {
 int launch_kv_tables(const KvTablesLaunch &L, hipStream_t s) {
     const uint64_t want = ((uint64_t)L.tokens + TOK - 1) / TOK;
     const uint32_t grid = want < 1 ? 1u : want > MAX_WG ? MAX_WG : (uint32_t)want;
-    hipLaunchKernelGGL(k_kv_tables, dim3(grid), dim3(TB), 0, s, L);
+    if (L.requests <= 256)
+        hipLaunchKernelGGL(k_kv_tables<256>, dim3(grid), dim3(256), 0, s, L);
+    else
+        hipLaunchKernelGGL(k_kv_tables<1024>, dim3(grid), dim3(1024), 0, s, L);
     return hipGetLastError() == hipSuccess ? 0 : 9;  // NQ_ERR_HIP
 }
 

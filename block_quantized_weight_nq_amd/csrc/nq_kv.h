@@ -150,6 +150,7 @@ struct KvLoadLaunch {
     void *out[2];
     int64_t n;
     int32_t code, out_dtype;
+    int32_t group;  // heads of a workgroup
 };
 int launch_kv_load(const KvLoadLaunch &L, hipStream_t s);
 
