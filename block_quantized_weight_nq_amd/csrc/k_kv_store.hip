@@ -7,10 +7,10 @@
 // So a block that fills token by token keeps one scale, and its earlier codes
 // are rounded again only when a new token is larger than all before it.
 //
-// One workgroup per block, head and kind (keys or values).  A thread takes
+// One workgroup per block and head, for keys and values.  A thread takes
 // tiles of four tokens by four channels: a dword of four codes is then a
 // token's four channels (keys) or a channel's four tokens (values) without a
-// transpose.  Its first two tiles stay in registers between the search for
+// transpose.  Its first one or two tiles of each stay in registers between the search for
 // amax and the writing, later ones (blocks of more than 8192 values) are read
 // again.  What bounds it: the bytes of the new values for prompts, and the
 // chain of dependent loads (starts, slot, values) for single tokens.
@@ -27,15 +27,23 @@ constexpr float qmax() {
     return CODE == KV_Q8 ? 127.0f : 448.0f;
 }
 
-// Largest magnitude among the finite ones of four values; *bad if one is not finite.
-__device__ __forceinline__ float amax4(const float (&f)[4], bool *bad) {
-    float m = 0.0f;
+// The larger of the magnitudes of four values and m, as words: integers in the
+// same order, infinities and NaN (0x7F800000 and up) above all finite ones.
+__device__ __forceinline__ uint32_t amax4(const float (&f)[4], uint32_t m) {
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        const float x = fabsf(f[i]);
-        const bool fin = x < __builtin_inff();
-        *bad |= !fin;
-        m = fmaxf(m, fin ? x : 0.0f);
+        const uint32_t x = __builtin_bit_cast(uint32_t, f[i]) & 0x7FFFFFFFu;
+        m = x > m ? x : m;
+    }
+    return m;
+}
+
+// The same over the finite ones.
+__device__ __forceinline__ uint32_t amax4_finite(const float (&f)[4], uint32_t m) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const uint32_t x = __builtin_bit_cast(uint32_t, f[i]) & 0x7FFFFFFFu;
+        m = x > m && x < 0x7F800000u ? x : m;
     }
     return m;
 }
@@ -53,14 +61,16 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
 
 __global__ void k_kv_clear_status(uint32_t *status) { *status = 0u; }
 
-template <int CODE, int IN, bool VEC>
+// HOLD: tiles of each kind that a thread keeps, 1 for blocks of up to 4096 values (fewer registers, more workgroups at
+// a time).
+template <int CODE, int IN, bool VEC, int HOLD>
 __global__ __launch_bounds__(TB) void k_kv_store(KvStoreLaunch a) {
-    __shared__ float wmax[TB / 64];
+    __shared__ uint32_t wmax[2][TB / 64];
     __shared__ int32_t found[3];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const uint32_t head = blockIdx.y, kind = blockIdx.z;
+    const uint32_t head = blockIdx.y;
     const int64_t u = blockIdx.x, T = (int64_t)1 << a.c.bsh, n = a.tokens;
-    const int D = (int)a.c.dim, bsh = (int)a.c.bsh;
+    const int bsh = (int)a.c.bsh, q4 = (int)a.c.dim / 4, qsh = __builtin_ctz(q4);  // dim is a power of two
 
     // the request of this unit
     if (tid == 0) found[0] = -1;
@@ -87,112 +97,132 @@ __global__ __launch_bounds__(TB) void k_kv_store(KvStoreLaunch a) {
     if (lo >= hi) return;
     // the values are on their way while the slots are checked
     const int cnt = (int)(hi - lo), first = lo > s0 ? 0 : (int)(slot0 & (T - 1)), last = first + cnt;
-    const void *x = a.x[kind];
-    const int64_t ts = a.ts[kind], x0 = (lo - first) * ts + head * a.hs[kind];
-    const int q4 = D / 4, g0 = first / 4, ng = (last + 3) / 4 - g0, tiles = ng * q4;
-    const auto place = [&](int i, int *g, int *c4) {  // lanes run along what the codes are contiguous in
-        *g = g0 + (kind == 0 ? i / q4 : i % ng);
-        *c4 = kind == 0 ? i % q4 : i / ng;
+    const int g0 = first / 4, ng = (last + 3) / 4 - g0, tiles = ng << qsh;
+    const auto place = [&](int kind, int i, int *g, int *c4) {  // lanes run along what the codes are contiguous in
+        *g = g0 + (kind == 0 ? i >> qsh : i % ng);
+        *c4 = kind == 0 ? i & (q4 - 1) : i / ng;
     };
-    const auto read = [&](int g, int c4, float (&f)[4][4]) {  // [token][channel], 0 where there is no new token
+    const auto read = [&](int kind, int g, int c4, float (&f)[4][4]) {  // [token][channel], 0 where there is no new token
+        const int64_t x0 = (lo - first) * a.ts[kind] + head * a.hs[kind];
 #pragma unroll
         for (int k = 0; k < 4; k++) {
             const int tok = 4 * g + k;
             f[k][0] = f[k][1] = f[k][2] = f[k][3] = 0.0f;
-            if (tok >= first && tok < last) kv_read4<IN, VEC>(x, x0 + (int64_t)tok * ts + 4 * c4, f[k]);
+            if (tok >= first && tok < last) kv_read4<IN, VEC>(a.x[kind], x0 + (int64_t)tok * a.ts[kind] + 4 * c4, f[k]);
         }
     };
-    float held[2][4][4], amax = 0.0f;
-    bool bad = false;
+    float held[2][HOLD][4][4];
+    uint32_t amax[2];
 #pragma unroll
-    for (int m = 0; m < 2; m++) {
-        int g, c4;
-        place(tid + m * TB < tiles ? tid + m * TB : 0, &g, &c4);
-        if (tid + m * TB < tiles) read(g, c4, held[m]);
-    }
+    for (int kind = 0; kind < 2; kind++)
+#pragma unroll
+        for (int m = 0; m < HOLD; m++) {
+            int g, c4;
+            place(kind, tid + m * TB < tiles ? tid + m * TB : 0, &g, &c4);
+            if (tid + m * TB < tiles) read(kind, g, c4, held[kind][m]);
+        }
     const int64_t slot = a.slots[lo];
     bool wrong = slot < 0 || slot >= pool || (slot & (T - 1)) != first;
     if (tid < cnt) wrong |= a.slots[lo + tid] != slot + tid;
     if (__syncthreads_or(wrong)) {
-        if (tid == 0) atomicOr(a.status, KV_ST_BAD_SLOT);
+        if (tid == 0 && head == 0) atomicOr(a.status, KV_ST_BAD_SLOT);
         return;
     }
-    const int64_t block = slot >> bsh;
-    uint8_t *codes = (kind ? a.c.v : a.c.k) + kv_tile_at(a.c, block, head);
-    float *scale = (kind ? a.c.vs : a.c.ks) + block * a.c.heads + head;
-    const float old = first > 0 ? *scale : 0.0f;
+    const int64_t block = slot >> bsh, tile = kv_tile_at(a.c, block, head), sat = block * a.c.heads + head;
+    const float old[2] = {first > 0 ? a.c.ks[sat] : 0.0f, first > 0 ? a.c.vs[sat] : 0.0f};
+    const auto largest = [&](bool finite) {
 #pragma unroll
-    for (int m = 0; m < 2; m++)
-        if (tid + m * TB < tiles)
+        for (int kind = 0; kind < 2; kind++) {
+            uint32_t top = 0;
 #pragma unroll
-            for (int k = 0; k < 4; k++) amax = fmaxf(amax, amax4(held[m][k], &bad));
-    for (int i = tid + 2 * TB; i < tiles; i += TB) {
-        int g, c4;
-        float f[4][4];
-        place(i, &g, &c4);
-        read(g, c4, f);
+            for (int m = 0; m < HOLD; m++)
+                if (tid + m * TB < tiles)
 #pragma unroll
-        for (int k = 0; k < 4; k++) amax = fmaxf(amax, amax4(f[k], &bad));
-    }
-    for (int d = 1; d < 64; d <<= 1) amax = fmaxf(amax, __shfl_xor(amax, d, 64));
-    if (lane == 0) wmax[wave] = amax;
-    if (__syncthreads_or(bad) && tid == 0) atomicOr(a.status, KV_ST_NOT_FINITE);
-    for (int w = 0; w < TB / 64; w++) amax = fmaxf(amax, wmax[w]);
-    const float now = fmaxf(fmaxf(old, amax / qmax<CODE>()), KV_TINY);
-    const float inv = 1.0f / now, ratio = old / now;
-    const bool grow = first > 0 && now > old;
-    if (tid == 0) *scale = now;  // every thread has the old one: they have passed a barrier since
-
-    const auto write = [&](int g, int c4, const float (&f)[4][4]) {
-        uint32_t is_new = 0;  // bytes of a dword of four tokens
+                    for (int k = 0; k < 4; k++) top = finite ? amax4_finite(held[kind][m][k], top) : amax4(held[kind][m][k], top);
+            for (int i = tid + HOLD * TB; i < tiles; i += TB) {
+                int g, c4;
+                float f[4][4];
+                place(kind, i, &g, &c4);
+                read(kind, g, c4, f);
 #pragma unroll
-        for (int k = 0; k < 4; k++)
-            if (4 * g + k >= first && 4 * g + k < last) is_new |= 0xFFu << (8 * k);
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-            float y[4];
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const float v = kind == 0 ? f[k][e] : f[e][k];
-                y[e] = (v == v ? v : 0.0f) * inv;
+                for (int k = 0; k < 4; k++) top = finite ? amax4_finite(f[k], top) : amax4(f[k], top);
             }
-            uint32_t w = kv_f32_codes4<CODE>(y);
-            if (kind == 0) {
-                if (is_new >> (8 * k) & 1u) ((uint32_t *)codes)[(4 * g + k) * q4 + c4] = w;
-            } else {
-                uint32_t *at = (uint32_t *)(codes + ((4 * c4 + k) << bsh) + 4 * g);
-                if (is_new != 0xFFFFFFFFu) {
-                    const uint32_t was = *at;
-                    uint32_t is_old = 0;
-#pragma unroll
-                    for (int e = 0; e < 4; e++)
-                        if (4 * g + e < first) is_old |= 0xFFu << (8 * e);
-                    const uint32_t kept = grow && is_old ? (rescale4<CODE>(was, ratio) & is_old) | (was & ~is_old) : was;
-                    w = (w & is_new) | (kept & ~is_new);
-                }
-                *at = w;
+            for (int d = 1; d < 64; d <<= 1) {
+                const uint32_t other = __shfl_xor(top, d, 64);
+                top = other > top ? other : top;
             }
+            if (lane == 0) wmax[kind][wave] = top;
         }
-    };
+        __syncthreads();
+        uint32_t all[2] = {0, 0};
 #pragma unroll
-    for (int m = 0; m < 2; m++) {
-        int g, c4;
-        place(tid + m * TB < tiles ? tid + m * TB : 0, &g, &c4);
-        if (tid + m * TB < tiles) write(g, c4, held[m]);
+        for (int kind = 0; kind < 2; kind++)
+            for (int w = 0; w < TB / 64; w++) all[kind] = wmax[kind][w] > all[kind] ? wmax[kind][w] : all[kind];
+        amax[0] = all[0], amax[1] = all[1];
+    };
+    largest(false);
+    const bool bad = amax[0] >= 0x7F800000u || amax[1] >= 0x7F800000u;
+    if (bad) {
+        if (tid == 0) atomicOr(a.status, KV_ST_NOT_FINITE);
+        __syncthreads();
+        largest(true);
     }
-    for (int i = tid + 2 * TB; i < tiles; i += TB) {
-        int g, c4;
-        float f[4][4];
-        place(i, &g, &c4);
-        read(g, c4, f);
-        write(g, c4, f);
-    }
-    if (!grow) return;
-    // codes before the first new token, four a dword; a dword of values that has a new token is done
-    const int old_dw = kind == 0 ? first * q4 : g0 * D;
-    for (int i = tid; i < old_dw; i += TB) {
-        uint32_t *w = (uint32_t *)codes + (kind == 0 ? i : (i / g0 << bsh) / 4 + i % g0);
-        *w = rescale4<CODE>(*w, ratio);
+#pragma unroll
+    for (int kind = 0; kind < 2; kind++) {
+        const float top = __builtin_bit_cast(float, amax[kind]);
+        const float now = fmaxf(fmaxf(old[kind], top / qmax<CODE>()), KV_TINY);
+        const float inv = 1.0f / now, ratio = old[kind] / now;
+        const bool grow = first > 0 && now > old[kind];
+        if (tid == 0) (kind ? a.c.vs : a.c.ks)[sat] = now;  // every thread has the old one: they have passed a barrier since
+        uint8_t *const codes = (kind ? a.c.v : a.c.k) + tile;
+        const auto write = [&](int g, int c4, const float (&f)[4][4]) {
+            uint32_t is_new = 0;  // bytes of a dword of four tokens
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                if (4 * g + k >= first && 4 * g + k < last) is_new |= 0xFFu << (8 * k);
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) y[e] = (kind == 0 ? f[k][e] : f[e][k]) * inv;
+                uint32_t w = bad ? kv_f32_codes4<CODE>(y) : kv_f32_codes4<CODE, true>(y);
+                if (kind == 0) {
+                    if (is_new >> (8 * k) & 1u) ((uint32_t *)codes)[((4 * g + k) << qsh) + c4] = w;
+                } else {
+                    uint32_t *at = (uint32_t *)(codes + ((4 * c4 + k) << bsh) + 4 * g);
+                    if (is_new != 0xFFFFFFFFu) {
+                        const uint32_t was = *at;
+                        uint32_t is_old = 0;
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            if (4 * g + e < first) is_old |= 0xFFu << (8 * e);
+                        const uint32_t kept = grow && is_old ? (rescale4<CODE>(was, ratio) & is_old) | (was & ~is_old) : was;
+                        w = (w & is_new) | (kept & ~is_new);
+                    }
+                    *at = w;
+                }
+            }
+        };
+#pragma unroll
+        for (int m = 0; m < HOLD; m++) {
+            int g, c4;
+            place(kind, tid + m * TB < tiles ? tid + m * TB : 0, &g, &c4);
+            if (tid + m * TB < tiles) write(g, c4, held[kind][m]);
+        }
+        for (int i = tid + HOLD * TB; i < tiles; i += TB) {
+            int g, c4;
+            float f[4][4];
+            place(kind, i, &g, &c4);
+            read(kind, g, c4, f);
+            write(g, c4, f);
+        }
+        if (!grow) continue;
+        // codes before the first new token, four a dword; a dword of values that has a new token is done
+        const int old_dw = kind == 0 ? first << qsh : g0 << (qsh + 2);
+        for (int i = tid; i < old_dw; i += TB) {
+            uint32_t *w = (uint32_t *)codes + (kind == 0 ? i : (i / g0 << bsh) / 4 + i % g0);
+            *w = rescale4<CODE>(*w, ratio);
+        }
     }
 }
 
@@ -206,11 +236,14 @@ static int store_in(const KvStoreLaunch &L, hipStream_t s) {
     bool vec = true;
     for (int i = 0; i < 2; i++)
         vec &= (uintptr_t)L.x[i] % (4 * ESZ) == 0 && L.ts[i] % 4 == 0 && L.hs[i] % 4 == 0;
-    const dim3 grid((uint32_t)units, L.c.heads, 2);
-    if (vec)
-        hipLaunchKernelGGL((k_kv_store<CODE, IN, true>), grid, dim3(TB), 0, s, L);
+    const dim3 grid((uint32_t)units, L.c.heads);
+    const bool one = (L.c.dim << L.c.bsh) <= 16 * TB;
+    if (vec && one)
+        hipLaunchKernelGGL((k_kv_store<CODE, IN, true, 1>), grid, dim3(TB), 0, s, L);
+    else if (vec)
+        hipLaunchKernelGGL((k_kv_store<CODE, IN, true, 2>), grid, dim3(TB), 0, s, L);
     else
-        hipLaunchKernelGGL((k_kv_store<CODE, IN, false>), grid, dim3(TB), 0, s, L);
+        hipLaunchKernelGGL((k_kv_store<CODE, IN, false, 2>), grid, dim3(TB), 0, s, L);
     return hipGetLastError() == hipSuccess ? 0 : 9;  // NQ_ERR_HIP
 }
 

@@ -27,21 +27,22 @@ __device__ __forceinline__ void kv_codes4_f32(uint32_t w, float (&f)[4]) {
 }
 
 // Four binary32 values as codes: nearest, ties to even, saturated; NaN is 0.
-template <int CODE>
+// FINITE: there is none.  Signed bytes round by the addition of 1.5 * 2^23,
+// after which the sum's low byte is the nearest integer (ties to even).
+template <int CODE, bool FINITE = false>
 __device__ __forceinline__ uint32_t kv_f32_codes4(const float (&f)[4]) {
+    constexpr float TOP = CODE == KV_Q8 ? 127.0f : 448.0f;
+    float x[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) x[i] = __builtin_amdgcn_fmed3f(FINITE || f[i] == f[i] ? f[i] : 0.0f, -TOP, TOP);
     if constexpr (CODE == KV_Q8) {
-        uint32_t w = 0;
+        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const float x = fminf(fmaxf(f[i] == f[i] ? f[i] : 0.0f, -127.0f), 127.0f);
-            w |= ((uint32_t)(int)rintf(x) & 0xFFu) << (8 * i);
-        }
-        return w;
+        for (int i = 0; i < 4; i++) w[i] = __builtin_bit_cast(uint32_t, x[i] + 12582912.0f);
+        return __builtin_amdgcn_perm(__builtin_amdgcn_perm(w[3], w[2], 0x0C0C0400u),
+                                     __builtin_amdgcn_perm(w[1], w[0], 0x0C0C0400u), 0x05040100u);
     } else {
-        float x[4];
-#pragma unroll
-        for (int i = 0; i < 4; i++) x[i] = fminf(fmaxf(f[i] == f[i] ? f[i] : 0.0f, -448.0f), 448.0f);
-        int w = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
+        const int w = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
         return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], w, true);
     }
 }
