@@ -15,7 +15,9 @@ int launch_kv_attn_e4m3(const KvAttnLaunch &L, hipStream_t s);
 // one and those past its own end return at once.
 //
 // Requests of at most `few` rows go to the kernel for few rows, the others to
-// the one for many.  A piece is `chunk` keys: several pieces a row let few
+// the one for many: measured at 32 requests of 2000 to 4000 keys, few against
+// many at 64 and 128 rows 84 / 105 and 98 / 131 us (64 channels), 119 / 194
+// and 166 / 198 us (128), at 32 and 48 rows 267 / 341 and 358 / 318 us (256).  A piece is `chunk` keys: several pieces a row let few
 // rows fill the card, each costs a workgroup's start and end and a partial
 // output.  Measured for few rows at pieces of 256, 512, 1024, 2048 and 4096
 // keys: 128 ragged requests of up to 8200 keys 127, 99, 86, 82 and 88 us; two
@@ -36,7 +38,7 @@ void kv_attn_plan(KvAttnLaunch &L, uint32_t cus) {
         *chunk = (int32_t)c;
         *splits = (int32_t)((span + c - 1) / c);
     };
-    L.few = 32;
+    L.few = L.c.dim == 256 ? 32 : 128;
     L.waves = 0;
     L.tiles = L.splits = 0;
     L.chunk = 256;

@@ -109,7 +109,7 @@ struct KvDec {
 };
 
 template <int CODE, int DIM, int IN, int TERMS>
-__global__ __launch_bounds__(256, 2) void k_kv_attn_dec(KvAttnArgs args) {
+__global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void k_kv_attn_dec(KvAttnArgs args) {
     using C = KvDec<CODE, DIM, IN, TERMS>;
     constexpr int KT = C::KT, KPG = C::KPG, NT = C::NT, NA = C::NA, ND = C::ND, NB = C::NB;
     extern __shared__ float lds[];
