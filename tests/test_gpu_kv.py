@@ -461,6 +461,21 @@ def test_step_in_a_graph():
         torch.randn(1000, device=DEV).sum().item()
 
 
+@pytest.mark.parametrize("code", ["q8", "e4m3"])
+def test_example_serving_loop(code):
+    """examples/kv_serving.py: no status bit, and the last step is attention over what the cache holds (both sides
+    round to bfloat16's or binary32's precision: within two bfloat16 steps of the largest output)."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "kv_serving.py")
+    spec = importlib.util.spec_from_file_location("kv_serving", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    announce(f"serving loop {code}")
+    problems, worst = example.main(requests=5, steps=12, code=code, prompt=150)
+    assert problems == 0 and worst < 2 * torch.finfo(torch.bfloat16).eps
+
+
 def test_attention_pool_past_32_bits():
     """Blocks whose code offsets pass 2^32 bytes."""
     heads, dim, block = 8, 128, 128
