@@ -15,8 +15,8 @@
 //     query is the sum of two binary16 terms, exact to 2^-24 of an element;
 //   * exp(s_j - m) vs_j / vref, at most 1, times 2^14 is rounded to binary16
 //     (2^-11 of its value), or to two terms for binary32 queries (2^-22).
-//     Weights too small for that precision (below 2^-28 of 1, or 2^-17 in two
-//     terms; a wave sees whether its tile has any) are multiplied up and
+//     Weights too small for that precision (below 2^-28 of 1; a wave sees
+//     whether its tile has any) are multiplied up and
 //     added by products of their own: a channel in which the dominant keys
 //     are 0 keeps the relative precision of what is left;
 //   * maxima, sums, outputs and the block scales stay in binary32, the
@@ -32,13 +32,10 @@ namespace nq {
 constexpr float KV_LOG2E = 1.44269504088896340736f, KV_LN2 = 0.69314718055994530942f;
 constexpr float KV_PSCALE = 16384.0f;  // 2^14
 
-// Weights (times 2^14) below LEAST lose precision in binary16 (in the second
-// term, for two); UP brings the next level to just below 2^14.
-template <int TERMS>
-struct KvLevel {
-    static constexpr float LEAST = TERMS == 1 ? 0x1p-14f : 0x1p-3f;
-    static constexpr float UP = TERMS == 1 ? 0x1p28f : 0x1p17f;
-};
+// Weights (times 2^14) below KV_LEAST lose precision in binary16; KV_UP brings
+// the next level to just below 2^14.  A second term is kept times KV_SECOND,
+// with a sum of its own, so that it keeps its precision as long as the first.
+constexpr float KV_LEAST = 0x1p-14f, KV_UP = 0x1p28f, KV_SECOND = 2048.0f;
 
 struct KvAttnArgs {
     KvAttnLaunch L;
@@ -88,7 +85,7 @@ __device__ __forceinline__ KvReq kv_request(const KvAttnLaunch &a, int r) {
 // maximum, sum and output, and the four are joined at the end.  Codes go from
 // memory to registers in the operands' own order, 16 bytes a lane: nothing is
 // staged, so nothing waits but the loads.  Per KT keys (64; 32 for 256
-// channels) with lane = 16 g + r:
+// channels, and for 128 in two terms) with lane = 16 g + r:
 //   scores  A = keys [16][32 channels]: row r of key tile t is key KT/4 * (r/4)
 //           + 4 t + r%4, channels 64 a + 16 g + 8 b ..+7 for step 2 a + b;
 //           the result gives lane (r = query row, g) the keys KT/4 * g + 4 t + i;
@@ -98,7 +95,7 @@ __device__ __forceinline__ KvReq kv_request(const KvAttnLaunch &a, int r) {
 // The keys of a lane lie in one block, so its scales are two registers.
 template <int CODE, int DIM, int IN, int TERMS>
 struct KvDec {
-    static constexpr int KT = DIM > 128 ? 32 : 64;  // keys of a tile
+    static constexpr int KT = DIM > 128 || (DIM == 128 && TERMS == 2) ? 32 : 64;  // keys of a tile (32: fewer registers)
     static constexpr int KPG = KT / 4;              // keys of a lane
     static constexpr int NT = KT / 16;              // score tiles
     static constexpr int NA = DIM / 64;             // 16-byte loads of a key
@@ -307,7 +304,7 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void k_kv_attn_dec(KvAttnAr
             }
         // O = O * fo + values * weights * ft: all weights at once, or level by level where some are small
         float fo = beta, ft = 1.0f;
-        for (bool slow = __ballot(least < KvLevel<TERMS>::LEAST) != 0;;) {
+        for (bool slow = __ballot(least < KV_LEAST) != 0;;) {
             float rest[NT][4];
             bool more = false;
             if (slow) {
@@ -315,7 +312,7 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void k_kv_attn_dec(KvAttnAr
                 for (int n = 0; n < NT; n++)
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
-                        rest[n][i] = fabsf(x[n][i]) < KvLevel<TERMS>::LEAST ? x[n][i] : 0.0f;
+                        rest[n][i] = fabsf(x[n][i]) < KV_LEAST ? x[n][i] : 0.0f;
                         more |= rest[n][i] != 0.0f;
                         x[n][i] -= rest[n][i];
                     }
@@ -327,30 +324,32 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void k_kv_attn_dec(KvAttnAr
                 for (int i = 0; i < 4; i++) {
                     const _Float16 h = (_Float16)x[n][i];
                     P[0][n >> 1][4 * (n & 1) + i] = h;
-                    if constexpr (TERMS == 2) P[1][n >> 1][4 * (n & 1) + i] = (_Float16)(x[n][i] - (float)h);
+                    if constexpr (TERMS == 2) P[1][n >> 1][4 * (n & 1) + i] = (_Float16)((x[n][i] - (float)h) * KV_SECOND);
                 }
 #pragma unroll
             for (int d = 0; d < ND; d++) {
-                kv_f4 acc = {0, 0, 0, 0};
+                kv_f4 acc = {0, 0, 0, 0}, acc2 = {0, 0, 0, 0};
 #pragma unroll
                 for (int b = 0; b < NB; b++) {
                     // keeps the conversion in this loop: hoisted, the values would hold twice the registers
                     asm volatile("" : "+v"(V[d][b]));
                     const kv_h8 vv = kv_codes8_f16<CODE>(V[d][b]);
-#pragma unroll
-                    for (int e = 0; e < TERMS; e++)
-                        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, P[e][b], acc, 0, 0, 0);
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, P[0][b], acc, 0, 0, 0);
+                    if constexpr (TERMS == 2) acc2 = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, P[1][b], acc2, 0, 0, 0);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; i++) O[d][i] = __builtin_fmaf(O[d][i], fo, acc[i] * ft);
+                for (int i = 0; i < 4; i++) {
+                    const float sum = TERMS == 2 ? __builtin_fmaf(acc2[i], 1.0f / KV_SECOND, acc[i]) : acc[i];
+                    O[d][i] = __builtin_fmaf(O[d][i], fo, sum * ft);
+                }
             }
             if (!slow || !__ballot(more)) break;  // weights are multiples of 2^-149: at most 10 rounds
             fo = 1.0f;
-            ft *= 1.0f / KvLevel<TERMS>::UP;
+            ft *= 1.0f / KV_UP;
 #pragma unroll
             for (int n = 0; n < NT; n++)
 #pragma unroll
-                for (int i = 0; i < 4; i++) x[n][i] = rest[n][i] * KvLevel<TERMS>::UP;
+                for (int i = 0; i < 4; i++) x[n][i] = rest[n][i] * KV_UP;
         }
     }
     l = kv_xor_add(kv_xor_add(l, 16), 32);
@@ -409,16 +408,20 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void k_kv_attn_dec(KvAttnAr
 // ---------------------------------------------------------------------------
 // Joining the pieces of a row
 // ---------------------------------------------------------------------------
-// One workgroup per new token and query head that has more than one piece:
-// out = sum_s 2^(lse_s - max) out_s / sum_s 2^(lse_s - max).
-template <int DIM, int IN>
+// out = sum_s 2^(lse_s - max) out_s / sum_s 2^(lse_s - max) for every new token
+// and query head that has more than one piece.  WAVES waves share a row: one
+// where there are at most 16 pieces (many short rows: 4096 workgroups took 8 us
+// for 128 requests, a quarter of them ended at once), four beyond.
+template <int DIM, int IN, int WAVES>
 __global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs args) {
+    constexpr int PL = DIM / 64;
     __shared__ float so[4][DIM], ssum[4];
     const KvAttnLaunch &a = args.L;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int h = (int)blockIdx.y, tok = (int)blockIdx.x, req = (int)blockIdx.z;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int part = wave % WAVES, tok = (int)blockIdx.x, req = (int)blockIdx.z;
+    const int h = (int)blockIdx.y * (4 / WAVES) + wave / WAVES;
     const KvReq q = kv_request(a, req);
-    if (tok >= q.s1 - q.s0) return;
+    if (tok >= q.s1 - q.s0 || h >= a.q_heads) return;
     const int row = tok * a.group + h % a.group;
     const bool few = (q.s1 - q.s0) * a.group <= a.few;
     const int ROWS = few ? 16 : 32 * a.waves;
@@ -431,44 +434,49 @@ __global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs args) {
     for (int s = lane; s < t.nsplit; s += 64) mm = fmaxf(mm, pl[s]);
     for (int d = 1; d < 64; d <<= 1) mm = kv_xor_max(mm, d);
     const float safe = mm == -__builtin_inff() ? 0.0f : mm;
-    constexpr int PL = DIM / 64;
     float o[PL], sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < PL; i++) o[i] = 0.0f;
-    for (int s0 = wave; s0 < t.nsplit; s0 += 32) {  // eight pieces of this wave on their way at a time
+    for (int s0 = part; s0 < t.nsplit; s0 += 8 * WAVES) {  // eight pieces of this wave on their way at a time
         float w[8], x[8][PL];
 #pragma unroll
         for (int k = 0; k < 8; k++) {
-            const int s = s0 + 4 * k < t.nsplit ? s0 + 4 * k : t.nsplit - 1;
+            const int s = s0 + WAVES * k < t.nsplit ? s0 + WAVES * k : t.nsplit - 1;
             w[k] = pl[s];
 #pragma unroll
             for (int i = 0; i < PL; i++) x[k][i] = po[(int64_t)s * DIM + lane + 64 * i];
         }
 #pragma unroll
         for (int k = 0; k < 8; k++) {
-            if (s0 + 4 * k >= t.nsplit) break;
-            const float e = kv_exp2(w[k] - safe);
+            const float e = s0 + WAVES * k < t.nsplit ? kv_exp2(w[k] - safe) : 0.0f;
             sum += e;
 #pragma unroll
             for (int i = 0; i < PL; i++) o[i] += e * x[k][i];
         }
     }
+    if constexpr (WAVES > 1) {
 #pragma unroll
-    for (int i = 0; i < PL; i++) so[wave][lane + 64 * i] = o[i];
-    if (lane == 0) ssum[wave] = sum;
-    __syncthreads();
-    sum = ssum[0] + ssum[1] + ssum[2] + ssum[3];
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    if (tid < DIM / 4) {
-        float f[4];
+        for (int i = 0; i < PL; i++) so[wave][lane + 64 * i] = o[i];
+        if (lane == 0) ssum[wave] = sum;
+        __syncthreads();  // the whole workgroup has this row
+        if (wave != 0) return;
+        sum = ssum[0] + ssum[1] + ssum[2] + ssum[3];
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int c = 4 * tid + i;
-            f[i] = (so[0][c] + so[1][c] + so[2][c] + so[3][c]) * inv;
-        }
-        kv_write4<IN>(a.out, at * DIM + 4 * tid, f);
+        for (int i = 0; i < PL; i++) o[i] = so[0][lane + 64 * i] + so[1][lane + 64 * i] + so[2][lane + 64 * i] + so[3][lane + 64 * i];
     }
-    if (tid == 0 && a.lse) a.lse[at] = (sum == 0.0f ? -__builtin_inff() : safe + __builtin_amdgcn_logf(sum)) * KV_LN2;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int i = 0; i < PL; i++) {
+        const int64_t c = at * DIM + lane + 64 * i;
+        const float y = o[i] * inv;
+        if constexpr (IN == 0)
+            ((float *)a.out)[c] = y;
+        else if constexpr (IN == 1)
+            ((_Float16 *)a.out)[c] = (_Float16)y;
+        else
+            ((__bf16 *)a.out)[c] = (__bf16)y;
+    }
+    if (lane == 0 && a.lse) a.lse[at] = (sum == 0.0f ? -__builtin_inff() : safe + __builtin_amdgcn_logf(sum)) * KV_LN2;
 }
 
 }  // namespace nq

@@ -359,7 +359,7 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void k_kv_attn_rows(KvA
                     x[i] = e * w;
                     sum += e;
                     P[g][i] = (_Float16)x[i];
-                    big = fmaxf(big, fabsf(x[i]) < KvLevel<1>::LEAST ? fabsf(x[i]) : 0.0f);
+                    big = fmaxf(big, fabsf(x[i]) < KV_LEAST ? fabsf(x[i]) : 0.0f);
                 }
                 l = __builtin_fmaf(sum, unit, l);
                 if (__ballot(big > 0.0f)) {
@@ -368,7 +368,7 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void k_kv_attn_rows(KvA
                     kv_h8 W;
 #pragma unroll
                     for (int i = 0; i < 8; i++) {
-                        const bool is = fabsf(x[i]) < KvLevel<1>::LEAST;
+                        const bool is = fabsf(x[i]) < KV_LEAST;
                         W[i] = (_Float16)(is ? x[i] * up : 0.0f);
                         P[g][i] = is ? (_Float16)0.0f : P[g][i];
                     }
@@ -475,8 +475,11 @@ int launch_kv_attn_dim(const KvAttnLaunch &L, hipStream_t s) {
     if (L.max_splits > 1) {
         // new tokens of a request that can have several pieces
         const int32_t most = L.splits > 1 || L.few / L.group >= L.max_new ? L.max_new : L.few / L.group;
-        const dim3 jgrid((uint32_t)(most < 1 ? 1 : most), (uint32_t)L.q_heads, (uint32_t)L.requests);
-        hipLaunchKernelGGL((k_kv_attn_join<DIM, IN>), jgrid, dim3(256), 0, s, a);
+        const uint32_t tokens = (uint32_t)(most < 1 ? 1 : most), heads = (uint32_t)L.q_heads, reqs = (uint32_t)L.requests;
+        if (L.max_splits <= 16)
+            hipLaunchKernelGGL((k_kv_attn_join<DIM, IN, 1>), dim3(tokens, (heads + 3) / 4, reqs), dim3(256), 0, s, a);
+        else
+            hipLaunchKernelGGL((k_kv_attn_join<DIM, IN, 4>), dim3(tokens, heads, reqs), dim3(256), 0, s, a);
         if (hipGetLastError() != hipSuccess) return 9;  // NQ_ERR_HIP
     }
     return 0;

@@ -52,10 +52,10 @@ EMU_API long nq_kv_emu_units(const int32_t *starts, int requests, const int32_t 
     return bad;
 }
 
-// The addresses of a request and key head in the few-rows attention kernel: keys per lane KT / 4, bytes
-// against the pool, table entries against its width.  visits[key] counts the tile-0 visits of every key.
+// The addresses of a request and key head in the few-rows attention kernel (key tiles of KT): bytes against the
+// pool, table entries against its width.  visits[key] counts the tile-0 visits of every key.
 EMU_API long nq_kv_emu_attention(int added, int length, int cap, int group, int window, int chunk, int max_splits,
-                                 const int32_t *table, int width, int bsh, int dim, int heads, int64_t blocks,
+                                 const int32_t *table, int width, int bsh, int dim, int KT, int heads, int64_t blocks,
                                  int32_t *visits) {
     nq::KvPool c = {};
     c.blocks = blocks;
@@ -63,7 +63,7 @@ EMU_API long nq_kv_emu_attention(int added, int length, int cap, int group, int 
     c.dim = (uint32_t)dim;
     c.bsh = (uint32_t)bsh;
     const int64_t pool = blocks * heads * (int64_t)dim << bsh;
-    const int KT = dim > 128 ? 32 : 64, KPG = KT / 4;
+    const int KPG = KT / 4;
     long bad = 0;
     const HostTable tab = {table, width, &bad};
     for (int tile = 0; tile * 16 < added * group; tile++) {

@@ -35,7 +35,7 @@ def emu():
     L.nq_kv_emu_units.argtypes = [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
                                   ctypes.c_void_p]
     L.nq_kv_emu_attention.restype = ctypes.c_long
-    L.nq_kv_emu_attention.argtypes = [ctypes.c_int] * 7 + [ctypes.c_void_p] + [ctypes.c_int] * 4 + [ctypes.c_int64,
+    L.nq_kv_emu_attention.argtypes = [ctypes.c_int] * 7 + [ctypes.c_void_p] + [ctypes.c_int] * 5 + [ctypes.c_int64,
                                                                                                     ctypes.c_void_p]
     return L
 
@@ -65,9 +65,9 @@ def test_store_units_stay_inside_for_bad_starts(emu, starts):
     assert hits[10] == 0
 
 
-@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("dim, tile", [(64, 64), (128, 64), (128, 32), (256, 32)])
 @pytest.mark.parametrize("bsh", [4, 5, 6, 7])
-def test_attention_reads_inside_the_pool(emu, dim, bsh):
+def test_attention_reads_inside_the_pool(emu, dim, tile, bsh):
     """Every address of a launch lies in the pool and every table index in the row, also for tables that name blocks
     outside the pool; the first tile visits each of its keys once."""
     rng = np.random.default_rng(dim + bsh)
@@ -80,12 +80,12 @@ def test_attention_reads_inside_the_pool(emu, dim, bsh):
         length = int(rng.choice([0, 1, 15, 16, 17, cap, cap + 100, 2 ** 31 - 1, int(rng.integers(1, cap + 1))]))
         added = int(rng.choice([1, 1, 2, 7, 40]))
         group, window = int(rng.choice([1, 3, 4, 16])), int(rng.choice([0, 0, 1, 50, 1000]))
-        chunk = int(rng.choice([256, 512, 1 << 20]))
+        chunk = int(rng.choice([512, 576, 1088, 1 << 20]))
         span = min(cap, window + 16 // group + 2 + 63) if window else cap
         splits = -(-span // chunk)
         visits = np.zeros(cap + 1, np.int32)
         bad = emu.nq_kv_emu_attention(added, length, cap, group, window, chunk, splits, table.ctypes.data, width, bsh,
-                                      dim, heads, blocks, visits.ctypes.data)
+                                      dim, tile, heads, blocks, visits.ctypes.data)
         assert bad == 0, (trial, length, cap, added, group, window, chunk)
         last = min((min(16, added * group) - 1) // group, added - 1)
         end = max(0, min(length, cap, length - added + last + 1))
