@@ -565,6 +565,8 @@ class KvCache:
 
     def __init__(self, k, v, k_scale, v_scale):
         import torch
+        if _I32 is None:
+            _torch_names()
         codes = {torch.int8: "q8", torch.float8_e4m3fn: "e4m3"}
         if k.dtype not in codes or v.dtype != k.dtype:
             raise ValueError("k and v must both be torch.int8 or both torch.float8_e4m3fn")
@@ -601,37 +603,42 @@ class KvCache:
 
 KvStep = collections.namedtuple("KvStep", "lengths token_start slots free_state status")
 
-# A serving step makes these calls once a layer, at a few microseconds each: they take the raw stream, compare device
-# indices, and pass nq_kv_attention_args as packed bytes (the fields of KvAttentionArgs, in its layout).
+# A serving step makes these calls once a layer, at a few microseconds each: they compare dtypes and device indices
+# in one expression (and look for the culprit only when it fails), take the raw stream, and pass
+# nq_kv_attention_args as packed bytes (the fields of KvAttentionArgs, in its layout).
 _ATTENTION_ARGS = struct.Struct("@PqqqqqPPPqqqqqPPif")
 assert _ATTENTION_ARGS.size == ctypes.sizeof(KvAttentionArgs)
+_I32 = _I64 = _F32 = _U8 = _STREAM = None
+_KV_DTYPES = {}
 
 
-_TYPES = {}  # torch dtypes and the raw-stream query, filled by the first call
+def _torch_names():
+    """torch's names that the calls below use, looked up at the first of them."""
+    global _I32, _I64, _F32, _U8, _STREAM
+    import torch
+    _KV_DTYPES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+    _I64, _F32, _U8, _STREAM = torch.int64, torch.float32, torch.uint8, torch._C._cuda_getCurrentRawStream
+    _I32 = torch.int32
 
 
-def _types():
-    if not _TYPES:
-        import torch
-        _TYPES.update(i32=torch.int32, i64=torch.int64, f32=torch.float32, u8=torch.uint8, on=torch.cuda.stream,
-                      handle=torch._C._cuda_getCurrentRawStream, codes={torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
-    return _TYPES
+def _on(stream):
+    """Outputs belong to the stream that the work runs on."""
+    import torch
+    return torch.cuda.stream(stream)
 
 
 def _kv_dtype(dtype):
-    code = _TYPES["codes"].get(dtype)
+    code = _KV_DTYPES.get(dtype)
     return _dtype_code(dtype) if code is None else code
 
 
-def _device_ints(index, dtype, name, t):
-    if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor on CUDA device {index}")
-
-
-def _block_table(table, requests, index, dtype):
-    if table.dtype is not dtype or table.get_device() != index or table.dim() != 2 or table.shape[0] != requests or \
-            table.shape[1] < 1 or table.stride(1) != 1:
-        raise ValueError(f"table must be {dtype} [{requests}, width] on CUDA device {index}, each row contiguous")
+def _refuse(index, table, requests, ints):
+    """Raise for the argument that is not what the call needs: ints are (name, tensor, dtype)."""
+    for name, t, dtype in ints:
+        if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor on CUDA device {index}")
+    if table is not None:
+        raise ValueError(f"table must be {_I32} [{requests}, width] on CUDA device {index}, each row contiguous")
 
 
 def kv_tables(lengths, added, table, ring, free_state, block, tokens, stream=None):
@@ -643,28 +650,30 @@ def kv_tables(lengths, added, table, ring, free_state, block, tokens, stream=Non
     [requests + 1], slots int64 [tokens], free_state, status int32 [1]); nothing changes if status is not 0 (1: too
     few free blocks, 2: a bad length, 4: more than `tokens` new tokens, 8: the ring cannot hold the blocks).
     """
-    t = _types()
-    if stream is not None:  # outputs belong to the stream that the work runs on
-        with t["on"](stream):
+    if _I32 is None:
+        _torch_names()
+    if stream is not None:
+        with _on(stream):
             return kv_tables(lengths, added, table, ring, free_state, block, tokens)
-    i32 = t["i32"]
     if not lengths.is_cuda:
         raise ValueError("lengths must be a CUDA tensor")
-    index = lengths.get_device()
-    n = lengths.numel()
-    _device_ints(index, i32, "lengths", lengths)
-    _device_ints(index, i32, "added", added)
-    _device_ints(index, i32, "ring", ring)
-    _device_ints(index, i32, "free_state", free_state)
-    _block_table(table, n, index, i32)
+    index, n, i32 = lengths.get_device(), lengths.numel(), _I32
+    if not (lengths.dtype is i32 and added.dtype is i32 and ring.dtype is i32 and free_state.dtype is i32 and
+            added.get_device() == index and ring.get_device() == index and free_state.get_device() == index and
+            lengths.is_contiguous() and added.is_contiguous() and ring.is_contiguous() and free_state.is_contiguous() and
+            table.dtype is i32 and table.get_device() == index and table.dim() == 2 and table.shape[0] == n and
+            table.shape[1] > 0 and table.stride(1) == 1):
+        _refuse(index, table, n, (("lengths", lengths, i32), ("added", added, i32), ("ring", ring, i32),
+                                  ("free_state", free_state, i32)))
     if added.numel() != n or free_state.numel() != 2:
         raise ValueError("added must have one entry for each request and free_state two")
     words = lengths.new_empty(2 * n + 4)
-    slots = lengths.new_empty(max(0, tokens), dtype=t["i64"])
+    slots = lengths.new_empty(max(0, tokens), dtype=_I64)
     p = words.data_ptr()
-    st = _lib().nq_kv_tables(lengths.data_ptr(), added.data_ptr(), n, table.data_ptr(), table.shape[1],
-                             table.stride(0), ring.data_ptr(), ring.numel(), free_state.data_ptr(), block, tokens, p,
-                             p + 4 * n, slots.data_ptr(), p + 8 * n + 4, p + 8 * n + 12, t["handle"](index))
+    st = (_LIB or _lib()).nq_kv_tables(
+        lengths.data_ptr(), added.data_ptr(), n, table.data_ptr(), table.shape[1], table.stride(0), ring.data_ptr(),
+        ring.numel(), free_state.data_ptr(), block, tokens, p, p + 4 * n, slots.data_ptr(), p + 8 * n + 4,
+        p + 8 * n + 12, _STREAM(index))
     if st != NQ_OK:
         raise NqError(st, f"{n} requests, table {list(table.shape)}, block {block}, {tokens} tokens")
     new_lengths, token_start, state, status = words.split_with_sizes((n, n + 1, 2, 1))
@@ -684,24 +693,24 @@ def kv_store(cache, k, v, slots, token_start, stream=None):
     into their blocks.  slots: int64 [tokens], token_start: int32 [requests + 1] (as kv_tables returns them).
     Returns status int32 [1]: 1 a value is not finite (NaN is stored as 0, infinities saturate), 2 a slot outside
     the pool or out of order (that block's tokens are not stored)."""
-    t = _types()
     if stream is not None:
-        with t["on"](stream):
+        with _on(stream):
             return kv_store(cache, k, v, slots, token_start)
     _heads_of("k", k, cache, cache.heads)
     _heads_of("v", v, cache, cache.heads)
-    n = k.shape[0]
+    n, index = k.shape[0], cache.index
     if v.dtype is not k.dtype or v.shape[0] != n:
         raise ValueError("k and v must have one type and one number of tokens")
-    _device_ints(cache.index, t["i64"], "slots", slots)
-    _device_ints(cache.index, t["i32"], "token_start", token_start)
+    if not (slots.dtype is _I64 and token_start.dtype is _I32 and slots.get_device() == index and
+            token_start.get_device() == index and slots.is_contiguous() and token_start.is_contiguous()):
+        _refuse(index, None, 0, (("slots", slots, _I64), ("token_start", token_start, _I32)))
     if slots.numel() < n or token_start.numel() < 2:
         raise ValueError("slots needs one entry for each token and token_start one for each request and one more")
     status = token_start.new_empty(1)
     ks, vs = k.stride(), v.stride()
-    st = _lib().nq_kv_store(cache._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], n,
-                            _kv_dtype(k.dtype), slots.data_ptr(), token_start.data_ptr(), token_start.numel() - 1,
-                            status.data_ptr(), t["handle"](cache.index))
+    st = (_LIB or _lib()).nq_kv_store(
+        cache._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], n, _kv_dtype(k.dtype), slots.data_ptr(),
+        token_start.data_ptr(), token_start.numel() - 1, status.data_ptr(), _STREAM(index))
     if st != NQ_OK:
         raise NqError(st, f"k {list(k.shape)} {k.dtype}")
     return status
@@ -709,19 +718,19 @@ def kv_store(cache, k, v, slots, token_start, stream=None):
 
 def kv_load(cache, ids, out_dtype=None, stream=None):
     """Keys and values of whole blocks (ids: int32 [n]), each [n, block, heads, dim] in out_dtype (default float32)."""
-    t = _types()
     if stream is not None:
-        with t["on"](stream):
+        with _on(stream):
             return kv_load(cache, ids, out_dtype)
-    _device_ints(cache.index, t["i32"], "ids", ids)
-    out_dtype = out_dtype or t["f32"]
+    index = cache.index
+    if not (ids.dtype is _I32 and ids.get_device() == index and ids.is_contiguous()):
+        _refuse(index, None, 0, (("ids", ids, _I32),))
+    out_dtype = out_dtype or _F32
     code = _kv_dtype(out_dtype)
     n = ids.numel()
     shape = (n, cache.block, cache.heads, cache.dim)
     k = ids.new_empty(shape, dtype=out_dtype)
     v = ids.new_empty(shape, dtype=out_dtype)
-    st = _lib().nq_kv_load(cache._ref, ids.data_ptr(), n, code, k.data_ptr(), v.data_ptr(),
-                           t["handle"](cache.index))
+    st = (_LIB or _lib()).nq_kv_load(cache._ref, ids.data_ptr(), n, code, k.data_ptr(), v.data_ptr(), _STREAM(index))
     if st != NQ_OK:
         raise NqError(st, f"{n} blocks as {out_dtype}")
     return k, v
@@ -738,16 +747,17 @@ def kv_attention(cache, q, token_start, lengths, table, scale=None, window=0, ma
     bounds save launches of idle workgroups.  Returns out in q's type and shape, and with return_lse also the
     natural logarithms of the sums, float32 [tokens, q_heads].
     """
-    t = _types()
     if stream is not None:
-        with t["on"](stream):
+        with _on(stream):
             return kv_attention(cache, q, token_start, lengths, table, scale, window, max_new, max_length, return_lse)
     _heads_of("q", q, cache)
     n, q_heads, dim = q.shape
-    requests, width, index, i32 = lengths.numel(), table.shape[-1], cache.index, t["i32"]
-    _device_ints(index, i32, "token_start", token_start)
-    _device_ints(index, i32, "lengths", lengths)
-    _block_table(table, requests, index, i32)
+    requests, width, index, i32 = lengths.numel(), table.shape[-1], cache.index, _I32
+    if not (token_start.dtype is i32 and lengths.dtype is i32 and table.dtype is i32 and
+            token_start.get_device() == index and lengths.get_device() == index and table.get_device() == index and
+            token_start.is_contiguous() and lengths.is_contiguous() and table.dim() == 2 and
+            table.shape[0] == requests and width > 0 and table.stride(1) == 1):
+        _refuse(index, table, requests, (("token_start", token_start, i32), ("lengths", lengths, i32)))
     if token_start.numel() != requests + 1:
         raise ValueError("token_start must have one entry more than lengths")
     if max_new is None:
@@ -757,9 +767,9 @@ def kv_attention(cache, q, token_start, lengths, table, scale=None, window=0, ma
     if scale is None:
         scale = dim ** -0.5
     code = _kv_dtype(q.dtype)
-    lib, ref, strides = _lib(), cache._ref, q.stride()
+    lib, ref, strides = _LIB or _lib(), cache._ref, q.stride()
     out = q.new_empty((n, q_heads, dim))
-    lse = q.new_empty((n, q_heads), dtype=t["f32"]) if return_lse else None
+    lse = q.new_empty((n, q_heads), dtype=_F32) if return_lse else None
     args = _ATTENTION_ARGS.pack(q.data_ptr(), strides[0], strides[1], n, q_heads, requests, token_start.data_ptr(),
                                 lengths.data_ptr(), table.data_ptr(), width, table.stride(0), window, max_new,
                                 max_length, out.data_ptr(), lse.data_ptr() if return_lse else 0, code, scale)
@@ -776,8 +786,8 @@ def kv_attention(cache, q, token_start, lengths, table, scale=None, window=0, ma
                 cache._workspaces.clear()
             cache._workspaces[sizes] = need
     if st == NQ_OK:
-        ws = q.new_empty(need, dtype=t["u8"]) if need else None
-        st = lib.nq_kv_attention(ref, args, ws.data_ptr() if need else None, need, t["handle"](index))
+        ws = q.new_empty(need, dtype=_U8) if need else None
+        st = lib.nq_kv_attention(ref, args, ws.data_ptr() if need else None, need, _STREAM(index))
     if st != NQ_OK:
         raise NqError(st, f"q {list(q.shape)} {q.dtype}, {requests} requests, table {list(table.shape)}, "
                           f"window {window}, max_new {max_new}, max_length {max_length}")

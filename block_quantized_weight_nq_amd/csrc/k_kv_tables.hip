@@ -30,7 +30,7 @@ struct Sums {
 
 struct Req {
     int64_t len, add, held, need, give;
-    bool bad;
+    bool bad, ends;
 };
 
 __device__ __forceinline__ Req request(const KvTablesLaunch &a, int r) {
@@ -42,6 +42,7 @@ __device__ __forceinline__ Req request(const KvTablesLaunch &a, int r) {
     q.held = (q.len + T1) >> a.bsh;
     q.need = ((q.len + q.add + T1) >> a.bsh) - q.held;
     q.give = n < 0 ? q.held : 0;
+    q.ends = n < 0;
     q.bad = q.len < 0 || n < -1 || q.len + q.add > ((int64_t)a.width << a.bsh);
     return q;
 }
@@ -56,19 +57,22 @@ __global__ __launch_bounds__(TB) void k_kv_tables(KvTablesLaunch a) {
     __shared__ Sums wsum[TB / 64];
     __shared__ int32_t any_bad, queued;
     __shared__ int32_t m_req[TB], m_held[TB], m_count[TB], m_first[TB];
-    __shared__ int32_t owner[TOK], o_req[TOK], o_start[TOK], o_took[TOK];
+    __shared__ int32_t owner[TOK], o_req[TOK], o_start[TOK], o_took[TOK], o_len[TOK];
     __shared__ int32_t wtop[TB / 64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int R = a.requests, per = (R + TB - 1) / TB;
     const int r0 = tid * per < R ? tid * per : R, r1 = r0 + per < R ? r0 + per : R;
+    const int64_t head = a.state[0], count = a.state[1], ring = a.ring_size;  // on its way with the lengths
     if (tid == 0) any_bad = 0;
+    const Req none = {0, 0, 0, 0, 0, false, false}, own = r0 < r1 ? request(a, r0) : none;  // read once: all of up to TB requests
+    const auto req = [&](int r) { return r == r0 ? own : request(a, r); };
     __syncthreads();
 
     // sums over this thread's requests, then over those of the threads before it
     Sums mine = {0, 0, 0};
     bool bad = false;
     for (int r = r0; r < r1; r++) {
-        const Req q = request(a, r);
+        const Req q = req(r);
         mine.add += q.add;
         mine.need += q.need;
         mine.give += q.give;
@@ -97,7 +101,6 @@ __global__ __launch_bounds__(TB) void k_kv_tables(KvTablesLaunch a) {
         all.need += wsum[w].need;
         all.give += wsum[w].give;
     }
-    const int64_t head = a.state[0], count = a.state[1], ring = a.ring_size;
     const bool no_ring = count < 0 || head < 0 || head >= ring || count - all.need + all.give > ring;
     const uint32_t status = (all.need > count ? KV_ST_NO_BLOCKS : 0u) | (any_bad ? KV_ST_BAD_LENGTH : 0u) |
                             (all.add > a.tokens ? KV_ST_TOKENS : 0u) | (no_ring ? KV_ST_RING : 0u);
@@ -106,9 +109,9 @@ __global__ __launch_bounds__(TB) void k_kv_tables(KvTablesLaunch a) {
     if (blockIdx.x == 0) {
         int64_t s = before.add;
         for (int r = r0; r < r1; r++) {
-            const Req q = request(a, r);
+            const Req q = req(r);
             a.starts[r] = ok ? (int32_t)s : 0;
-            a.lengths_out[r] = (int32_t)(!ok ? q.len : a.added[r] < 0 ? 0 : q.len + q.add);
+            a.lengths_out[r] = (int32_t)(!ok ? q.len : q.ends ? 0 : q.len + q.add);
             s += q.add;
         }
         if (tid == 0) {
@@ -136,7 +139,7 @@ __global__ __launch_bounds__(TB) void k_kv_tables(KvTablesLaunch a) {
             __syncthreads();
             const int r = r0 + k;
             if (r < r1) {
-                const Req q = request(a, r);
+                const Req q = req(r);
                 const int64_t n = pass == 0 ? q.need : q.give;
                 if (n > 0 && (uint32_t)r % G == blockIdx.x) {
                     const int i = atomicAdd(&queued, 1);
@@ -171,13 +174,14 @@ __global__ __launch_bounds__(TB) void k_kv_tables(KvTablesLaunch a) {
         __syncthreads();
         int64_t s = before.add, took = before.need;
         for (int r = r0; r < r1; r++) {
-            const Req q = request(a, r);
+            const Req q = req(r);
             if (q.add > 0 && s < t0 + TOK && s + q.add > t0) {
                 const int p = (int)(s > t0 ? s - t0 : 0);
                 owner[p] = p;
                 o_req[p] = r;
                 o_start[p] = (int32_t)s;
                 o_took[p] = (int32_t)took;
+                o_len[p] = (int32_t)q.len;
             }
             s += q.add;
             took += q.need;
@@ -207,7 +211,7 @@ __global__ __launch_bounds__(TB) void k_kv_tables(KvTablesLaunch a) {
             int64_t slot = -1;
             if (tok < all.add && p >= 0) {
                 const int r = o_req[p];
-                const int64_t len = a.lengths[r];
+                const int64_t len = o_len[p];
                 const int64_t held = (len + (((int64_t)1 << a.bsh) - 1)) >> a.bsh;
                 const int64_t pos = len + tok - o_start[p], col = pos >> a.bsh;
                 const int64_t block = col < held ? a.table[(int64_t)r * a.table_stride + col]

@@ -358,6 +358,42 @@ def test_attention_prompt_in_pieces(dtype):
     run_attention(case, "q8", dtype, 0, f"prompt {dtype}", max_new=150, max_length=1050)
 
 
+@pytest.mark.parametrize("requests", [2, 17, 256, 300])
+def test_attention_many_requests(requests):
+    """Chunks and single tokens of many requests in one call (the longest of up to 256 start first)."""
+    rng = np.random.default_rng(requests)
+    new = [int(rng.choice([1, 1, 1, 3, 140 if r % 16 == 1 else 2])) for r in range(requests)]
+    new[1] = 150
+    past = [int(rng.integers(0, 90)) for _ in new]
+    past[0] = past[-1] = 70
+    case = attention_case(rng, past, new, 1, 1, 64, 16, "q8", "bf16")
+    run_attention(case, "q8", "bf16", 0, f"{requests} requests", max_new=max(new))
+
+
+@pytest.mark.parametrize("code, dim, block", [("q8", 64, 64), ("q8", 128, 16), ("e4m3", 256, 32)])
+def test_attention_chunks_in_a_graph(code, dim, block):
+    """Chunks of changing lengths under one captured call, against the eager calls, bit for bit."""
+    rng = np.random.default_rng(dim)
+    host, q, starts, lengths, table = attention_case(rng, [300, 20, 150], [80, 90, 5], 2, 4, dim, block, code, "f16")
+    cache = upload(*host, code)
+    qd, s, n, t = q.to(DEV), dev(starts), dev(lengths), dev(table)
+    call = lambda: nq.kv_attention(cache, qd, s, n, t, max_new=90, max_length=400, return_lse=True)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = call()
+    for trial in range(4):
+        n.copy_(dev(lengths - np.array([31, 0, 7], np.int32) * trial))
+        s.copy_(dev(np.array([0, 80 - 20 * trial, 170 - 20 * trial, 175 - 20 * trial], np.int32)))
+        eager = call()
+        held[0].fill_(7), held[1].fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(held[0], eager[0]) and torch.equal(held[1], eager[1]), trial
+        torch.randn(1000, device=DEV).sum().item()
+
+
 def test_attention_rows_without_keys():
     """More new tokens than the length, a length of 0, tables without blocks."""
     rng = np.random.default_rng(13)
