@@ -131,7 +131,7 @@ __global__ __launch_bounds__(TB) void k_kv_tables(KvTablesLaunch a) {
     // 32-bit ring arithmetic: ring <= 2^30, first + j < count < 2^31 going in and < ring coming back.
     const int64_t tail = (head + count) % ring;
     // Blocks in (pass 0) and out (pass 1).  The workgroup's requests that have any queue up in LDS, one a thread at a
-    // time, and all threads move their blocks.
+    // time, and each wave moves the blocks of some.
     auto move = [&](int pass) {
         int64_t at = pass == 0 ? before.need : before.give;
         for (int k = 0; k < per; k++) {
@@ -151,14 +151,25 @@ __global__ __launch_bounds__(TB) void k_kv_tables(KvTablesLaunch a) {
                 at += n;
             }
             __syncthreads();
-            for (int i = 0; i < queued; i++) {
+            for (int i = wave; i < queued; i += TB / 64) {
                 int32_t *row = a.table + (int64_t)m_req[i] * a.table_stride;
                 const int held = m_held[i], n = m_count[i], first = m_first[i];
-                for (int j = tid; j < n; j += TB) {
-                    if (pass == 0)
-                        row[held + j] = a.ring[(uint32_t)(head + first + j) % (uint32_t)ring];
-                    else
-                        a.ring[(uint32_t)(tail + first + j) % (uint32_t)ring] = row[j];
+                for (int j0 = lane; j0 < n; j0 += 512) {  // eight blocks a lane on their way
+                    int32_t id[8];
+#pragma unroll
+                    for (int e = 0; e < 8; e++) {
+                        const int j = j0 + 64 * e < n ? j0 + 64 * e : j0;
+                        id[e] = pass == 0 ? a.ring[(uint32_t)(head + first + j) % (uint32_t)ring] : row[j];
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; e++) {
+                        const int j = j0 + 64 * e;
+                        if (j >= n) break;
+                        if (pass == 0)
+                            row[held + j] = id[e];
+                        else
+                            a.ring[(uint32_t)(tail + first + j) % (uint32_t)ring] = id[e];
+                    }
                 }
             }
             __syncthreads();
