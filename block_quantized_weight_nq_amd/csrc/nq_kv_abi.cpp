@@ -17,13 +17,19 @@ int launch_kv_attn_e4m3(const KvAttnLaunch &L, hipStream_t s);
 // Requests of at most `few` rows go to the kernel for few rows, the others to
 // the one for many: measured at 32 requests of 2000 to 4000 keys, few against
 // many at 64 and 128 rows 84 / 105 and 98 / 131 us (64 channels), 119 / 194
-// and 166 / 198 us (128), at 32 and 48 rows 267 / 341 and 358 / 318 us (256).  A piece is `chunk` keys: several pieces a row let few
-// rows fill the card, each costs a workgroup's start and end and a partial
-// output.  Measured for few rows at pieces of 256, 512, 1024, 2048 and 4096
-// keys: 128 ragged requests of up to 8200 keys 127, 99, 86, 82 and 88 us; two
-// of 131001 and about 90000 keys 153, 114, 97, 95 and 92 us; 32 requests
-// with 5 tokens and a window of 2049 keys 37, 33, 32, 38 and 33 us.  Many rows
-// are cut only where the tiles leave compute units idle.
+// and 166 / 198 us (128), at 32 and 48 rows 267 / 341 and 358 / 318 us (256).
+// Binary32 queries stay with few rows: their second terms cost the other
+// kernel its second wave a SIMD.  Built for them too, it measured, few against
+// many at 256 rows of such requests, 152 / 199 us (64 channels) and 256 / 386
+// us (128), and at 2048 tokens of one request 228 / 231 and 554 / 485 us.
+//
+// A piece is `chunk` keys: several pieces a row let few rows fill the card,
+// each costs a workgroup's start and end and a partial output.  Measured for
+// few rows at pieces of 256, 512, 1024, 2048 and 4096 keys: 128 ragged
+// requests of up to 8200 keys 127, 99, 86, 82 and 88 us; two of 131001 and
+// about 90000 keys 153, 114, 97, 95 and 92 us; 32 requests with 5 tokens and a
+// window of 2049 keys 37, 33, 32, 38 and 33 us.  Many rows are cut only where
+// the tiles leave compute units idle.
 void kv_attn_plan(KvAttnLaunch &L, uint32_t cus) {
     const int64_t rows = (int64_t)L.max_new * L.group;
     auto span_of = [&](int64_t tile_rows) {
@@ -42,7 +48,7 @@ void kv_attn_plan(KvAttnLaunch &L, uint32_t cus) {
     L.waves = 0;
     L.tiles = L.splits = 0;
     L.chunk = 256;
-    if (L.dtype == 0) L.few = 1 << 30;  // two terms leave no registers for 32 rows a wave
+    if (L.dtype == 0) L.few = 1 << 30;  // binary32: two terms a row
     if (rows > L.few) {
         L.waves = L.c.dim == 128 ? 8 : 4;
         const int64_t tr = 32 * L.waves;
