@@ -1,0 +1,64 @@
+"""GPU: the 8-bit key/value cache where its inputs or bounds reach the ends of their ranges, against plain
+implementations."""
+import numpy as np
+import pytest
+import torch
+
+import block_quantized_weight_nq_amd as nq
+import kv_ref
+from gpu_util import announce
+from kv_ref import DT
+from test_gpu_kv import DEV, attention_case, dev, upload
+
+pytestmark = pytest.mark.gpu
+TINY = np.float32(2.0 ** -126)  # the scale that the store gives a block of zeros
+
+
+def attend(case, code, dtype, what, window=0, max_new=None, max_length=None, scale=None, ref=None, keys=None):
+    """A call against the reference (kv_ref.attention unless given), within kv_ref.check_attention's bound."""
+    host, q, starts, lengths, table = case
+    dim = host[0].shape[3]
+    scale = dim ** -0.5 if scale is None else scale
+    announce(f"kv_attention {what}")
+    cache = upload(*host, code)
+    out, lse = nq.kv_attention(cache, q.to(DEV), dev(starts), dev(lengths), dev(table), scale=scale, window=window,
+                               max_new=max_new, max_length=max_length, return_lse=True)
+    torch.cuda.synchronize()
+    if ref is None:
+        ref = kv_ref.attention(host, code, q.float().numpy(), starts, lengths, table, float(np.float32(scale)), window,
+                               max_length)
+        if max_new is not None:  # rows past it: no output
+            at = np.concatenate([np.arange(s0 + max_new, s1) for s0, s1 in zip(starts, starts[1:])] + [[]]).astype(int)
+            ref[0][at], ref[1][at], ref[2][at] = 0, -np.inf, 0
+    kv_ref.check_attention(out.double().cpu().numpy(), lse.double().cpu().numpy(), ref, dtype,
+                           int(max(lengths)) if keys is None else keys, dim, what)
+
+
+# dim and heads that leave the rows' keys in one piece or cut them in two of about 20000
+@pytest.mark.parametrize("dim, heads", [(64, 128), (64, 64), (128, 128), (128, 64), (256, 64), (256, 32)])
+@pytest.mark.parametrize("tail", [0, 300])
+@pytest.mark.parametrize("code, dtype", [("q8", "bf16"), ("e4m3", "f16")])
+def test_zero_heads_over_long_contexts(dim, heads, tail, code, dtype):
+    """Keys of zero, and values of zero up to the last `tail` keys: every weight is equal, so a row's output is the
+    mean of its values and lse = ln(keys)."""
+    rng = np.random.default_rng(dim + heads + tail)
+    block, new, length, past_zero = 64, 150, [40000, 39937], 39000 if tail else 40000
+    blocks = 1 + -(-(40000 - past_zero) // block)
+    kc = np.zeros((blocks, heads, block, dim), np.uint8)
+    vc = np.zeros((blocks, heads, dim, block), np.uint8)
+    ks, vs = (np.full((blocks, heads), TINY) for _ in range(2))
+    vc[1:] = rng.integers(0, 100, vc[1:].shape)
+    vs[1:] = rng.uniform(0.01, 0.03, vs[1:].shape).astype(np.float32)
+    first = past_zero // block  # the table entry of the first value that may not be 0
+    row = np.zeros(-(-40000 // block), np.int32)
+    row[first:] = 1 + np.arange(row.size - first)
+    starts = np.array([0, new, 2 * new], np.int32)
+    q = torch.from_numpy(rng.normal(0, 1, (2 * new, heads, dim)).astype(np.float32)).to(DT[dtype])
+    v = kv_ref.code_values(vc[1:], code) * vs[1:].astype(np.float64)[:, :, None, None]
+    sums = np.concatenate([np.zeros((1, heads, dim)), v.transpose(0, 3, 1, 2).reshape(-1, heads, dim).cumsum(0)])
+    seen = np.concatenate([np.arange(n - new, n) + 1 for n in length])
+    out = sums[np.maximum(seen - first * block, 0)] / seen[:, None, None]
+    lse = np.broadcast_to(np.log(seen)[:, None], (2 * new, heads))
+    case = (kc, vc, ks, vs), q, starts, np.array(length, np.int32), np.stack([row, row])
+    attend(case, code, dtype, f"zero heads dim {dim} heads {heads} tail {tail} {code}", max_new=new,
+           ref=(out, lse, out, np.zeros((2 * new, heads))))
