@@ -62,3 +62,19 @@ def test_zero_heads_over_long_contexts(dim, heads, tail, code, dtype):
     case = (kc, vc, ks, vs), q, starts, np.array(length, np.int32), np.stack([row, row])
     attend(case, code, dtype, f"zero heads dim {dim} heads {heads} tail {tail} {code}", max_new=new,
            ref=(out, lse, out, np.zeros((2 * new, heads))))
+
+
+@pytest.mark.parametrize("code, dtype", [("q8", "bf16"), ("e4m3", "f16"), ("q8", "f32")])
+@pytest.mark.parametrize("dim, block", [(64, 64), (128, 16), (256, 32)])
+@pytest.mark.parametrize("window", [0, 45])
+def test_zero_keys_at_the_edge(code, dtype, dim, block, window):
+    """Blocks of zero keys (scale 2^-126) where the mask ends, values as usual, small queries: the factor of their
+    scores is below binary32's range."""
+    rng = np.random.default_rng(dim + window)
+    host, q, starts, lengths, table = attention_case(rng, [90, 7, 0], [150, 133, 1], 2, 2, dim, block, code, dtype,
+                                                     spread=1e-3)
+    for r, n in enumerate(lengths):
+        for j in range(0 if r == 1 else n // block // 2, -(-n // block)):  # the second half, or all
+            host[0][table[r, j]], host[2][table[r, j]] = 0, TINY
+    attend((host, q, starts, lengths, table), code, dtype, f"zero keys {code} {dtype} dim {dim} w {window}", window,
+           max_new=150)
