@@ -52,6 +52,11 @@ __device__ __forceinline__ float kv_row_scale(float amax) {
     return bits_f32((uint32_t)(s > 250 ? 250 : s) << 23);
 }
 
+// A score's factor (row scale times key scale) kept finite: a query row whose channels of 2^127 meet keys of 0 only
+// has scores of 0, not NaN.
+constexpr float KV_MOST = 3.40282346638528859812e38f;
+__device__ __forceinline__ float kv_finite(float x) { return __builtin_amdgcn_fmed3f(x, -KV_MOST, KV_MOST); }
+
 __device__ __forceinline__ float kv_xor_max(float x, int d) { return fmaxf(x, __shfl_xor(x, d, 64)); }
 __device__ __forceinline__ float kv_xor_add(float x, int d) { return x + __shfl_xor(x, d, 64); }
 
@@ -248,7 +253,7 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void k_kv_attn_dec(KvAttnAr
         at_v = ev;
         find(key0 + 8 * KT);
 
-        const float cf = qscale * ks;
+        const float cf = kv_finite(qscale * ks);
         const bool dead = pg < 0;
         const bool edge = key0 < all_lo || key0 + KT > all_hi || __ballot(dead) != 0;
         float top = -__builtin_inff();

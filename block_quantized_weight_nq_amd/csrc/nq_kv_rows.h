@@ -283,19 +283,21 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void k_kv_attn_rows(KvA
         const bool odd = (flags & 2) || !(a.scale > 0.0f) || __ballot(fewest * 0x1p20f < vr1);
         // Otherwise the factor multiplies masked scores of -inf too and has to be positive: one that is too small for
         // binary32 (keys of zero and a small query row) is taken as 2^-126: S is below 2^32, so no score is off by 2^-94.
+        // One that is too large must not turn a score of 0 into NaN (kv_finite).
         float cf[4];
 #pragma unroll
         for (int g = 0; g < 4; g++) cf[g] = qscale * ks[g];
         if (odd) {
 #pragma unroll
             for (int g = 0; g < 4; g++) {
+                cf[g] = kv_finite(cf[g]);
 #pragma unroll
                 for (int i = 0; i < 8; i++) S[g >> 1][8 * (g & 1) + i] *= cf[g];
                 cf[g] = 1.0f;
             }
         } else {
 #pragma unroll
-            for (int g = 0; g < 4; g++) cf[g] = fmaxf(cf[g], KV_TINY);
+            for (int g = 0; g < 4; g++) cf[g] = __builtin_amdgcn_fmed3f(cf[g], KV_TINY, KV_MOST);
         }
         if (key0 < all_lo || key0 + KT > all_hi || (flags & 1)) {
 #pragma unroll

@@ -78,3 +78,17 @@ def test_zero_keys_at_the_edge(code, dtype, dim, block, window):
             host[0][table[r, j]], host[2][table[r, j]] = 0, TINY
     attend((host, q, starts, lengths, table), code, dtype, f"zero keys {code} {dtype} dim {dim} w {window}", window,
            max_new=150)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("new", [3, 150])
+def test_large_factor_of_zero_scores(dtype, new):
+    """A channel in which the queries are huge and every key is zero: scores of 0 times a factor above binary32's
+    range."""
+    rng = np.random.default_rng(new)
+    host, q, starts, lengths, table = attention_case(rng, [100], [new], 2, 1, 64, 16, "q8", dtype)
+    host[0][:, :, :, 5] = 0
+    host[2][:] = 1e9
+    q[:] = 0
+    q[:, :, 5] = 3e38
+    attend((host, q, starts, lengths, table), "q8", dtype, f"large factor {dtype} {new}", max_new=new)
