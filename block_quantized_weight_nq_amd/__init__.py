@@ -744,8 +744,9 @@ def kv_attention(cache, q, token_start, lengths, table, scale=None, window=0, ma
     cache.heads; token_start: int32 [requests + 1]; lengths: int32 [requests], new tokens included; table: int32
     [requests, width].  scale: default dim ** -0.5; window: keys a token sees at most, 0 for all.  max_new and
     max_length bound a request's new tokens and length (default: `tokens` and what the table can name); tight
-    bounds save launches of idle workgroups.  Returns out in q's type and shape, and with return_lse also the
-    natural logarithms of the sums, float32 [tokens, q_heads].
+    bounds save launches of idle workgroups, new tokens past max_new get 0, keys past max_length are not seen.
+    Returns out in q's type and shape, and with return_lse also the natural logarithms of the sums, float32
+    [tokens, q_heads].
     """
     if stream is not None:
         with _on(stream):

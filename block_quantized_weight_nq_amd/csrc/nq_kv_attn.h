@@ -66,19 +66,23 @@ struct KvTableRow {
     __device__ __forceinline__ int operator()(int i) const { return row[i]; }
 };
 
-// A request's token range and length, made safe: starts inside [0, tokens].
+// A request's token range and length, made safe: starts inside [0, tokens].  Of more than max_new new tokens the first
+// max_new are computed, [s0, s1); without the others, up to `end`, the request is one that ends there (len), so the
+// positions stay what they are.
 struct KvReq {
-    int s0, s1, len;
+    int s0, s1, end, len;
 };
 __device__ __forceinline__ KvReq kv_request(const KvAttnLaunch &a, int r) {
     KvReq q;
     q.s0 = a.starts[r];
-    q.s1 = a.starts[r + 1];
+    int s1 = a.starts[r + 1];
     q.len = a.lengths[r];
     q.s0 = q.s0 < 0 ? 0 : q.s0 > a.tokens ? a.tokens : q.s0;
-    q.s1 = q.s1 < q.s0 ? q.s0 : q.s1 > a.tokens ? a.tokens : q.s1;
-    if (q.s1 - q.s0 > a.max_new) q.s1 = q.s0 + a.max_new;
+    s1 = s1 < q.s0 ? q.s0 : s1 > 1 << 30 ? 1 << 30 : s1;  // 2^30 tokens at most: no sum below leaves 32 bits
     if (q.len < 0) q.len = 0;
+    q.end = s1 > a.tokens ? a.tokens : s1;
+    q.s1 = q.end - q.s0 > a.max_new ? q.s0 + a.max_new : q.end;
+    q.len -= s1 - q.s1;
     return q;
 }
 
@@ -121,11 +125,8 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void k_kv_attn_dec(KvAttnAr
     const int tile = (int)(blockIdx.x / a.c.heads), split = (int)blockIdx.y, req = (int)blockIdx.z;
     const int group = a.group;
 
-    if (req == a.requests) {  // tokens of no request: zeros
-        if (split != 0) return;
-        int s = a.starts[a.requests];
-        s = s < 0 ? 0 : s;
-        for (int64_t tok = (int64_t)s + tile; tok < a.tokens; tok += a.tiles_few)
+    auto zeros = [&](int64_t from, int64_t to) {  // outputs of rows that are not computed
+        for (int64_t tok = from + tile; tok < to; tok += a.tiles_few)
             for (int i = tid; i < group * DIM; i += 256) {
                 const int64_t row = tok * a.q_heads + (int64_t)head * group + i / DIM;
                 if constexpr (IN == 0)
@@ -134,9 +135,15 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void k_kv_attn_dec(KvAttnAr
                     ((uint16_t *)a.out)[row * DIM + i % DIM] = 0;
                 if (a.lse && i % DIM == 0) a.lse[row] = -__builtin_inff();
             }
+    };
+    if (req == a.requests) {  // tokens of no request
+        if (split != 0) return;
+        const int s = a.starts[a.requests];
+        zeros(s < 0 ? 0 : s, a.tokens);
         return;
     }
     const KvReq q = kv_request(a, req);
+    if (split == 0 && q.end > q.s1) zeros(q.s1, q.end);
     const int rows = (q.s1 - q.s0) * group;
     if (rows > a.few || tile * 16 >= rows) return;
     const KvTile t = kv_tile(q.s1 - q.s0, q.len, a.cap, group, tile, 16, a.window, a.chunk_few);

@@ -442,7 +442,9 @@ int nq_kv_load(const nq_kv_cache *cache, const int32_t *ids, int64_t n, int32_t 
  * aligned; lse (binary32, [tokens, q_heads]) may be NULL.  Tokens past
  * token_start[requests] get 0 and -inf.
  * max_new and max_length bound the new tokens and the length of every
- * request (rows past them are not computed; keys past them are not seen).
+ * request: of more new tokens the first max_new are computed, at the same
+ * positions, and the others get 0 and -inf; keys from max_length on are not
+ * seen.
  * They and the counts alone set the launch and the workspace, so a captured
  * graph stays valid for other lengths within them.
  * Products are binary16 with binary32 accumulation; queries in binary32 and

@@ -92,3 +92,16 @@ def test_large_factor_of_zero_scores(dtype, new):
     q[:] = 0
     q[:, :, 5] = 3e38
     attend((host, q, starts, lengths, table), "q8", dtype, f"large factor {dtype} {new}", max_new=new)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("group", [1, 4])
+@pytest.mark.parametrize("window", [0, 50])
+@pytest.mark.parametrize("max_new, max_length", [(1, None), (40, None), (200, 150), (200, 1), (140, 333), (60, 171)])
+def test_bounds_below_the_requests(dtype, group, window, max_new, max_length):
+    """max_new and max_length below a request's new tokens and length: the rows within max_new keep their positions,
+    those past it are 0 with a sum of 0, keys from max_length on are not seen."""
+    rng = np.random.default_rng(max_new + window)
+    case = attention_case(rng, [100, 0, 33, 0], [150, 151, 5, 64], 2, group, 64, 32, "q8", dtype, pad=2)
+    attend(case, "q8", dtype, f"bounds {max_new} {max_length} {dtype} group {group} w {window}", window, max_new,
+           max_length)
