@@ -101,7 +101,7 @@ __global__ __launch_bounds__(TB) void k_kv_tables(KvTablesLaunch a) {
         all.need += wsum[w].need;
         all.give += wsum[w].give;
     }
-    const bool no_ring = count < 0 || head < 0 || head >= ring || count - all.need + all.give > ring;
+    const bool no_ring = count < 0 || count > ring || head < 0 || head >= ring || count - all.need + all.give > ring;
     const uint32_t status = (all.need > count ? KV_ST_NO_BLOCKS : 0u) | (any_bad ? KV_ST_BAD_LENGTH : 0u) |
                             (all.add > a.tokens ? KV_ST_TOKENS : 0u) | (no_ring ? KV_ST_RING : 0u);
     const bool ok = status == 0;
@@ -128,7 +128,7 @@ __global__ __launch_bounds__(TB) void k_kv_tables(KvTablesLaunch a) {
     if (solo && blockIdx.x != 0) return;
     const uint32_t G = solo ? 1u : gridDim.x;
 
-    // 32-bit ring arithmetic: ring <= 2^30, first + j < count < 2^31 going in and < ring coming back.
+    // 32-bit ring arithmetic: ring <= 2^30, first + j < count <= ring going in and < ring coming back.
     const int64_t tail = (head + count) % ring;
     // Blocks in (pass 0) and out (pass 1).  The workgroup's requests that have any queue up in LDS, one a thread at a
     // time, and each wave moves the blocks of some.

@@ -105,3 +105,19 @@ def test_bounds_below_the_requests(dtype, group, window, max_new, max_length):
     case = attention_case(rng, [100, 0, 33, 0], [150, 151, 5, 64], 2, group, 64, 32, "q8", dtype, pad=2)
     attend(case, "q8", dtype, f"bounds {max_new} {max_length} {dtype} group {group} w {window}", window, max_new,
            max_length)
+
+
+@pytest.mark.parametrize("count, need", [(15, 12), (15, 5), (11, 1), (2 ** 31 - 1, 11)])
+def test_tables_refuse_a_count_above_the_ring(count, need):
+    """More free blocks than a ring of 10 holds cannot be: status 8 and nothing changes, whatever the step takes."""
+    ring = np.arange(10, dtype=np.int32)
+    table = np.full((2, 12), -1, np.int32)
+    added = np.array([need * 16 - 32, 20], np.int32) if need > 2 else np.array([0, 16], np.int32)
+    announce(f"kv_tables count {count} need {need}")
+    t, g = dev(table), dev(ring)
+    step = nq.kv_tables(dev(np.zeros(2, np.int32)), dev(added), t, g, dev(np.array([3, count], np.int32)), 16, 200)
+    torch.cuda.synchronize()
+    assert int(step.status) == 8
+    assert np.array_equal(t.cpu().numpy(), table) and np.array_equal(g.cpu().numpy(), ring)
+    assert step.lengths.tolist() == [0, 0] and step.token_start.tolist() == [0, 0, 0]
+    assert step.free_state.tolist() == [3, count] and bool((step.slots == -1).all())
