@@ -162,8 +162,10 @@ struct KvAttnLaunch {
     int64_t table_stride;
     void *out;           // [tokens, q_heads, dim], contiguous
     float *lse;          // [tokens, q_heads] or NULL
-    float *part;         // normalized outputs of the pieces, [tokens, q_heads, max_splits, dim]
-    float *part_lse;     // their base-2 logarithms of the sums, [tokens, q_heads, max_splits]
+    float *part;         // normalized outputs of the many-rows kernel's pieces, [tokens, q_heads, splits, dim]
+    float *part_lse;     // their base-2 logarithms of the sums, [tokens, q_heads, splits]
+    float *few_part;     // likewise of the few-rows kernel, rows as kv_few_row has them, splits_few
+    float *few_part_lse;
     int32_t tokens, requests, q_heads, group;
     int32_t cap;         // keys a request can have: max_length, and what its table row can name
     int32_t max_new, window;
@@ -176,9 +178,19 @@ struct KvAttnLaunch {
     int32_t tiles, tiles_few;    // tiles of a request and key head, at most
     int32_t chunk, chunk_few;    // keys of a piece
     int32_t splits, splits_few;  // pieces of a tile, at most
-    int32_t max_splits;          // the larger of them: the stride of the pieces
+    int32_t few_tokens;  // new tokens of a request that the few-rows kernel can have, or 0: see kv_few_row
 };
+// The place of a row's pieces among the few-rows kernel's: every request has few_tokens * q_heads places, where that
+// is less than one for each row of the call (a prompt's rows take none), or (few_tokens = 0) its own rows' places.
+NQ_HD int64_t kv_few_row(const KvAttnLaunch &a, int req, int start, int tok, int head) {
+    const int64_t at = a.few_tokens > 0 ? (int64_t)req * a.few_tokens : (int64_t)start;
+    return (at + tok) * a.q_heads + head;
+}
+NQ_HD uint64_t kv_part_rows(const KvAttnLaunch &a) { return a.splits > 1 ? (uint64_t)a.tokens * (uint64_t)a.q_heads : 0u; }
+NQ_HD uint64_t kv_few_part_rows(const KvAttnLaunch &a) {
+    if (a.splits_few <= 1) return 0;
+    return (a.few_tokens > 0 ? (uint64_t)a.requests * (uint64_t)a.few_tokens : (uint64_t)a.tokens) * (uint64_t)a.q_heads;
+}
 void kv_attn_plan(KvAttnLaunch &L, uint32_t cus);
-int launch_kv_attn(const KvAttnLaunch &L, hipStream_t s);
 
 }  // namespace nq

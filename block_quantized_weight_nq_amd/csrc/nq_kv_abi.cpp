@@ -71,7 +71,9 @@ void kv_attn_plan(KvAttnLaunch &L, uint32_t cus) {
     int64_t pieces = busy > 0 ? (6ll * cus + busy - 1) / busy : 1;
     if (L.tiles_few <= 4 && pieces < (span + 2047) / 2048) pieces = (span + 2047) / 2048;
     cut(span, pieces, 512, &L.chunk_few, &L.splits_few);
-    L.max_splits = L.splits > L.splits_few ? L.splits : L.splits_few;
+    const int64_t most = L.few / L.group < L.max_new ? L.few / L.group : L.max_new;
+    if (most == 0) L.splits_few = 1;  // a single token has more rows than the few-rows kernel takes
+    L.few_tokens = most * L.requests < L.tokens ? (int32_t)most : 0;
 }
 }  // namespace nq
 
@@ -141,8 +143,7 @@ int check_attention(const nq_kv_cache *cache, const nq_kv_attention_args *x, nq:
 }
 
 uint64_t attention_workspace(const nq::KvAttnLaunch &L) {
-    if (L.max_splits <= 1) return 0;
-    const uint64_t pieces = (uint64_t)L.tokens * (uint64_t)L.q_heads * (uint64_t)L.max_splits;
+    const uint64_t pieces = nq::kv_part_rows(L) * (uint64_t)L.splits + nq::kv_few_part_rows(L) * (uint64_t)L.splits_few;
     return pieces * 4 * ((uint64_t)L.c.dim + 1);
 }
 
@@ -272,7 +273,12 @@ NQ_API int nq_kv_attention(const nq_kv_cache *cache, const nq_kv_attention_args 
     L.table = args->table;
     L.out = args->out;
     L.lse = args->lse;
-    L.part = (float *)workspace;
-    L.part_lse = need ? L.part + (uint64_t)L.tokens * (uint64_t)L.q_heads * (uint64_t)L.max_splits * L.c.dim : nullptr;
+    const uint64_t many = nq::kv_part_rows(L) * (uint64_t)L.splits, few = nq::kv_few_part_rows(L) * (uint64_t)L.splits_few;
+    if (need > 0) {
+        L.part = (float *)workspace;
+        L.few_part = L.part + many * L.c.dim;
+        L.part_lse = L.few_part + few * L.c.dim;
+        L.few_part_lse = L.part_lse + many;
+    }
     return L.code == NQ_KV_Q8 ? nq::launch_kv_attn_q8(L, stream) : nq::launch_kv_attn_e4m3(L, stream);
 }

@@ -410,10 +410,10 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void k_kv_attn_dec(KvAttnAr
         }
         if (a.lse && c0 == 0) a.lse[oat] = lse2 * KV_LN2;
     } else {
-        float *part = a.part + (oat * a.max_splits + split) * DIM + c0;
+        const int64_t pat = kv_few_row(a, req, q.s0, otok, oh) * a.splits_few + split;
 #pragma unroll
-        for (int i = 0; i < ND; i++) part[i] = res[i];
-        if (c0 == 0) a.part_lse[oat * a.max_splits + split] = lse2;
+        for (int i = 0; i < ND; i++) a.few_part[pat * DIM + c0 + i] = res[i];
+        if (c0 == 0) a.few_part_lse[pat] = lse2;
     }
 }
 
@@ -440,8 +440,9 @@ __global__ __launch_bounds__(256) void k_kv_attn_join(KvAttnArgs args) {
     const KvTile t = kv_tile(q.s1 - q.s0, q.len, a.cap, a.group, row / ROWS, ROWS, a.window, few ? a.chunk_few : a.chunk);
     if (t.nsplit == 1) return;
     const int64_t at = (int64_t)(q.s0 + tok) * a.q_heads + h;
-    const float *pl = a.part_lse + at * a.max_splits;
-    const float *po = a.part + at * a.max_splits * DIM;
+    const int64_t pat = few ? kv_few_row(a, req, q.s0, tok, h) * a.splits_few : at * a.splits;
+    const float *pl = (few ? a.few_part_lse : a.part_lse) + pat;
+    const float *po = (few ? a.few_part : a.part) + pat * DIM;
     float mm = -__builtin_inff();
     for (int s = lane; s < t.nsplit; s += 64) mm = fmaxf(mm, pl[s]);
     for (int d = 1; d < 64; d <<= 1) mm = kv_xor_max(mm, d);

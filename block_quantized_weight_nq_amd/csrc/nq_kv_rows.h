@@ -456,7 +456,7 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void k_kv_attn_rows(KvA
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const float lse2 = l == 0.0f ? -__builtin_inff() : (m == -__builtin_inff() ? 0.0f : m) + __builtin_amdgcn_logf(l / unit);
     const int64_t oat = (int64_t)(q.s0 + tok) * a.q_heads + (int64_t)head * group + row % group;
-    const int64_t pat = oat * a.max_splits + split;
+    const int64_t pat = oat * a.splits + split;
 #pragma unroll
     for (int d = 0; d < ND; d++)
 #pragma unroll
@@ -495,11 +495,12 @@ int launch_kv_attn_dim(const KvAttnLaunch &L, hipStream_t s) {
     constexpr uint32_t lds = KvDec<CODE, DIM, IN, TERMS>::LDS_FLOATS * 4;
     hipLaunchKernelGGL((k_kv_attn_dec<CODE, DIM, IN, TERMS>), grid, dim3(256), lds, s, a);
     if (hipGetLastError() != hipSuccess) return 9;  // NQ_ERR_HIP
-    if (L.max_splits > 1) {
+    const int32_t most_splits = L.splits > L.splits_few ? L.splits : L.splits_few;
+    if (most_splits > 1) {
         // new tokens of a request that can have several pieces
         const int32_t most = L.splits > 1 || L.few / L.group >= L.max_new ? L.max_new : L.few / L.group;
         const uint32_t tokens = (uint32_t)(most < 1 ? 1 : most), heads = (uint32_t)L.q_heads, reqs = (uint32_t)L.requests;
-        if (L.max_splits <= 16)
+        if (most_splits <= 16)
             hipLaunchKernelGGL((k_kv_attn_join<DIM, IN, 1>), dim3(tokens, (heads + 3) / 4, reqs), dim3(256), 0, s, a);
         else
             hipLaunchKernelGGL((k_kv_attn_join<DIM, IN, 4>), dim3(tokens, heads, reqs), dim3(256), 0, s, a);

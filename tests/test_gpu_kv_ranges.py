@@ -121,3 +121,13 @@ def test_tables_refuse_a_count_above_the_ring(count, need):
     assert np.array_equal(t.cpu().numpy(), table) and np.array_equal(g.cpu().numpy(), ring)
     assert step.lengths.tolist() == [0, 0] and step.token_start.tolist() == [0, 0, 0]
     assert step.free_state.tolist() == [3, count] and bool((step.slots == -1).all())
+
+
+@pytest.mark.parametrize("code, dtype, dim", [("q8", "bf16", 64), ("e4m3", "f16", 128)])
+@pytest.mark.parametrize("window", [0, 1500])
+def test_pieces_beside_a_chunk(code, dtype, dim, window):
+    """Few rows over several pieces in a call whose chunk has more tokens than the few-rows kernel takes: the pieces
+    have a place for each request's few tokens, not for each token of the call."""
+    rng = np.random.default_rng(dim + window)
+    case = attention_case(rng, [2300, 1900, 20, 3100], [1, 60, 16, 2], 1, 8, dim, 32, code, dtype, holes=2)
+    attend(case, code, dtype, f"pieces beside a chunk {code} {dtype} w {window}", window, max_new=60)
