@@ -72,10 +72,18 @@ __global__ __launch_bounds__(TB) void k_kv_store(KvStoreLaunch a) {
     const int64_t u = blockIdx.x, T = (int64_t)1 << a.c.bsh, n = a.tokens;
     const int bsh = (int)a.c.bsh, q4 = (int)a.c.dim / 4, qsh = __builtin_ctz(q4);  // dim is a power of two
 
-    // the request of this unit
+    // the request of this unit, among TB of them at the end
     if (tid == 0) found[0] = -1;
+    int32_t from = 0, left = a.requests;
+    while (left > TB) {
+        const int32_t step = kv_probe_step(left, TB), i = from + tid * step;
+        const int hits = __syncthreads_count(tid * step < left && kv_unit_first(a.starts[i], i, a.c.bsh) <= u);
+        if (hits == 0) return;
+        kv_narrow(&from, &left, step, hits);
+    }
     __syncthreads();
-    for (int i = tid; i < a.requests; i += TB) {
+    if (tid < left) {
+        const int i = from + tid;
         const int32_t s0 = a.starts[i], s1 = a.starts[i + 1];
         if (kv_unit_first(s0, i, a.c.bsh) <= u && u < kv_unit_first(s1, i + 1, a.c.bsh)) {
             found[0] = i;

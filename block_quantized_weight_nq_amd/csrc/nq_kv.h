@@ -45,6 +45,16 @@ NQ_HD int64_t kv_tile_at(const KvPool &c, int64_t block, uint32_t head) {
 // up to those of request r + 1: the launch needs no host copy of the starts.
 NQ_HD int64_t kv_unit_first(int64_t start, int64_t r, uint32_t bsh) { return (start >> bsh) + 2 * r; }
 
+// The request of a unit, among requests [lo, lo + n), by a workgroup: its threads look at every step-th of them; `hits`
+// have a first unit at or before this one (the starts are sorted, so these are the first), and the request is the last of
+// them or one of those up to the next that was looked at.  Whatever the starts are, [lo, lo + n) stays inside itself.
+NQ_HD int32_t kv_probe_step(int32_t n, int32_t threads) { return (n - 1) / threads + 1; }
+NQ_HD void kv_narrow(int32_t *lo, int32_t *n, int32_t step, int32_t hits) {
+    const int32_t skip = (hits - 1) * step;
+    *lo += skip;
+    *n = *n - skip < step ? *n - skip : step;
+}
+
 // Tokens [lo, hi) of unit j of a request whose tokens are [s0, s1) and whose
 // first one sits at offset off0 of its block.
 NQ_HD void kv_unit_tokens(int64_t s0, int64_t s1, int64_t j, int64_t off0, uint32_t bsh, int64_t *lo, int64_t *hi) {

@@ -131,3 +131,43 @@ def test_pieces_beside_a_chunk(code, dtype, dim, window):
     rng = np.random.default_rng(dim + window)
     case = attention_case(rng, [2300, 1900, 20, 3100], [1, 60, 16, 2], 1, 8, dim, 32, code, dtype, holes=2)
     attend(case, code, dtype, f"pieces beside a chunk {code} {dtype} w {window}", window, max_new=60)
+
+
+@pytest.mark.parametrize("requests, filled", [(257, 257), (1000, 1000), (70000, 70000), (1 << 20, 3000)])
+def test_store_of_many_requests(requests, filled):
+    """One call for all requests stores what calls of 200 requests store."""
+    rng = np.random.default_rng(requests)
+    heads, dim, block = 1, 64, 16
+    new = np.zeros(requests, np.int64)
+    new[rng.permutation(requests)[:filled]] = rng.choice([0, 1, 1, 1, 2, 17], filled)
+    starts = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    n = int(starts[-1])
+    at = rng.permutation(2 * filled)  # two blocks for each request that may have tokens
+    first = np.zeros(requests, np.int64)
+    first[np.nonzero(new)[0]] = np.arange(np.count_nonzero(new))
+    off = rng.integers(0, block, requests)
+    r = np.repeat(np.arange(requests), new)
+    pos = off[r] + np.arange(n) - starts[r]  # 15 + 17 tokens at most
+    slots = at[2 * first[r] + pos // block] * block + pos % block
+    k, v = (torch.randn((n, heads, dim), device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    caches = []
+    for _ in range(2):
+        c = nq.KvCache.empty(2 * filled, heads, block, dim, "q8", DEV)
+        for x in (c.k, c.v, c.k_scale, c.v_scale):
+            x.fill_(1)
+        caches.append(c)
+    announce(f"kv_store of {requests} requests, {n} tokens")
+    s, t = dev(slots.astype(np.int64)), dev(starts)
+    status = nq.kv_store(caches[0], k, v, s, t)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    used = np.nonzero(new)[0]
+    for i in range(0, used.size, 200):
+        part = used[i:i + 200]
+        a, b = int(starts[part[0]]), int(starts[part[-1] + 1])
+        own = np.concatenate([[0], np.cumsum(new[part])]).astype(np.int32)
+        nq.kv_store(caches[1], k[a:b], v[a:b], s[a:b], dev(own))
+    torch.cuda.synchronize()
+    for x, y in zip((caches[0].k, caches[0].v, caches[0].k_scale, caches[0].v_scale),
+                    (caches[1].k, caches[1].v, caches[1].k_scale, caches[1].v_scale)):
+        assert torch.equal(x, y)
