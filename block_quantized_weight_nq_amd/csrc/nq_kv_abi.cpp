@@ -80,6 +80,7 @@ void kv_attn_plan(KvAttnLaunch &L, uint32_t cus) {
 namespace {
 
 constexpr int64_t MAX_LEN = 1ll << 30;
+constexpr int64_t MAX_GROUPS = (1ll << 24) - 1;  // of 256 threads: a grid has less than 2^32 threads along an axis
 
 int check_cache(const nq_kv_cache *c, nq::KvPool *p) {
     if (!c) return NQ_ERR_NULL_ARG;
@@ -137,8 +138,9 @@ int check_attention(const nq_kv_cache *cache, const nq_kv_attention_args *x, nq:
     L->code = cache->code;
     L->dtype = x->dtype;
     L->scale = x->scale;
-    if (((int64_t)L->max_new * L->group / 16 + 1) * cache->heads >= (1ll << 31)) return NQ_ERR_OVERFLOW;
     nq::kv_attn_plan(*L, nq::device_compute_units());
+    if ((int64_t)L->tiles_few * cache->heads > MAX_GROUPS || (int64_t)L->tiles * L->waves * cache->heads > 4 * MAX_GROUPS)
+        return NQ_ERR_OVERFLOW;
     return NQ_OK;
 }
 
@@ -199,6 +201,7 @@ NQ_API int nq_kv_store(const nq_kv_cache *cache, const void *k, int64_t k_token_
         bad_stride(v_token_stride, tokens) || bad_stride(k_head_stride, cache->heads) ||
         bad_stride(v_head_stride, cache->heads))
         return NQ_ERR_OVERFLOW;
+    if (nq::kv_unit_first(tokens, requests, L.c.bsh) > MAX_GROUPS) return NQ_ERR_OVERFLOW;
     if (!status || !token_start || (tokens > 0 && (!k || !v || !slots))) return NQ_ERR_NULL_ARG;
     const uintptr_t esz = (uintptr_t)element_size(in_dtype);
     if ((uintptr_t)k % esz || (uintptr_t)v % esz || (uintptr_t)slots % 8 || (uintptr_t)token_start % 4 ||
@@ -227,7 +230,7 @@ NQ_API int nq_kv_load(const nq_kv_cache *cache, const int32_t *ids, int64_t n, i
     if (st != NQ_OK) return st;
     if (bad_dtype(out_dtype)) return NQ_ERR_BAD_DTYPE;
     if (n < 0) return NQ_ERR_BAD_DIM;
-    if (n >= (1ll << 31)) return NQ_ERR_OVERFLOW;
+    if (n > MAX_GROUPS) return NQ_ERR_OVERFLOW;
     if (n == 0) return NQ_OK;
     if (!ids || !k_out || !v_out) return NQ_ERR_NULL_ARG;
     if ((uintptr_t)ids % 4 || (uintptr_t)k_out % 16 || (uintptr_t)v_out % 16) return NQ_ERR_MISALIGNED;

@@ -418,7 +418,8 @@ int nq_kv_tables(const int32_t *lengths, const int32_t *added, int64_t requests,
  *   RN32(code * RN32(s / s')).
  * status is cleared on the stream, then ORed with 1 for a non-finite value
  * and 2 for slots outside the pool or not consecutive: those tokens of that
- * block are not stored.  Tokens past token_start[requests] are ignored. */
+ * block are not stored.  Tokens past token_start[requests] are ignored.
+ * tokens / block + 2 * requests < 2^24 (NQ_ERR_OVERFLOW). */
 int nq_kv_store(const nq_kv_cache *cache, const void *k, int64_t k_token_stride, int64_t k_head_stride,
                 const void *v, int64_t v_token_stride, int64_t v_head_stride, int64_t tokens, int32_t in_dtype,
                 const int64_t *slots, const int32_t *token_start, int64_t requests, uint32_t *status,
@@ -426,7 +427,7 @@ int nq_kv_store(const nq_kv_cache *cache, const void *k, int64_t k_token_stride,
 
 /* nq_kv_load: the values of n whole blocks, k_out and v_out [n, block, heads,
  * dim], rounded once to out_dtype.  An id outside the pool gives zeros.
- * Outputs are 16-byte aligned. */
+ * Outputs are 16-byte aligned, n < 2^24 (NQ_ERR_OVERFLOW). */
 int nq_kv_load(const nq_kv_cache *cache, const int32_t *ids, int64_t n, int32_t out_dtype, void *k_out,
                void *v_out, hipStream_t stream);
 
@@ -452,7 +453,8 @@ int nq_kv_load(const nq_kv_cache *cache, const int32_t *ids, int64_t n, int32_t 
  * order of sums is fixed by the shapes: repeated calls give identical bits.
  * Checks beyond the cache's: 1 <= requests <= 65534, q_heads a multiple of
  * heads, max_new, max_length, table_width >= 1, window >= 0, scale finite
- * (NQ_ERR_BAD_DIM); q_heads <= 65535 and tokens * q_heads <= 2^30
+ * (NQ_ERR_BAD_DIM); q_heads <= 65535, tokens * q_heads <= 2^30 and, for
+ * binary32, heads * ceil(max_new * (q_heads / heads) / 16) < 2^24
  * (NQ_ERR_OVERFLOW).  nq_kv_attention_workspace gives the bytes of device
  * memory (16-byte aligned, not used by another call until this one's work is
  * done) that the call needs, 0 for many; fewer are refused (NQ_ERR_SCRATCH). */

@@ -100,3 +100,24 @@ def test_workspace_of_a_mixed_step(dim, heads, group):
     few = min(128 // group, 8192)
     st, need = workspace(15 + 8192, 16, 8192, 131072, heads, group, dim)
     assert st == 0 and single > 0 and need <= few * single
+
+
+def test_sizes_past_the_launch_are_refused():
+    """A grid holds less than 2^32 threads along an axis: sizes that need more are refused as such (7), not launched."""
+    buf = np.zeros(64, np.uint32)
+    p = (buf.ctypes.data + 15) // 16 * 16
+    L = nq.library()
+    d = nq.KvCacheDesc(0, 1, 64, 16, 1000, p, p, p, p)
+    ref = ctypes.byref(d)
+    store = lambda tokens, requests: L.nq_kv_store(  # noqa: E731  (no token starts: 1 where the sizes are in order)
+        ref, p, 64, 64, p, 64, 64, tokens, 0, p, None, requests, p, None)
+    assert store(1, 1 << 23) == 7 and store(31, (1 << 23) - 1) == 1 and store(32, (1 << 23) - 1) == 7
+    assert store((1 << 28) - 48, 1) == 1 and store((1 << 28) - 32, 1) == 7
+    load = lambda n: L.nq_kv_load(ref, None, n, 0, p, p, None)  # noqa: E731
+    assert load((1 << 24) - 1) == 1 and load(1 << 24) == 7
+    for heads, group in ((1, 1), (2, 1), (1, 4)):
+        most = (1 << 28) // (heads * group)  # its tiles of 16 rows: 2^24 / heads a head
+        size = dict(max_length=1 << 16, heads=heads, group=group, dim=64)
+        assert workspace(most, 1, most, dtype=0, **size)[0] == 7
+        assert workspace(most - 16, 1, most - 16, dtype=0, **size)[0] == 0
+        assert workspace(most, 1, most, dtype=1, **size)[0] == 0
