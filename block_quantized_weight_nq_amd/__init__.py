@@ -8,6 +8,7 @@ and streams.  There is no fallback: if libnq.so is missing, every call raises.
     y = nq.dequantize_packed("gguf:q4_k", payload_u8_cuda, [4096, 4096], torch.bfloat16)
 """
 import collections
+import contextlib
 import ctypes
 import os
 import struct
@@ -248,20 +249,23 @@ def dequantize_packed_many(items, out_dtype=None, stream=None):
     where out is not given), decoded on `stream` (default: the current stream).
     """
     import torch
-    descs, outs = [], []
+    descs, outs, on = [], [], _SAME_DEVICE
     for it in items:
         fmt, payload, shape = it[0], it[1], it[2]
         out = it[3] if len(it) > 3 else None
         fid = fmt if isinstance(fmt, int) else format_query(fmt).id
         code, out, stream = _prepare(payload, shape, out_dtype if out_dtype is not None else
                                      (out.dtype if out is not None else torch.float32), out, stream)
+        if not descs:
+            on = _device_of(payload)
         descs.append((fid, payload.data_ptr(), payload.numel(), shape, out.data_ptr()))
         outs.append(out)
     if stream is None:
         stream = torch.cuda.current_stream()
     if out_dtype is None:
         out_dtype = outs[0].dtype if outs else torch.float32
-    st, failed = dequantize_packed_many_raw(descs, _dtype_code(out_dtype), stream.cuda_stream)
+    with on:
+        st, failed = dequantize_packed_many_raw(descs, _dtype_code(out_dtype), stream.cuda_stream)
     if st != NQ_OK:
         raise NqError(st, f"tensor {failed}")
     return outs
@@ -295,6 +299,18 @@ def dequantize_nvfp4_stacked_raw(payload_ptr, nbytes, shape, divisors, out_dtype
                                               ctypes.c_void_p(stream_handle))
 
 
+_SAME_DEVICE = contextlib.nullcontext()
+
+
+def _device_of(t):
+    """A context in which the CUDA tensor's device is the current one: a launch on a default stream goes to the current
+    device's, and a launch plan asks that device's size."""
+    import torch
+    if not t.is_cuda or torch._C._cuda_getDevice() == t.get_device():
+        return _SAME_DEVICE
+    return torch.cuda.device(t.get_device())
+
+
 def _prepare(payload, shape, out_dtype, out, stream):
     import torch
     if out_dtype is None:
@@ -321,8 +337,9 @@ def dequantize_nvfp4_stacked(payload, shape, divisors, out_dtype=None, out=None,
     """Decode an "nvfp4" plane stacked from `divisors` sources (one binary32
     divisor per source after the blocks) into a new (or the given) tensor."""
     code, out, stream = _prepare(payload, shape, out_dtype, out, stream)
-    st = dequantize_nvfp4_stacked_raw(payload.data_ptr(), payload.numel(), shape, divisors, code,
-                                      out.data_ptr(), stream.cuda_stream)
+    with _device_of(payload):
+        st = dequantize_nvfp4_stacked_raw(payload.data_ptr(), payload.numel(), shape, divisors, code,
+                                          out.data_ptr(), stream.cuda_stream)
     if st != NQ_OK:
         raise NqError(st, f"nvfp4 {list(shape)} divisors={divisors}")
     return out
@@ -350,8 +367,9 @@ def dequantize_fp8_row(fmt, payload, shape, out_dtype=None, out=None, stream=Non
     """Decode a row-scaled FP8 matrix ("fp8_e4m3fn_row_bf16" or "_fp16":
     N*K codes, then N scale words) into a new (or the given) [N, K] tensor."""
     code, out, stream = _prepare(payload, shape, out_dtype, out, stream)
-    st = dequantize_fp8_row_raw(FP8_ROW_KINDS[fmt], payload.data_ptr(), payload.numel(), shape, code,
-                                out.data_ptr(), stream.cuda_stream)
+    with _device_of(payload):
+        st = dequantize_fp8_row_raw(FP8_ROW_KINDS[fmt], payload.data_ptr(), payload.numel(), shape, code,
+                                    out.data_ptr(), stream.cuda_stream)
     if st != NQ_OK:
         raise NqError(st, f"{fmt} {list(shape)}")
     return out
@@ -391,8 +409,9 @@ def quantize_grouped_absmax(scheme, x, stream=None, check=True):
     status = torch.empty(1, dtype=torch.int32, device=x.device)
     if stream is None:
         stream = torch.cuda.current_stream(x.device)
-    st = quantize_grouped_absmax_raw(sid, x.data_ptr(), [N, K], _dtype_code(x.dtype), codes.data_ptr(),
-                                     scales.data_ptr(), status.data_ptr(), stream.cuda_stream)
+    with _device_of(x):
+        st = quantize_grouped_absmax_raw(sid, x.data_ptr(), [N, K], _dtype_code(x.dtype), codes.data_ptr(),
+                                         scales.data_ptr(), status.data_ptr(), stream.cuda_stream)
     if st != NQ_OK:
         raise NqError(st, f"{scheme} {[N, K]}")
     if check:
@@ -434,8 +453,9 @@ def quantize_q8_1(x, stream=None, check=True):
     status = torch.empty(1, dtype=torch.int32, device=x.device)
     if stream is None:
         stream = torch.cuda.current_stream(x.device)
-    st = quantize_q8_1_raw(x.data_ptr(), [M, K], _dtype_code(x.dtype), blocks.data_ptr(), status.data_ptr(),
-                           stream.cuda_stream)
+    with _device_of(x):
+        st = quantize_q8_1_raw(x.data_ptr(), [M, K], _dtype_code(x.dtype), blocks.data_ptr(), status.data_ptr(),
+                               stream.cuda_stream)
     if st != NQ_OK:
         raise NqError(st, f"q8_1 {[M, K]}")
     if check:
@@ -501,7 +521,8 @@ def _product(raw, fmt, weight, N, K, xq, out, stream):
         raise ValueError("out must be a contiguous float32 tensor of M * N elements")
     if stream is None:
         stream = torch.cuda.current_stream(weight.device)
-    st = raw(fid, weight.data_ptr(), weight.numel(), N, K, xq.data_ptr(), M, out.data_ptr(), stream.cuda_stream)
+    with _device_of(weight):
+        st = raw(fid, weight.data_ptr(), weight.numel(), N, K, xq.data_ptr(), M, out.data_ptr(), stream.cuda_stream)
     if st != NQ_OK:
         raise NqError(st, f"{fmt} [{N}, {K}] x {M}")
     return out
@@ -525,7 +546,8 @@ def gemm_q8_1(fmt, weight, N, K, xq, out=None, stream=None, split=True):
     M = xq.numel() // (K // 32 * 36) if K % 32 == 0 and K > 0 else 0
     ws, ws_bytes = None, 0
     if split and M > 0:
-        st, ws_bytes = gemm_q8_1_workspace(fid, N, K, M)
+        with _device_of(weight):
+            st, ws_bytes = gemm_q8_1_workspace(fid, N, K, M)
         if st != NQ_OK:
             raise NqError(st, f"{fmt} [{N}, {K}] x {M}")
         if ws_bytes:
@@ -548,8 +570,9 @@ def dequantize_packed(fmt, payload, shape, out_dtype=None, out=None, stream=None
     """
     fid = fmt if isinstance(fmt, int) else format_query(fmt).id
     code, out, stream = _prepare(payload, shape, out_dtype, out, stream)
-    st = dequantize_packed_raw(fid, payload.data_ptr(), payload.numel(), shape, code,
-                               out.data_ptr(), stream.cuda_stream)
+    with _device_of(payload):
+        st = dequantize_packed_raw(fid, payload.data_ptr(), payload.numel(), shape, code,
+                                   out.data_ptr(), stream.cuda_stream)
     if st != NQ_OK:
         raise NqError(st, f"{fmt} {list(shape)}")
     return out
@@ -608,23 +631,32 @@ KvStep = collections.namedtuple("KvStep", "lengths token_start slots free_state 
 # nq_kv_attention_args as packed bytes (the fields of KvAttentionArgs, in its layout).
 _ATTENTION_ARGS = struct.Struct("@PqqqqqPPPqqqqqPPif")
 assert _ATTENTION_ARGS.size == ctypes.sizeof(KvAttentionArgs)
-_I32 = _I64 = _F32 = _U8 = _STREAM = None
+_I32 = _I64 = _F32 = _U8 = _STREAM = _DEVICE = None
 _KV_DTYPES = {}
 
 
 def _torch_names():
     """torch's names that the calls below use, looked up at the first of them."""
-    global _I32, _I64, _F32, _U8, _STREAM
+    global _I32, _I64, _F32, _U8, _STREAM, _DEVICE
     import torch
     _KV_DTYPES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
     _I64, _F32, _U8, _STREAM = torch.int64, torch.float32, torch.uint8, torch._C._cuda_getCurrentRawStream
+    _DEVICE = torch._C._cuda_getDevice
     _I32 = torch.int32
 
 
-def _on(stream):
+def _on(stream, index):
     """Outputs belong to the stream that the work runs on."""
     import torch
+    if stream.device.index != index:
+        raise ValueError(f"stream must be one of CUDA device {index}")
     return torch.cuda.stream(stream)
+
+
+def _at(index):
+    """The calls' work goes to their tensors' device, whichever is the current one (as _device_of)."""
+    import torch
+    return torch.cuda.device(index)
 
 
 def _kv_dtype(dtype):
@@ -652,12 +684,15 @@ def kv_tables(lengths, added, table, ring, free_state, block, tokens, stream=Non
     """
     if _I32 is None:
         _torch_names()
-    if stream is not None:
-        with _on(stream):
-            return kv_tables(lengths, added, table, ring, free_state, block, tokens)
     if not lengths.is_cuda:
         raise ValueError("lengths must be a CUDA tensor")
     index, n, i32 = lengths.get_device(), lengths.numel(), _I32
+    if stream is not None:
+        with _on(stream, index):
+            return kv_tables(lengths, added, table, ring, free_state, block, tokens)
+    if _DEVICE() != index:
+        with _at(index):
+            return kv_tables(lengths, added, table, ring, free_state, block, tokens)
     if not (lengths.dtype is i32 and added.dtype is i32 and ring.dtype is i32 and free_state.dtype is i32 and
             added.get_device() == index and ring.get_device() == index and free_state.get_device() == index and
             lengths.is_contiguous() and added.is_contiguous() and ring.is_contiguous() and free_state.is_contiguous() and
@@ -694,7 +729,10 @@ def kv_store(cache, k, v, slots, token_start, stream=None):
     Returns status int32 [1]: 1 a value is not finite (NaN is stored as 0, infinities saturate), 2 a slot outside
     the pool or out of order (that block's tokens are not stored)."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, cache.index):
+            return kv_store(cache, k, v, slots, token_start)
+    if _DEVICE() != cache.index:
+        with _at(cache.index):
             return kv_store(cache, k, v, slots, token_start)
     _heads_of("k", k, cache, cache.heads)
     _heads_of("v", v, cache, cache.heads)
@@ -719,7 +757,10 @@ def kv_store(cache, k, v, slots, token_start, stream=None):
 def kv_load(cache, ids, out_dtype=None, stream=None):
     """Keys and values of whole blocks (ids: int32 [n]), each [n, block, heads, dim] in out_dtype (default float32)."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, cache.index):
+            return kv_load(cache, ids, out_dtype)
+    if _DEVICE() != cache.index:
+        with _at(cache.index):
             return kv_load(cache, ids, out_dtype)
     index = cache.index
     if not (ids.dtype is _I32 and ids.get_device() == index and ids.is_contiguous()):
@@ -749,7 +790,10 @@ def kv_attention(cache, q, token_start, lengths, table, scale=None, window=0, ma
     [tokens, q_heads].
     """
     if stream is not None:
-        with _on(stream):
+        with _on(stream, cache.index):
+            return kv_attention(cache, q, token_start, lengths, table, scale, window, max_new, max_length, return_lse)
+    if _DEVICE() != cache.index:
+        with _at(cache.index):
             return kv_attention(cache, q, token_start, lengths, table, scale, window, max_new, max_length, return_lse)
     _heads_of("q", q, cache)
     n, q_heads, dim = q.shape
