@@ -126,6 +126,41 @@ NQ_HD int64_t kv_v_at(const KvPool &c, int page, uint32_t head, int channel, int
 }
 
 // ---------------------------------------------------------------------------
+// Attention for many rows: who stages what
+// ---------------------------------------------------------------------------
+// NW waves stage the codes of 64 keys.  All pieces of a wave lie in the same
+// 16 keys (its `sub`, shared by PER waves, of which it is `part`), so a tile
+// takes it one table entry.  A piece of the keys is 1 KB in a row (KL keys),
+// one of the values 16 keys of 64 channels; 16 bytes of it are a lane's.
+template <int DIM, int NW>
+struct KvRows {
+    static constexpr int KT = 64, ROWS = 32 * NW;
+    static constexpr int PER = NW / 4;                      // waves that stage 16 keys
+    static constexpr int KL = 1024 / DIM;                   // keys of a 1 KB piece
+    static constexpr int NL = 16 / (PER * KL);              // a wave's pieces of the keys, and of the values
+    static constexpr int KS = DIM + 8, VS = KT + 8;         // row strides in LDS, binary16 elements
+    static constexpr int K_ELEMS = KT * KS, V_ELEMS = DIM * VS;
+    static constexpr int SC = 20;                           // floats of a buffer's scales
+    static constexpr int LDS_BYTES = 2 * (K_ELEMS + V_ELEMS) * 2 + 2 * SC * 4;
+    static_assert(NL >= 1 && NL * PER * KL == 16 && NL * PER * 64 == DIM, "the waves share 16 keys evenly");
+
+    // byte offsets of a lane's part of piece n: in the codes of 16 keys, and in those of DIM channels from a key on
+    NQ_HD static uint32_t k_from(int part, int lane, int n) { return (uint32_t)((part * NL + n) * 1024 + 16 * lane); }
+    NQ_HD static uint32_t v_from(int part, int lane, int n, uint32_t bsh) { return (uint32_t)(64 * (part * NL + n) + lane) << bsh; }
+    // its places in the LDS buffers, in elements
+    NQ_HD static int k_put(int sub, int part, int lane, int n) {
+        return (16 * sub + (part * NL + n) * KL + lane / (DIM / 16)) * KS + 16 * (lane % (DIM / 16));
+    }
+    NQ_HD static int v_put(int sub, int part, int lane, int n) { return (64 * (part * NL + n) + lane) * VS + 16 * sub; }
+    // the block that kv_named named (block 0 for none), and a key's codes in a block
+    NQ_HD static uint64_t block_at(const KvPool &c, int page) {
+        return (uint64_t)(uint32_t)(page < 0 ? 0 : page) * (c.heads * ((uint32_t)DIM << c.bsh));  // 2^16 * 2^15 at most
+    }
+    NQ_HD static uint32_t k_at(int key, uint32_t bsh) { return (uint32_t)(key & ((1 << bsh) - 1)) * DIM; }
+    NQ_HD static uint32_t v_at(int key, uint32_t bsh) { return (uint32_t)(key & ((1 << bsh) - 1)); }
+};
+
+// ---------------------------------------------------------------------------
 // Launch arguments
 // ---------------------------------------------------------------------------
 struct KvTablesLaunch {
@@ -190,6 +225,27 @@ struct KvAttnLaunch {
     int32_t splits, splits_few;  // pieces of a tile, at most
     int32_t few_tokens;  // new tokens of a request that the few-rows kernel can have, or 0: see kv_few_row
 };
+
+// A request's token range and length, made safe: starts inside [0, tokens].  Of more than max_new new tokens the first
+// max_new are computed, [s0, s1); without the others, up to `end`, the request is one that ends there (len), so the
+// positions stay what they are.
+struct KvReq {
+    int s0, s1, end, len;
+};
+NQ_HD KvReq kv_request(const KvAttnLaunch &a, int r) {
+    KvReq q;
+    q.s0 = a.starts[r];
+    int s1 = a.starts[r + 1];
+    q.len = a.lengths[r];
+    q.s0 = q.s0 < 0 ? 0 : q.s0 > a.tokens ? a.tokens : q.s0;
+    s1 = s1 < q.s0 ? q.s0 : s1 > 1 << 30 ? 1 << 30 : s1;  // 2^30 tokens at most: no sum below leaves 32 bits
+    if (q.len < 0) q.len = 0;
+    q.end = s1 > a.tokens ? a.tokens : s1;
+    q.s1 = q.end - q.s0 > a.max_new ? q.s0 + a.max_new : q.end;
+    q.len -= s1 - q.s1;
+    return q;
+}
+
 // The place of a row's pieces among the few-rows kernel's: every request has few_tokens * q_heads places, where that
 // is less than one for each row of the call (a prompt's rows take none), or (few_tokens = 0) its own rows' places.
 NQ_HD int64_t kv_few_row(const KvAttnLaunch &a, int req, int start, int tok, int head) {
@@ -201,6 +257,72 @@ NQ_HD uint64_t kv_few_part_rows(const KvAttnLaunch &a) {
     if (a.splits_few <= 1) return 0;
     return (a.few_tokens > 0 ? (uint64_t)a.requests * (uint64_t)a.few_tokens : (uint64_t)a.tokens) * (uint64_t)a.q_heads;
 }
-void kv_attn_plan(KvAttnLaunch &L, uint32_t cus);
+
+// How the work of an attention call is cut: the host knows the bounds
+// max_new and max_length, not the lengths themselves (reading those would
+// wait for the stream), so every request gets the workgroups of the longest
+// one and those past its own end return at once.
+//
+// Requests of at most `few` rows go to the kernel for few rows, the others to
+// the one for many: measured at 32 requests of 2000 to 4000 keys, few against
+// many at 64 and 128 rows 84 / 105 and 98 / 131 us (64 channels), 119 / 194
+// and 166 / 198 us (128), at 32 and 48 rows 267 / 341 and 358 / 318 us (256).
+// Binary32 queries stay with few rows: their second terms cost the other
+// kernel its second wave a SIMD.  Built for them too, it measured, few against
+// many at 256 rows of such requests, 152 / 199 us (64 channels) and 256 / 386
+// us (128), and at 2048 tokens of one request 228 / 231 and 554 / 485 us.
+//
+// A piece is `chunk` keys: several pieces a row let few rows fill the card,
+// each costs a workgroup's start and end and a partial output.  Measured for
+// few rows at pieces of 256, 512, 1024, 2048 and 4096 keys: 128 ragged
+// requests of up to 8200 keys 127, 99, 86, 82 and 88 us; two of 131001 and
+// about 90000 keys 153, 114, 97, 95 and 92 us; 32 requests with 5 tokens and a
+// window of 2049 keys 37, 33, 32, 38 and 33 us.  Many rows are cut only where
+// the tiles leave compute units idle.
+inline void kv_attn_plan(KvAttnLaunch &L, uint32_t cus) {
+    const int64_t rows = (int64_t)L.max_new * L.group;
+    auto span_of = [&](int64_t tile_rows) {
+        const int64_t seen = (int64_t)L.window + tile_rows / L.group + 2 + 63;
+        const int64_t span = L.window > 0 && seen < L.cap ? seen : L.cap;
+        return span < 1 ? 1 : span;
+    };
+    auto cut = [](int64_t span, int64_t pieces, int64_t least, int32_t *chunk, int32_t *splits) {
+        if (pieces > 65535) pieces = 65535;
+        int64_t c = ((span + pieces - 1) / pieces + 63) / 64 * 64;
+        if (c < least) c = least;
+        *chunk = (int32_t)c;
+        *splits = (int32_t)((span + c - 1) / c);
+    };
+    L.few = L.c.dim == 256 ? 32 : 128;
+    L.waves = 0;
+    L.tiles = L.splits = 0;
+    L.chunk = 256;
+    if (L.dtype == 0) L.few = 1 << 30;  // binary32: two terms a row
+    if (rows > L.few) {
+        L.waves = L.c.dim == 128 ? 8 : 4;
+        const int64_t tr = 32 * L.waves;
+        const int64_t tiles = (rows + tr - 1) / tr;
+        L.tiles = (int32_t)tiles;
+        // tiles that have rows, at most
+        int64_t busy = (int64_t)L.tokens * L.group / tr + L.requests;
+        if (busy > L.requests * tiles) busy = L.requests * tiles;
+        busy *= L.c.heads;
+        const int64_t want = L.c.dim == 64 ? 2 * cus : cus;  // workgroups that the card holds
+        cut(span_of(tr), busy >= want ? 1 : (want + busy - 1) / busy, 512, &L.chunk, &L.splits);
+    }
+    const int64_t few_rows = rows < L.few ? rows : L.few;
+    L.tiles_few = (int32_t)((few_rows + 15) / 16);
+    const int64_t span = span_of(16);
+    int64_t busy = (int64_t)L.tokens * L.group / 16 + L.requests;
+    if (busy > (int64_t)L.requests * L.tiles_few) busy = (int64_t)L.requests * L.tiles_few;
+    busy *= L.c.heads;
+    // six workgroups a compute unit, and no piece above 2048 keys where lengths differ
+    int64_t pieces = busy > 0 ? (6ll * cus + busy - 1) / busy : 1;
+    if (L.tiles_few <= 4 && pieces < (span + 2047) / 2048) pieces = (span + 2047) / 2048;
+    cut(span, pieces, 512, &L.chunk_few, &L.splits_few);
+    const int64_t most = L.few / L.group < L.max_new ? L.few / L.group : L.max_new;
+    if (most == 0) L.splits_few = 1;  // a single token has more rows than the few-rows kernel takes
+    L.few_tokens = most * L.requests < L.tokens ? (int32_t)most : 0;
+}
 
 }  // namespace nq

@@ -9,72 +9,6 @@ uint32_t device_compute_units();
 int launch_kv_attn_q8(const KvAttnLaunch &L, hipStream_t s);
 int launch_kv_attn_e4m3(const KvAttnLaunch &L, hipStream_t s);
 
-// How the work of an attention call is cut: the host knows the bounds
-// max_new and max_length, not the lengths themselves (reading those would
-// wait for the stream), so every request gets the workgroups of the longest
-// one and those past its own end return at once.
-//
-// Requests of at most `few` rows go to the kernel for few rows, the others to
-// the one for many: measured at 32 requests of 2000 to 4000 keys, few against
-// many at 64 and 128 rows 84 / 105 and 98 / 131 us (64 channels), 119 / 194
-// and 166 / 198 us (128), at 32 and 48 rows 267 / 341 and 358 / 318 us (256).
-// Binary32 queries stay with few rows: their second terms cost the other
-// kernel its second wave a SIMD.  Built for them too, it measured, few against
-// many at 256 rows of such requests, 152 / 199 us (64 channels) and 256 / 386
-// us (128), and at 2048 tokens of one request 228 / 231 and 554 / 485 us.
-//
-// A piece is `chunk` keys: several pieces a row let few rows fill the card,
-// each costs a workgroup's start and end and a partial output.  Measured for
-// few rows at pieces of 256, 512, 1024, 2048 and 4096 keys: 128 ragged
-// requests of up to 8200 keys 127, 99, 86, 82 and 88 us; two of 131001 and
-// about 90000 keys 153, 114, 97, 95 and 92 us; 32 requests with 5 tokens and a
-// window of 2049 keys 37, 33, 32, 38 and 33 us.  Many rows are cut only where
-// the tiles leave compute units idle.
-void kv_attn_plan(KvAttnLaunch &L, uint32_t cus) {
-    const int64_t rows = (int64_t)L.max_new * L.group;
-    auto span_of = [&](int64_t tile_rows) {
-        const int64_t seen = (int64_t)L.window + tile_rows / L.group + 2 + 63;
-        const int64_t span = L.window > 0 && seen < L.cap ? seen : L.cap;
-        return span < 1 ? 1 : span;
-    };
-    auto cut = [](int64_t span, int64_t pieces, int64_t least, int32_t *chunk, int32_t *splits) {
-        if (pieces > 65535) pieces = 65535;
-        int64_t c = ((span + pieces - 1) / pieces + 63) / 64 * 64;
-        if (c < least) c = least;
-        *chunk = (int32_t)c;
-        *splits = (int32_t)((span + c - 1) / c);
-    };
-    L.few = L.c.dim == 256 ? 32 : 128;
-    L.waves = 0;
-    L.tiles = L.splits = 0;
-    L.chunk = 256;
-    if (L.dtype == 0) L.few = 1 << 30;  // binary32: two terms a row
-    if (rows > L.few) {
-        L.waves = L.c.dim == 128 ? 8 : 4;
-        const int64_t tr = 32 * L.waves;
-        const int64_t tiles = (rows + tr - 1) / tr;
-        L.tiles = (int32_t)tiles;
-        // tiles that have rows, at most
-        int64_t busy = (int64_t)L.tokens * L.group / tr + L.requests;
-        if (busy > L.requests * tiles) busy = L.requests * tiles;
-        busy *= L.c.heads;
-        const int64_t want = L.c.dim == 64 ? 2 * cus : cus;  // workgroups that the card holds
-        cut(span_of(tr), busy >= want ? 1 : (want + busy - 1) / busy, 512, &L.chunk, &L.splits);
-    }
-    const int64_t few_rows = rows < L.few ? rows : L.few;
-    L.tiles_few = (int32_t)((few_rows + 15) / 16);
-    const int64_t span = span_of(16);
-    int64_t busy = (int64_t)L.tokens * L.group / 16 + L.requests;
-    if (busy > (int64_t)L.requests * L.tiles_few) busy = (int64_t)L.requests * L.tiles_few;
-    busy *= L.c.heads;
-    // six workgroups a compute unit, and no piece above 2048 keys where lengths differ
-    int64_t pieces = busy > 0 ? (6ll * cus + busy - 1) / busy : 1;
-    if (L.tiles_few <= 4 && pieces < (span + 2047) / 2048) pieces = (span + 2047) / 2048;
-    cut(span, pieces, 512, &L.chunk_few, &L.splits_few);
-    const int64_t most = L.few / L.group < L.max_new ? L.few / L.group : L.max_new;
-    if (most == 0) L.splits_few = 1;  // a single token has more rows than the few-rows kernel takes
-    L.few_tokens = most * L.requests < L.tokens ? (int32_t)most : 0;
-}
 }  // namespace nq
 
 namespace {

@@ -66,26 +66,6 @@ struct KvTableRow {
     __device__ __forceinline__ int operator()(int i) const { return row[i]; }
 };
 
-// A request's token range and length, made safe: starts inside [0, tokens].  Of more than max_new new tokens the first
-// max_new are computed, [s0, s1); without the others, up to `end`, the request is one that ends there (len), so the
-// positions stay what they are.
-struct KvReq {
-    int s0, s1, end, len;
-};
-__device__ __forceinline__ KvReq kv_request(const KvAttnLaunch &a, int r) {
-    KvReq q;
-    q.s0 = a.starts[r];
-    int s1 = a.starts[r + 1];
-    q.len = a.lengths[r];
-    q.s0 = q.s0 < 0 ? 0 : q.s0 > a.tokens ? a.tokens : q.s0;
-    s1 = s1 < q.s0 ? q.s0 : s1 > 1 << 30 ? 1 << 30 : s1;  // 2^30 tokens at most: no sum below leaves 32 bits
-    if (q.len < 0) q.len = 0;
-    q.end = s1 > a.tokens ? a.tokens : s1;
-    q.s1 = q.end - q.s0 > a.max_new ? q.s0 + a.max_new : q.end;
-    q.len -= s1 - q.s1;
-    return q;
-}
-
 // ---------------------------------------------------------------------------
 // Few rows: one wave per run of keys
 // ---------------------------------------------------------------------------

@@ -28,19 +28,6 @@ namespace nq {
 typedef float kv_f16x __attribute__((ext_vector_type(16)));
 typedef __bf16 kv_b8 __attribute__((ext_vector_type(8)));
 
-template <int DIM, int NW>
-struct KvRows {
-    static constexpr int KT = 64, ROWS = 32 * NW;
-    static constexpr int PER = NW / 4;                      // waves that stage 16 keys
-    static constexpr int KL = 1024 / DIM;                   // keys of a 1 KB piece
-    static constexpr int NL = 16 / (PER * KL);              // a wave's pieces of the keys, and of the values
-    static constexpr int KS = DIM + 8, VS = KT + 8;         // row strides in LDS, binary16 elements
-    static constexpr int K_ELEMS = KT * KS, V_ELEMS = DIM * VS;
-    static constexpr int SC = 20;                           // floats of a buffer's scales, below
-    static constexpr int LDS_BYTES = 2 * (K_ELEMS + V_ELEMS) * 2 + 2 * SC * 4;
-    static_assert(NL >= 1 && NL * PER * KL == 16 && NL * PER * 64 == DIM, "the waves share 16 keys evenly");
-};
-
 // Weights are times 2^14: a row's maximum in use may lag behind by 2^KV_LAG
 // before its output is multiplied down (binary16 holds up to 2^16).
 constexpr float KV_ROWS_PSCALE = 16384.0f, KV_LAG = 1.5f;
@@ -146,7 +133,7 @@ __device__ __forceinline__ int kv_ranked(const KvAttnLaunch &a, int z) {
 template <int CODE, int DIM, int IN, int NW>
 __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void k_kv_attn_rows(KvAttnArgs args) {
     using C = KvRows<DIM, NW>;
-    constexpr int KT = C::KT, NL = C::NL, KS = C::KS, VS = C::VS, SC = C::SC, KL = C::KL;
+    constexpr int KT = C::KT, NL = C::NL, KS = C::KS, VS = C::VS, SC = C::SC;
     constexpr int NS = DIM / 16;  // channel steps of a score
     constexpr int ND = DIM / 32;  // output tiles
     extern __shared__ __align__(16) uint8_t lds_raw[];
@@ -183,17 +170,14 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void k_kv_attn_rows(KvA
     kv_h8 Q[NS];
     const float qscale = kv_load_rows<IN, NS>(a, (int64_t)(q.s0 + tok) * a.q_ts + ((int64_t)head * group + row % group) * a.q_hs + 8 * h, Q);
 
-    // Staging: all pieces of a wave lie in the same 16 keys, so a tile takes it one table entry.  A piece of the keys
-    // is 1 KB in a row (KL keys), one of the values 16 keys of 64 channels.  What lies past the last tile is fetched
-    // and staged as if it were there (from block 0): nothing reads it.
+    // Staging.  What lies past the last tile is fetched and staged as if it were there (from block 0): nothing reads it.
     const int sub = wave / C::PER, part = wave % C::PER;
     const int32_t *const table = a.table + (int64_t)req * a.table_stride;
-    const uint32_t bsh = a.c.bsh, tmask = (1u << bsh) - 1, tile_bytes = (uint32_t)DIM << bsh;
-    const uint8_t *const kbase = a.c.k + (uint64_t)head * tile_bytes + (part * NL * KL) * DIM + 16 * lane;
-    const uint8_t *const vbase = a.c.v + (uint64_t)head * tile_bytes + (((uint32_t)(64 * part * NL + lane)) << bsh);
-    const uint32_t block_bytes = a.c.heads * tile_bytes;  // at most 2^16 * 2^15
-    _Float16 *const kput = kbuf + (16 * sub + part * NL * KL + lane / (DIM / 16)) * KS + 16 * (lane % (DIM / 16));
-    _Float16 *const vput = vbuf + (64 * part * NL + lane) * VS + 16 * sub;
+    const uint32_t bsh = a.c.bsh, tile_bytes = (uint32_t)DIM << bsh;
+    const uint8_t *const kbase = a.c.k + (uint64_t)head * tile_bytes + C::k_from(part, lane, 0);
+    const uint8_t *const vbase = a.c.v + (uint64_t)head * tile_bytes + C::v_from(part, lane, 0, bsh);
+    _Float16 *const kput = kbuf + C::k_put(sub, part, lane, 0);
+    _Float16 *const vput = vbuf + C::v_put(sub, part, lane, 0);
     kv_u4 rk[NL], rv[NL];
     int entry = 0, page = -1, was = -1;  // the table entry on its way, the block of the keys and of the values fetched last
     float rks = 0.0f, rvs = 0.0f;
@@ -204,18 +188,17 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void k_kv_attn_rows(KvA
     auto find = [&](int key0) { entry = table[kv_entry(key0 + 16 * sub, t, bsh) + none]; };
     auto fetch_k = [&](int key0) {
         page = kv_named(__builtin_amdgcn_readfirstlane(entry), key0 + 16 * sub, t, bsh, a.c.blocks);
-        const uint8_t *const src = kbase + (uint64_t)(uint32_t)(page < 0 ? 0 : page) * block_bytes + (((key0 + 16 * sub) & tmask) * DIM);
+        const uint8_t *const src = kbase + C::block_at(a.c, page) + C::k_at(key0 + 16 * sub, bsh);
 #pragma unroll
-        for (int n = 0; n < NL; n++) rk[n] = *(const kv_u4 *)(src + n * 1024);
+        for (int n = 0; n < NL; n++) rk[n] = *(const kv_u4 *)(src + C::k_from(0, 0, n));
     };
     auto fetch_v = [&](int key0, int block) {
         was = block;
-        const uint32_t at = block < 0 ? 0 : (uint32_t)block;
-        const uint8_t *const src = vbase + (uint64_t)at * block_bytes + ((key0 + 16 * sub) & tmask);
+        const uint8_t *const src = vbase + C::block_at(a.c, block) + C::v_at(key0 + 16 * sub, bsh);
 #pragma unroll
-        for (int n = 0; n < NL; n++) rv[n] = *(const kv_u4 *)(src + ((uint32_t)(64 * n) << bsh));
+        for (int n = 0; n < NL; n++) rv[n] = *(const kv_u4 *)(src + C::v_from(0, 0, n, bsh));
         if (part == 0) {
-            const uint64_t s = (uint64_t)at * a.c.heads + head + none;
+            const uint64_t s = (uint64_t)(block < 0 ? 0 : (uint32_t)block) * a.c.heads + head + none;
             rks = a.c.ks[s];
             rvs = a.c.vs[s];
         }
@@ -228,7 +211,7 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void k_kv_attn_rows(KvA
     auto stage_k = [&](int b) {
 #pragma unroll
         for (int n = 0; n < NL; n++) {
-            _Float16 *const d = kput + b * C::K_ELEMS + n * KL * KS;
+            _Float16 *const d = kput + b * C::K_ELEMS + C::k_put(0, 0, 0, n);
             *(kv_h8 *)d = kv_codes8_f16<CODE>(kv_u2{rk[n][0], rk[n][1]});
             *(kv_h8 *)(d + 8) = kv_codes8_f16<CODE>(kv_u2{rk[n][2], rk[n][3]});
         }
@@ -236,7 +219,7 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void k_kv_attn_rows(KvA
     auto stage_v = [&](int b) {
 #pragma unroll
         for (int n = 0; n < NL; n++) {
-            _Float16 *const d = vput + b * C::V_ELEMS + 64 * n * VS;
+            _Float16 *const d = vput + b * C::V_ELEMS + C::v_put(0, 0, 0, n);
             *(kv_h8 *)d = kv_codes8_f16<CODE>(kv_u2{rv[n][0], rv[n][2]});
             *(kv_h8 *)(d + 8) = kv_codes8_f16<CODE>(kv_u2{rv[n][1], rv[n][3]});
         }

@@ -30,6 +30,9 @@ def emu():
     L = ctypes.CDLL(EMU)
     L.nq_kv_emu_request.argtypes = [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int, ctypes.c_int,
                                     ctypes.c_void_p, ctypes.c_void_p]
+    L.nq_kv_emu_call.restype = ctypes.c_long
+    L.nq_kv_emu_call.argtypes = ([ctypes.c_void_p] * 2 + [ctypes.c_int] * 10 + [ctypes.c_void_p, ctypes.c_int,
+                                 ctypes.c_int64, ctypes.c_int] + [ctypes.c_void_p] * 2)
     return L
 
 
@@ -121,3 +124,75 @@ def test_sizes_past_the_launch_are_refused():
         assert workspace(most, 1, most, dtype=0, **size)[0] == 7
         assert workspace(most - 16, 1, most - 16, dtype=0, **size)[0] == 0
         assert workspace(most, 1, most, dtype=1, **size)[0] == 0
+
+
+# --- a call's plan, pieces and staging --------------------------------------------------------------------------
+
+def run_call(emu, starts, lengths, tokens, heads, group, dim, bsh, dtype, window, max_new, max_length, table, blocks,
+             cus=256):
+    """(what was wrong, how often each token's row is computed, [splits, splits_few, few_tokens])."""
+    rows, cuts = np.zeros(tokens + 1, np.int32), np.zeros(3, np.int32)
+    bad = emu.nq_kv_emu_call(starts.ctypes.data, lengths.ctypes.data, lengths.size, tokens, heads, group, dim, bsh, dtype,
+                             window, max_new, max_length, table.ctypes.data, table.shape[1], blocks, cus,
+                             rows.ctypes.data, cuts.ctypes.data)
+    return bad, rows, cuts
+
+
+def any_table(rng, requests, width, blocks):
+    t = rng.integers(0, blocks, (requests, width)).astype(np.int32)
+    t[rng.random(t.shape) < 0.1] = rng.choice([-1, -2 ** 31, blocks, 2 ** 31 - 1])
+    return t
+
+
+@pytest.mark.parametrize("dim, heads, group", [(64, 3, 1), (64, 1, 5), (128, 1, 4), (128, 2, 1), (256, 1, 8),
+                                               (128, 1, 140)])
+@pytest.mark.parametrize("dtype", [0, 2])
+@pytest.mark.parametrize("bsh", [4, 7])
+def test_a_calls_pieces_and_staging(emu, dim, heads, group, dtype, bsh):
+    """The plan that the library makes: no tile or piece beyond its launch, each piece of a row in a place of its own
+    inside the workspace, every staged code from its key's own place in the pool, every row within max_new once."""
+    rng = np.random.default_rng(dim + group + bsh)
+    cut = np.zeros(3, bool)
+    for trial in range(12):
+        blocks, requests = 7, int(rng.choice([1, 2, 5, 30]))
+        if trial == 0:  # one chunk over many keys: cut
+            requests = 1
+        new = rng.choice([0, 1, 1, 1, 2, 5, 33, 150], requests) if trial else np.array([150])
+        starts = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        tokens = int(starts[-1]) + int(rng.integers(0, 4)) + (starts[-1] == 0)
+        longest = int(rng.choice([64, 700, 3000])) if trial else 3000
+        lengths = rng.integers(0 if trial else longest // 2, longest, requests)
+        lengths = (lengths + new * (trial % 4 > 0)).astype(np.int32)
+        most = int(max(1, new.max()))
+        max_new, max_length = most, longest + most
+        if trial and trial % 3 == 0:
+            max_new, max_length = max(1, most // 2), longest // 2
+        window = int(rng.choice([0, 0, 1, 100, 1500])) if trial else 0
+        table = any_table(rng, requests, -(-(longest + most) >> bsh) + 1, blocks)
+        bad, rows, cuts = run_call(emu, starts, lengths, tokens, heads, group, dim, bsh, dtype, window, max_new,
+                                   max_length, table, blocks, cus=int(rng.choice([8, 256])) if trial else 256)
+        assert bad == 0, (trial, requests, window, max_new, max_length)
+        want = np.zeros(tokens + 1, np.int32)
+        for s0, s1 in zip(starts, starts[1:]):
+            want[s0:min(s1, s0 + max_new)] = 1
+        assert np.array_equal(rows, want)
+        cut |= cuts > 1
+    assert (cut[1] or group > 128) and (cut[0] or dtype == 0)  # both kernels' rows were cut, where they have some
+
+
+@pytest.mark.parametrize("seed", range(30))
+def test_a_calls_pieces_stay_inside_for_any_lengths(emu, seed):
+    """Starts and lengths that no step makes: still nothing outside the workspace, the table or the pool."""
+    rng = np.random.default_rng(seed)
+    requests, blocks, tokens = int(rng.integers(1, 6)), 5, int(rng.integers(1, 300))
+    odd = [-2 ** 31, -1, 0, 1, 7, tokens, tokens + 1, 2 ** 30 + 5, 2 ** 31 - 1]
+    starts = rng.choice(odd, requests + 1).astype(np.int32)
+    lengths = rng.choice(odd, requests).astype(np.int32)
+    # requests that share tokens write their rows' pieces twice: look at one request at a time for that
+    for r in range(requests):
+        one = np.ascontiguousarray(starts[r:r + 2])
+        dim, group = int(rng.choice([64, 128, 256])), int(rng.choice([1, 4, 9]))
+        bad, _, _ = run_call(emu, one, lengths[r:r + 1].copy(), tokens, 2, group, dim, 5, int(rng.choice([0, 1])),
+                             int(rng.choice([0, 1, 500, 2 ** 30])), int(rng.choice([1, 50, 1 << 20])), 1500,
+                             any_table(rng, 1, 40, blocks), blocks)
+        assert bad == 0, (one, lengths[r])
