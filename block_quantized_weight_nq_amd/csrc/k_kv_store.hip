@@ -16,6 +16,8 @@
 // chain of dependent loads (starts, slot, values) for single tokens.
 #include "nq_kv_codes.h"
 
+#include <type_traits>
+
 namespace nq {
 
 namespace {
@@ -62,8 +64,9 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
 __global__ void k_kv_clear_status(uint32_t *status) { *status = 0u; }
 
 // HOLD: tiles of each kind that a thread keeps, 1 for blocks of up to 4096 values (fewer registers, more workgroups at
-// a time).
-template <int CODE, int IN, bool VEC, int HOLD>
+// a time).  MANY: more than TB requests, which are searched (with the search in it, 30.6 us instead of 29.8 for 16000
+// tokens of 6 requests).
+template <int CODE, int IN, bool VEC, int HOLD, bool MANY>
 __global__ __launch_bounds__(TB) void k_kv_store(KvStoreLaunch a) {
     __shared__ uint32_t wmax[2][TB / 64];
     __shared__ int32_t found[3];
@@ -75,11 +78,13 @@ __global__ __launch_bounds__(TB) void k_kv_store(KvStoreLaunch a) {
     // the request of this unit, among TB of them at the end
     if (tid == 0) found[0] = -1;
     int32_t from = 0, left = a.requests;
-    while (left > TB) {
-        const int32_t step = kv_probe_step(left, TB), i = from + tid * step;
-        const int hits = __syncthreads_count(tid * step < left && kv_unit_first(a.starts[i], i, a.c.bsh) <= u);
-        if (hits == 0) return;
-        kv_narrow(&from, &left, step, hits);
+    if constexpr (MANY) {
+        while (left > TB) {
+            const int32_t step = kv_probe_step(left, TB), i = from + tid * step;
+            const int hits = __syncthreads_count(tid * step < left && kv_unit_first(a.starts[i], i, a.c.bsh) <= u);
+            if (hits == 0) return;
+            kv_narrow(&from, &left, step, hits);
+        }
     }
     __syncthreads();
     if (tid < left) {
@@ -246,12 +251,18 @@ static int store_in(const KvStoreLaunch &L, hipStream_t s) {
         vec &= (uintptr_t)L.x[i] % (4 * ESZ) == 0 && L.ts[i] % 4 == 0 && L.hs[i] % 4 == 0;
     const dim3 grid((uint32_t)units, L.c.heads);
     const bool one = (L.c.dim << L.c.bsh) <= 16 * TB;
-    if (vec && one)
-        hipLaunchKernelGGL((k_kv_store<CODE, IN, true, 1>), grid, dim3(TB), 0, s, L);
-    else if (vec)
-        hipLaunchKernelGGL((k_kv_store<CODE, IN, true, 2>), grid, dim3(TB), 0, s, L);
+    const auto launch = [&](auto many) {
+        if (vec && one)
+            hipLaunchKernelGGL((k_kv_store<CODE, IN, true, 1, many()>), grid, dim3(TB), 0, s, L);
+        else if (vec)
+            hipLaunchKernelGGL((k_kv_store<CODE, IN, true, 2, many()>), grid, dim3(TB), 0, s, L);
+        else
+            hipLaunchKernelGGL((k_kv_store<CODE, IN, false, 2, many()>), grid, dim3(TB), 0, s, L);
+    };
+    if (L.requests > TB)
+        launch(std::true_type());
     else
-        hipLaunchKernelGGL((k_kv_store<CODE, IN, false, 2>), grid, dim3(TB), 0, s, L);
+        launch(std::false_type());
     return hipGetLastError() == hipSuccess ? 0 : 9;  // NQ_ERR_HIP
 }
 
