@@ -362,7 +362,9 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void k_kv_attn_dec(KvAttnAr
 #pragma unroll
     for (int w = 0; w < 4; w++) mm = fmaxf(mm, sm[w * 16 + orow]);
     const float safe = mm == -__builtin_inff() ? 0.0f : mm;
-    float sum = 0.0f, fw[4];
+    float sum = 0.0f, fw[4], vmax = sv[0];
+#pragma unroll
+    for (int w = 1; w < 4; w++) vmax = fmaxf(vmax, sv[w]);
 #pragma unroll
     for (int w = 0; w < 4; w++) {
         const float e = kv_exp2(sm[w * 16 + orow] - safe);
@@ -371,7 +373,7 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void k_kv_attn_dec(KvAttnAr
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-    for (int w = 0; w < 4; w++) fw[w] = fw[w] * inv * (sv[w] * (1.0f / KV_PSCALE));
+    for (int w = 0; w < 4; w++) fw[w] = fw[w] * inv * (sv[w] / vmax);  // vmax itself may be near 2^-126: the sum's factor
     const float lse2 = sum == 0.0f ? -__builtin_inff() : safe + __builtin_amdgcn_logf(sum);
     const int otok = (tile * 16 + orow) / group, oh = (int)head * group + (tile * 16 + orow) % group;
     const int64_t oat = (int64_t)(q.s0 + otok) * a.q_heads + oh;
@@ -381,6 +383,7 @@ __global__ __launch_bounds__(256, DIM > 128 ? 1 : 2) void k_kv_attn_dec(KvAttnAr
         res[i] = 0.0f;
 #pragma unroll
         for (int w = 0; w < 4; w++) res[i] += lds[w * 16 * C::OS + orow * C::OS + c0 + i] * fw[w];
+        res[i] = res[i] * (1.0f / KV_PSCALE) * vmax;
     }
     if (t.nsplit == 1) {
 #pragma unroll

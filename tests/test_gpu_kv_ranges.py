@@ -171,3 +171,23 @@ def test_store_of_many_requests(requests, filled):
     for x, y in zip((caches[0].k, caches[0].v, caches[0].k_scale, caches[0].v_scale),
                     (caches[1].k, caches[1].v, caches[1].k_scale, caches[1].v_scale)):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("code", ["q8", "e4m3"])
+@pytest.mark.parametrize("new", [1, 40])
+def test_values_near_the_least_scale(code, new):
+    """Value scales of 2^-112 and a channel in which the first 64 keys, whose weights are e^12 times the others', are 0:
+    binary32 outputs of about 2^-122 there, in full precision."""
+    rng = np.random.default_rng(new)
+    host, q, starts, lengths, table = attention_case(rng, [330, 280], [new, new], 2, 4, 64, 32, code, "f32")
+    kc, vc, ks, vs = host
+    q[:] = 1
+    for row in table:
+        for j, b in enumerate(row[: -(-330 // 32)]):
+            if 0 <= b < ks.shape[0]:
+                kc[b] = (1 if code == "q8" else 0x38) if j < 2 else 0
+                ks[b] = 1.5
+                if j < 2:
+                    vc[b, :, :8] = 0
+    vs[np.isfinite(vs)] = 2.0 ** -112
+    attend((host, q, starts, lengths, table), code, "f32", f"least scales {code} {new}", max_new=new)
