@@ -116,7 +116,7 @@ NQ_HD int kv_named(int entry, int key, const KvTile &t, uint32_t bsh, int64_t bl
 }
 
 // Byte offsets of a key's codes and of a channel's codes from token `key` on,
-// in the block `page` that kv_page named (block 0 stands in for -1: what is
+// in the block `page` that kv_named named (block 0 stands in for -1: what is
 // read there is masked).
 NQ_HD int64_t kv_k_at(const KvPool &c, int page, uint32_t head, int key) {
     return kv_tile_at(c, page < 0 ? 0 : page, head) + (int64_t)(key & ((1 << c.bsh) - 1)) * c.dim;

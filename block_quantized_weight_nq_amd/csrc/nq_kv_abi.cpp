@@ -1,4 +1,4 @@
-// nq_kv_abi.cpp -- the C ABI of the 8-bit key/value cache: argument checks and launch plans.
+// nq_kv_abi.cpp -- the C ABI of the 8-bit key/value cache: argument checks (the launch plan is nq_kv.h's).
 #include "../../include/nq.h"
 #include "nq_kv.h"
 

@@ -10,9 +10,11 @@
 // Arithmetic.  A code is exact in binary16, so the products run on
 // the binary16 matrix instructions with binary32 accumulation:
 //   * a query row is multiplied by a power of two that brings its largest
-//     element to [2^14, 2^15): binary16 and bfloat16 queries are then exact
-//     (bfloat16's smaller elements down to 2^-39 of the largest); a binary32
-//     query is the sum of two binary16 terms, exact to 2^-24 of an element;
+//     element to [2^14, 2^15) and rounded to binary16, whose least step is
+//     2^-24: binary16 queries stay exact (but for subnormals beside elements
+//     of 2^15), bfloat16 ones down to 2^-31 of the largest element; a
+//     binary32 query is the sum of two terms, off by 2^-22 of an element.
+//     What is smaller is off by at most 2^-39 of the largest;
 //   * exp(s_j - m) vs_j / vref, at most 1, times 2^14 is rounded to binary16
 //     (2^-11 of its value), or to two terms for binary32 queries (2^-22).
 //     Weights too small for that precision (below 2^-28 of 1; a wave sees

@@ -30,7 +30,7 @@ typedef __bf16 kv_b8 __attribute__((ext_vector_type(8)));
 
 // Weights are times 2^14: a row's maximum in use may lag behind by 2^KV_LAG
 // before its output is multiplied down (binary16 holds up to 2^16).
-constexpr float KV_ROWS_PSCALE = 16384.0f, KV_LAG = 1.5f;
+constexpr float KV_LAG = 1.5f;
 // vref is at least KV_VREF_MIN.  The sum l is in units of 2^14 / vref and, where every value is 0 (block scales of
 // 2^-126), stays in those of KV_VREF_MIN: 2^30 keys whose weights lag by KV_LAG make it 2^125.5.
 constexpr float KV_VREF_MIN = 0x1p-80f, KV_LUNIT_MAX = 94.0f;  // and log2(2^14 / KV_VREF_MIN)
@@ -235,7 +235,7 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void k_kv_attn_rows(KvA
 #pragma unroll
         for (int i = 0; i < 16; i++) O[d][i] = 0.0f;
     float m = -__builtin_inff(), l = 0.0f;
-    float vref = KV_VREF_MIN, unit = KV_ROWS_PSCALE / KV_VREF_MIN, lunit = KV_LUNIT_MAX;  // and log2(unit)
+    float vref = KV_VREF_MIN, unit = KV_PSCALE / KV_VREF_MIN, lunit = KV_LUNIT_MAX;  // and log2(unit)
 
     auto scores = [&](int b, kv_f16x (&S)[2]) {
         const _Float16 *const K = kbuf + b * C::K_ELEMS + r * KS + 8 * h;
@@ -317,7 +317,7 @@ __global__ __launch_bounds__(64 * NW, DIM > 128 ? 1 : 2) void k_kv_attn_rows(KvA
                 for (int i = 0; i < 16; i++) O[d][i] *= fo;
             m = m1;
             vref = vr1;
-            unit = KV_ROWS_PSCALE / vref;
+            unit = KV_PSCALE / vref;
             lunit = __builtin_amdgcn_logf(unit);
         }
         const float safe = m == -__builtin_inff() ? 0.0f : m;

@@ -449,7 +449,7 @@ int nq_kv_load(const nq_kv_cache *cache, const int32_t *ids, int64_t n, int32_t 
  * They and the counts alone set the launch and the workspace, so a captured
  * graph stays valid for other lengths within them.
  * Products are binary16 with binary32 accumulation; queries in binary32 and
- * their probabilities are taken in two binary16 terms (about 2^-23).  The
+ * their probabilities are taken in two binary16 terms (2^-22).  The
  * order of sums is fixed by the shapes: repeated calls give identical bits.
  * Checks beyond the cache's: 1 <= requests <= 65534, q_heads a multiple of
  * heads, max_new, max_length, table_width >= 1, window >= 0, scale finite
