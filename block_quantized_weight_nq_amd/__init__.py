@@ -29,10 +29,13 @@ EXPORTS = ["nq_format_count", "nq_format_by_id", "nq_format_query", "nq_validate
            "nq_quantize_grouped_absmax", "nq_validate_quantize_q8_1", "nq_quantize_q8_1",
            "nq_validate_gemv_q8_1", "nq_gemv_q8_1", "nq_validate_gemm_q8_1", "nq_gemm_q8_1_workspace", "nq_gemm_q8_1", "nq_gemm_q8_1_noalloc",
            "nq_kv_tables", "nq_kv_store", "nq_kv_load", "nq_kv_attention_workspace", "nq_kv_attention",
+           "nq_quantize_fp8_block", "nq_dequantize_fp8_block", "nq_gemm_fp8_block_workspace", "nq_gemm_fp8_block",
+           "nq_moe_sort_workspace", "nq_moe_sort", "nq_moe_gather", "nq_moe_combine", "nq_moe_combine_grad",
            "nq_status_string"]
 GEMV_MAX_M = 8
 GQ_SCHEMES = {"q4_g64_fp16": (0, 64), "q5_g64_fp16": (1, 64), "q6_g64_fp16": (2, 64), "q8_g32_fp16": (3, 32)}
 KV_CODES = {"q8": 0, "e4m3": 1}
+FP8_BLOCK, MOE_MAX_EXPERTS = 128, 1024
 KV_DIMS, KV_BLOCKS = (64, 128, 256), (16, 32, 64, 128)
 FP8_ROW_KINDS = {"fp8_e4m3fn_row_bf16": 0, "fp8_e4m3fn_row_fp16": 1}
 
@@ -75,6 +78,20 @@ class KvAttentionArgs(ctypes.Structure):
                 ("table_width", ctypes.c_int64), ("table_stride", ctypes.c_int64), ("window", ctypes.c_int64),
                 ("max_new", ctypes.c_int64), ("max_length", ctypes.c_int64), ("out", ctypes.c_void_p),
                 ("lse", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class MoePlanDesc(ctypes.Structure):
+    """nq_moe_plan."""
+    _fields_ = [("order", ctypes.c_void_p), ("places", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
+                ("tokens", ctypes.c_int64), ("top", ctypes.c_int64), ("experts", ctypes.c_int64)]
+
+
+class Fp8BlockArgs(ctypes.Structure):
+    """nq_fp8_block_args."""
+    _fields_ = [("x", ctypes.c_void_p), ("x_row_stride", ctypes.c_int64), ("x_scales", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("weight_scales", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("x_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("gated", ctypes.c_int32), ("sorted", ctypes.c_int32)]
 
 
 _LIB = None
@@ -134,6 +151,21 @@ def _lib():
         # (the arguments: a KvAttentionArgs by reference, or its bytes)
         L.nq_kv_attention_workspace.argtypes = [c.POINTER(KvCacheDesc), c.c_void_p, c.POINTER(c.c_uint64)]
         L.nq_kv_attention.argtypes = [c.POINTER(KvCacheDesc), c.c_void_p, c.c_void_p, c.c_uint64, c.c_void_p]
+        L.nq_quantize_fp8_block.argtypes = [c.c_void_p, c.c_int32, c.c_int64, c.c_int64, c.c_int64, c.c_int64, c.c_int32,
+                                            c.c_void_p, c.c_void_p, c.c_void_p]
+        L.nq_dequantize_fp8_block.argtypes = [c.c_void_p, c.c_void_p, c.c_int64, c.c_int64, c.c_int64, c.c_int32,
+                                              c.c_int32, c.c_void_p, c.c_void_p]
+        # (the arguments: an Fp8BlockArgs by reference, or its bytes)
+        L.nq_gemm_fp8_block_workspace.argtypes = [c.c_void_p, c.POINTER(MoePlanDesc), c.POINTER(c.c_uint64)]
+        L.nq_gemm_fp8_block.argtypes = [c.c_void_p, c.POINTER(MoePlanDesc), c.c_void_p, c.c_uint64, c.c_void_p]
+        L.nq_moe_sort_workspace.argtypes = [c.c_int64, c.c_int64, c.c_int64, c.POINTER(c.c_uint64)]
+        L.nq_moe_sort.argtypes = [c.c_void_p, c.c_int32, c.c_int64, c.c_int64, c.c_int64, c.c_void_p, c.c_void_p,
+                                  c.c_void_p, c.c_void_p, c.c_uint64, c.c_void_p]
+        L.nq_moe_gather.argtypes = [c.POINTER(MoePlanDesc), c.c_void_p, c.c_int64, c.c_int64, c.c_void_p, c.c_void_p]
+        L.nq_moe_combine.argtypes = [c.POINTER(MoePlanDesc), c.c_void_p, c.c_int64, c.c_int32, c.c_int64, c.c_void_p,
+                                     c.c_void_p, c.c_void_p]
+        L.nq_moe_combine_grad.argtypes = [c.POINTER(MoePlanDesc), c.c_void_p, c.c_int64, c.c_void_p, c.c_int64, c.c_int32,
+                                          c.c_int64, c.c_void_p, c.c_void_p, c.c_void_p, c.c_void_p]
         L.nq_status_string.argtypes = [c.c_int]
         L.nq_status_string.restype = c.c_char_p
         _LIB = L
@@ -631,17 +663,17 @@ KvStep = collections.namedtuple("KvStep", "lengths token_start slots free_state 
 # nq_kv_attention_args as packed bytes (the fields of KvAttentionArgs, in its layout).
 _ATTENTION_ARGS = struct.Struct("@PqqqqqPPPqqqqqPPif")
 assert _ATTENTION_ARGS.size == ctypes.sizeof(KvAttentionArgs)
-_I32 = _I64 = _F32 = _U8 = _STREAM = _DEVICE = None
+_I32 = _I64 = _F32 = _U8 = _F8 = _STREAM = _DEVICE = None
 _KV_DTYPES = {}
 
 
 def _torch_names():
     """torch's names that the calls below use, looked up at the first of them."""
-    global _I32, _I64, _F32, _U8, _STREAM, _DEVICE
+    global _I32, _I64, _F32, _U8, _F8, _STREAM, _DEVICE
     import torch
     _KV_DTYPES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
     _I64, _F32, _U8, _STREAM = torch.int64, torch.float32, torch.uint8, torch._C._cuda_getCurrentRawStream
-    _DEVICE = torch._C._cuda_getDevice
+    _DEVICE, _F8 = torch._C._cuda_getDevice, torch.float8_e4m3fn
     _I32 = torch.int32
 
 
@@ -837,3 +869,324 @@ def kv_attention(cache, q, token_start, lengths, table, scale=None, window=0, ma
         raise NqError(st, f"q {list(q.shape)} {q.dtype}, {requests} requests, table {list(table.shape)}, "
                           f"window {window}, max_new {max_new}, max_length {max_length}")
     return (out, lse) if return_lse else out
+
+
+# --- E4M3 blocks of 128, and rows sorted by expert ----------------------------------------------------------------
+
+_BLOCK_ARGS = struct.Struct("@PqPPPPqqqiiii")
+assert _BLOCK_ARGS.size == ctypes.sizeof(Fp8BlockArgs)
+
+
+def _block_shapes(shape, tile):
+    """(matrices, rows, cols, shape of the scales) of a [rows, cols] or [matrices, rows, cols] tensor."""
+    if tile not in (1, FP8_BLOCK):
+        raise ValueError(f"tile must be 1 or {FP8_BLOCK}")
+    if len(shape) not in (2, 3):
+        raise ValueError("a matrix [rows, cols] or several [matrices, rows, cols] are wanted")
+    rows, cols = shape[-2], shape[-1]
+    return (shape[0] if len(shape) == 3 else 1), rows, cols, (*shape[:-2], -(-rows // tile), cols // FP8_BLOCK)
+
+
+def quantize_fp8_block(x, tile=1, stream=None):
+    """E4M3 codes and binary32 scales of x, [rows, cols] or [matrices, rows, cols] (float32, float16 or bfloat16,
+    columns contiguous, any row stride): one scale for each 128 columns of `tile` rows, 1 for activations and 128 for
+    weights.  cols must be a multiple of 128.  What is not finite becomes NaN.  Returns (codes float8_e4m3fn in x's
+    shape, scales float32 [..., ceil(rows / tile), cols / 128])."""
+    if _I32 is None:
+        _torch_names()
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    index = x.get_device()
+    if stream is not None:
+        with _on(stream, index):
+            return quantize_fp8_block(x, tile)
+    if _DEVICE() != index:
+        with _at(index):
+            return quantize_fp8_block(x, tile)
+    shape, strides = x.shape, x.stride()
+    matrices, rows, cols, scales_shape = _block_shapes(shape, tile)
+    if strides[-1] != 1 and x.numel() or (len(shape) == 3 and matrices > 1 and strides[0] != rows * strides[1]):
+        raise ValueError("x must have contiguous columns, and matrices must follow each other row by row")
+    codes = x.new_empty(shape, dtype=_F8)
+    scales = x.new_empty(scales_shape, dtype=_F32)
+    st = (_LIB or _lib()).nq_quantize_fp8_block(x.data_ptr(), _kv_dtype(x.dtype), matrices, rows, cols, strides[-2], tile,
+                                                codes.data_ptr(), scales.data_ptr(), _STREAM(index))
+    if st != NQ_OK:
+        raise NqError(st, f"x {list(shape)} {x.dtype}, tile {tile}")
+    return codes, scales
+
+
+def _scales_of(name, scales, shape, index):
+    if scales.dtype is not _F32 or tuple(scales.shape) != tuple(shape) or scales.get_device() != index or \
+            not scales.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor {list(shape)} on CUDA device {index}")
+
+
+def dequantize_fp8_block(codes, scales, tile=1, out_dtype=None, stream=None):
+    """The values of E4M3 codes and their scales (as quantize_fp8_block returns them) in out_dtype (default float32)."""
+    if _I32 is None:
+        _torch_names()
+    index = codes.get_device()
+    if not codes.is_cuda or codes.dtype is not _F8 or not codes.is_contiguous():
+        raise ValueError("codes must be a contiguous float8_e4m3fn CUDA tensor")
+    if stream is not None:
+        with _on(stream, index):
+            return dequantize_fp8_block(codes, scales, tile, out_dtype)
+    if _DEVICE() != index:
+        with _at(index):
+            return dequantize_fp8_block(codes, scales, tile, out_dtype)
+    matrices, rows, cols, scales_shape = _block_shapes(codes.shape, tile)
+    _scales_of("scales", scales, scales_shape, index)
+    out = codes.new_empty(codes.shape, dtype=out_dtype or _F32)
+    st = (_LIB or _lib()).nq_dequantize_fp8_block(codes.data_ptr(), scales.data_ptr(), matrices, rows, cols, tile,
+                                                  _kv_dtype(out.dtype), out.data_ptr(), _STREAM(index))
+    if st != NQ_OK:
+        raise NqError(st, f"codes {list(codes.shape)} as {out.dtype}")
+    return out
+
+
+class Fp8Weight:
+    """A linear layer's weight in E4M3 blocks: codes float8_e4m3fn [N, K], or [experts, N, K] for one of each expert;
+    scales float32 [..., ceil(N / 128), K / 128].  Contiguous CUDA tensors that the caller owns."""
+
+    def __init__(self, codes, scales):
+        if _I32 is None:
+            _torch_names()
+        if codes.dtype is not _F8 or codes.dim() not in (2, 3) or not codes.is_cuda or not codes.is_contiguous():
+            raise ValueError("codes must be a contiguous float8_e4m3fn CUDA tensor [N, K] or [experts, N, K]")
+        self.N, self.K = codes.shape[-2:]
+        self.experts = codes.shape[0] if codes.dim() == 3 else 0
+        if self.N < 1 or self.K < 1 or self.K % FP8_BLOCK or (codes.dim() == 3 and not 1 <= self.experts <= MOE_MAX_EXPERTS):
+            raise ValueError(f"N and K must be positive, K a multiple of {FP8_BLOCK}, experts 1 to {MOE_MAX_EXPERTS}")
+        self.device, self.index = codes.device, codes.get_device()
+        _scales_of("scales", scales, (*codes.shape[:-2], -(-self.N // FP8_BLOCK), self.K // FP8_BLOCK), self.index)
+        self.codes, self.scales = codes, scales
+        self._workspaces = {}
+
+    @classmethod
+    def quantize(cls, weight, stream=None):
+        """From values: [N, K] or [experts, N, K] (float32, float16 or bfloat16)."""
+        return cls(*quantize_fp8_block(weight, FP8_BLOCK, stream))
+
+
+class MoePlan:
+    """A router's pairs (token, choice) in the experts' order, as moe_sort returns them: order int32 [tokens * top], the
+    pair token * top + choice at each place (-1 behind the last), places int32 [tokens, top], the place of each pair
+    (-1: left out), offsets int32 [experts + 1], the first place of each expert."""
+
+    def __init__(self, order, places, offsets):
+        if _I32 is None:
+            _torch_names()
+        if not order.is_cuda:
+            raise ValueError("the plan's tensors must be CUDA tensors")
+        self.index = order.get_device()
+        _refuse_other(self.index, (("order", order, _I32), ("places", places, _I32), ("offsets", offsets, _I32)))
+        if places.dim() != 2 or order.numel() != places.numel() or not 2 <= offsets.numel() <= MOE_MAX_EXPERTS + 1:
+            raise ValueError("places must be [tokens, top], order one entry for each pair, offsets experts + 1")
+        self.order, self.places, self.offsets = order, places, offsets
+        self.tokens, self.top = places.shape
+        self.pairs, self.experts, self.device = order.numel(), offsets.numel() - 1, order.device
+        self._ref = ctypes.byref(MoePlanDesc(order.data_ptr(), places.data_ptr(), offsets.data_ptr(), self.tokens,
+                                             self.top, self.experts))
+
+
+def _refuse_other(index, ints):
+    """As _refuse, where any of them is not what the call needs."""
+    for _, t, dtype in ints:
+        if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+            _refuse(index, None, 0, ints)
+
+
+def _rows_of(name, x, rows, cols, index):
+    shape = x.shape
+    if len(shape) != 2 or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols) or \
+            x.get_device() != index or (x.stride(1) != 1 and x.numel()):
+        raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, {'cols' if cols is None else cols}] on CUDA "
+                         f"device {index}, columns contiguous")
+
+
+def _block_product(weight, x, x_scales, plan, sorted_rows, gated, out_dtype):
+    index, n, k = weight.index, weight.N, weight.K
+    if plan is None:
+        rows, wanted = x.shape[0], None
+        out_rows = rows
+    else:
+        if plan.index != index or plan.experts != weight.experts:
+            raise ValueError("the plan must be one of the weight's experts and device")
+        wanted = rows = plan.pairs if sorted_rows else plan.tokens
+        out_rows = plan.pairs
+    _rows_of("x", x, wanted, k, index)
+    pointer, stride, dtype = x.data_ptr(), x.stride(0), x.dtype
+    if x_scales is None:
+        code, xs = _kv_dtype(dtype), 0
+        out_dtype = out_dtype or dtype
+    else:
+        if dtype is not _F8:
+            raise ValueError("x must be float8_e4m3fn where x_scales is given")
+        _scales_of("x_scales", x_scales, (rows, k // FP8_BLOCK), index)
+        code, xs = 3, x_scales.data_ptr()
+        out_dtype = out_dtype or _F32
+    out_code = _kv_dtype(out_dtype)
+    out = x.new_empty((out_rows, n // 2 if gated else n), dtype=out_dtype)
+    lib, ref = _LIB or _lib(), plan._ref if plan is not None else None
+    args = _BLOCK_ARGS.pack(pointer, stride, xs, weight.codes.data_ptr(), weight.scales.data_ptr(), out.data_ptr(), rows, n, k,
+                            code, out_code, gated, sorted_rows)
+    # the workspace is a function of these alone: asked for once for each
+    sizes = (rows, out_rows, code, out_code, gated, stride & 15, pointer & 15, sorted_rows)
+    need = weight._workspaces.get(sizes)
+    st = NQ_OK
+    if need is None:
+        asked = ctypes.c_uint64()
+        st = lib.nq_gemm_fp8_block_workspace(args, ref, asked)
+        need = asked.value
+        if st == NQ_OK:
+            if len(weight._workspaces) >= 1024:
+                weight._workspaces.clear()
+            weight._workspaces[sizes] = need
+    if st == NQ_OK:
+        ws = x.new_empty(need, dtype=_U8) if need else None
+        st = lib.nq_gemm_fp8_block(args, ref, ws.data_ptr() if need else None, need, _STREAM(index))
+    if st != NQ_OK:
+        raise NqError(st, f"x {list(x.shape)} {dtype}, weight {list(weight.codes.shape)}, gated {gated}")
+    return out
+
+
+def gemm_fp8_block(weight, x, x_scales=None, gated=False, out_dtype=None, stream=None):
+    """x @ w^T for an Fp8Weight [N, K].
+
+    x: [rows, K] float32, float16 or bfloat16 (any row stride), rounded to E4M3 blocks of one row and 128 columns within
+    the call; or codes float8_e4m3fn with x_scales float32 [rows, K / 128], as quantize_fp8_block returns them.
+    gated: the weight's first N / 2 rows are gates, the others up (N a multiple of 256); returns silu(gate) * up,
+    [rows, N / 2].  out_dtype: default x's type (float32 for codes).  Sums are binary32; binary32 outputs and calls of up
+    to 64 rows multiply exactly, others on the 8-bit matrix instructions (include/nq.h states the difference).
+    """
+    if weight.experts:
+        raise ValueError("an [experts, N, K] weight takes moe_gemm_fp8_block")
+    if stream is not None:
+        with _on(stream, weight.index):
+            return _block_product(weight, x, x_scales, None, False, bool(gated), out_dtype)
+    if _DEVICE() != weight.index:
+        with _at(weight.index):
+            return _block_product(weight, x, x_scales, None, False, bool(gated), out_dtype)
+    return _block_product(weight, x, x_scales, None, False, bool(gated), out_dtype)
+
+
+def moe_gemm_fp8_block(weight, x, plan, x_scales=None, sorted_rows=False, gated=False, out_dtype=None, stream=None):
+    """Each expert's product with its own rows, in the plan's order: [pairs, N] (gated: [pairs, N / 2]), zeros behind the
+    last place.  weight: Fp8Weight [experts, N, K]; x: one row for each token, which the product takes in the plan's
+    order, or with sorted_rows one for each place (as a product before this one returned them).  The other arguments
+    are gemm_fp8_block's."""
+    if not weight.experts:
+        raise ValueError("an [N, K] weight takes gemm_fp8_block")
+    if stream is not None:
+        with _on(stream, weight.index):
+            return _block_product(weight, x, x_scales, plan, bool(sorted_rows), bool(gated), out_dtype)
+    if _DEVICE() != weight.index:
+        with _at(weight.index):
+            return _block_product(weight, x, x_scales, plan, bool(sorted_rows), bool(gated), out_dtype)
+    return _block_product(weight, x, x_scales, plan, bool(sorted_rows), bool(gated), out_dtype)
+
+
+def moe_sort(ids, experts, stream=None):
+    """The pairs of a router's choices, ids [tokens, top] (int32 or int64), sorted by expert; those outside 0 ..
+    experts - 1 are left out.  Returns a MoePlan; nothing is copied to the host."""
+    if _I32 is None:
+        _torch_names()
+    if not ids.is_cuda or ids.dim() != 2 or ids.dtype not in (_I32, _I64) or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous CUDA tensor [tokens, top] of int32 or int64")
+    index = ids.get_device()
+    if stream is not None:
+        with _on(stream, index):
+            return moe_sort(ids, experts)
+    if _DEVICE() != index:
+        with _at(index):
+            return moe_sort(ids, experts)
+    tokens, top = ids.shape
+    if not 1 <= experts <= MOE_MAX_EXPERTS or top < 1:
+        raise ValueError(f"experts must be 1 to {MOE_MAX_EXPERTS} and top at least 1")
+    pairs, lib = tokens * top, _LIB or _lib()
+    asked = ctypes.c_uint64()
+    st = lib.nq_moe_sort_workspace(tokens, top, experts, asked)
+    need = asked.value
+    words = ids.new_empty(2 * pairs + experts + 1 + need // 4, dtype=_I32)
+    p = words.data_ptr()
+    if st == NQ_OK:
+        st = lib.nq_moe_sort(ids.data_ptr(), ids.dtype is _I64, tokens, top, experts, p, p + 4 * pairs, p + 8 * pairs,
+                             p + 8 * pairs + 4 * (experts + 1) if need else None, need, _STREAM(index))
+    if st != NQ_OK:
+        raise NqError(st, f"ids {list(ids.shape)}, {experts} experts")
+    order, places, offsets = words[:2 * pairs + experts + 1].split_with_sizes((pairs, pairs, experts + 1))
+    return MoePlan(order, places.view(tokens, top), offsets)
+
+
+def moe_gather(x, plan, stream=None):
+    """The rows of x [tokens, cols] (any type, columns contiguous) in the plan's order, [pairs, cols], zeros behind the last
+    place.  The gradient of x is moe_combine(gradient of the rows, plan)."""
+    index = plan.index
+    if stream is not None:
+        with _on(stream, index):
+            return moe_gather(x, plan)
+    if _DEVICE() != index:
+        with _at(index):
+            return moe_gather(x, plan)
+    _rows_of("x", x, plan.tokens, None, index)
+    size, cols = x.element_size(), x.shape[1]
+    out = x.new_empty((plan.pairs, cols))
+    st = (_LIB or _lib()).nq_moe_gather(plan._ref, x.data_ptr(), cols * size, x.stride(0) * size, out.data_ptr(), _STREAM(index))
+    if st != NQ_OK:
+        raise NqError(st, f"x {list(x.shape)} {x.dtype}")
+    return out
+
+
+def _weights_of(weights, plan):
+    if weights is None:
+        return None
+    _scales_of("weights", weights, (plan.tokens, plan.top), plan.index)
+    return weights.data_ptr()
+
+
+def moe_combine(rows, plan, weights=None, stream=None):
+    """The sorted rows [pairs, cols] (float32, float16 or bfloat16) back to their tokens: [tokens, cols], each the sum of
+    its rows times weights (float32 [tokens, top], 1 if not given), summed in binary32 in the order of the choices."""
+    index = plan.index
+    if stream is not None:
+        with _on(stream, index):
+            return moe_combine(rows, plan, weights)
+    if _DEVICE() != index:
+        with _at(index):
+            return moe_combine(rows, plan, weights)
+    _rows_of("rows", rows, plan.pairs, None, index)
+    cols = rows.shape[1]
+    out = rows.new_empty((plan.tokens, cols))
+    st = (_LIB or _lib()).nq_moe_combine(plan._ref, rows.data_ptr(), rows.stride(0), _kv_dtype(rows.dtype), cols,
+                                         _weights_of(weights, plan), out.data_ptr(), _STREAM(index))
+    if st != NQ_OK:
+        raise NqError(st, f"rows {list(rows.shape)} {rows.dtype}")
+    return out
+
+
+def moe_combine_grad(grad, rows, plan, weights=None, stream=None):
+    """The gradients of moe_combine(rows, plan, weights) for its result's gradient grad [tokens, cols] (rows' type):
+    (grad_rows [pairs, cols] in that type, 0 behind the last place; grad_weights float32 [tokens, top], 0 for pairs left
+    out, None without weights)."""
+    index = plan.index
+    if stream is not None:
+        with _on(stream, index):
+            return moe_combine_grad(grad, rows, plan, weights)
+    if _DEVICE() != index:
+        with _at(index):
+            return moe_combine_grad(grad, rows, plan, weights)
+    _rows_of("rows", rows, plan.pairs, None, index)
+    cols = rows.shape[1]
+    _rows_of("grad", grad, plan.tokens, cols, index)
+    if grad.dtype is not rows.dtype:
+        raise ValueError("grad must have the rows' type")
+    out = rows.new_empty((plan.pairs, cols))
+    pointer = _weights_of(weights, plan)
+    out_weights = weights.new_empty(weights.shape) if weights is not None else None
+    st = (_LIB or _lib()).nq_moe_combine_grad(plan._ref, grad.data_ptr(), grad.stride(0), rows.data_ptr(), rows.stride(0),
+                                              _kv_dtype(rows.dtype), cols, pointer, out.data_ptr(),
+                                              out_weights.data_ptr() if weights is not None else None, _STREAM(index))
+    if st != NQ_OK:
+        raise NqError(st, f"rows {list(rows.shape)} {rows.dtype}")
+    return out, out_weights

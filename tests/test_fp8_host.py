@@ -1,0 +1,230 @@
+"""E4M3 blocks and the experts' rows on the host: argument checks of the C ABI, the binding's devices and streams, the
+launch plan and the tile rule against the tensors (no GPU)."""
+import ctypes
+import fcntl
+import os
+import subprocess
+import types
+
+import numpy as np
+import pytest
+import torch
+
+import block_quantized_weight_nq_amd as nq
+from test_binding_device import Tensor, gpus  # noqa: F401
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+SAN = os.environ.get("NQ_SANITIZE") == "1"
+EMU = os.path.join(HERE, "emu", "libnq_fp8_emu_san.so" if SAN else "libnq_fp8_emu.so")
+CSRC = os.path.join(os.path.dirname(HERE), "block_quantized_weight_nq_amd", "csrc")
+P = 1 << 20  # an aligned address that no refused call reads
+
+
+# --- refusals ---------------------------------------------------------------------------------------------------
+
+def quantize(x=P, dtype=0, matrices=1, rows=4, cols=256, stride=256, tile=1, codes=P, scales=P):
+    return nq.library().nq_quantize_fp8_block(x, dtype, matrices, rows, cols, stride, tile, codes, scales, None)
+
+
+@pytest.mark.parametrize("kw, status", [
+    (dict(dtype=3), 8), (dict(dtype=-1), 8), (dict(rows=-1), 4), (dict(cols=-128), 4), (dict(matrices=-1), 4), (dict(tile=64), 4),
+    (dict(tile=0), 4), (dict(cols=100), 5), (dict(cols=200, rows=0), 5), (dict(rows=2 ** 30 + 1), 7), (dict(cols=2 ** 31), 7),
+    (dict(rows=2 ** 30, cols=2 ** 30), 7), (dict(matrices=2 ** 30, rows=2 ** 30), 7), (dict(stride=-1), 4),
+    (dict(stride=2 ** 60), 7), (dict(x=0), 1), (dict(codes=0), 1), (dict(scales=0), 1), (dict(x=P + 2), 11), (dict(dtype=2, x=P + 1), 11),
+    (dict(codes=P + 8), 11), (dict(scales=P + 2), 11), (dict(rows=0, x=0, codes=0, scales=0), 0), (dict(cols=0, x=0), 0)])
+def test_quantize_refuses(kw, status):
+    assert quantize(**kw) == status
+
+
+@pytest.mark.parametrize("kw, status", [
+    (dict(dtype=3), 8), (dict(rows=-1), 4), (dict(cols=130), 5), (dict(tile=2), 4), (dict(rows=2 ** 31), 7), (dict(codes=0), 1),
+    (dict(scales=0), 1), (dict(out=0), 1), (dict(codes=P + 4), 11), (dict(scales=P + 1), 11), (dict(out=P + 8), 11), (dict(rows=0, out=0), 0)])
+def test_values_refuse(kw, status):
+    a = dict(codes=P, scales=P, matrices=1, rows=4, cols=256, tile=1, dtype=0, out=P)
+    a.update(kw)
+    assert nq.library().nq_dequantize_fp8_block(*a.values(), None) == status
+
+
+ARGS = dict(x=P, x_row_stride=256, x_scales=0, weight=P, weight_scales=P, out=P, rows=4, N=512, K=256, x_dtype=2, out_dtype=2,
+            gated=0, sorted=0)
+PLAN = dict(order=P, places=P, offsets=P, tokens=4, top=2, experts=8)
+
+
+def product(plan=None, ws=0, ws_bytes=0, asked=False, **kw):
+    args = nq.Fp8BlockArgs(*{**ARGS, **kw}.values())
+    plan = ctypes.byref(nq.MoePlanDesc(*{**PLAN, **plan}.values())) if plan is not None else None
+    need = ctypes.c_uint64(77)
+    L = nq.library()
+    st = L.nq_gemm_fp8_block_workspace(ctypes.byref(args), plan, need)
+    assert st == 0 or need.value == 0
+    if asked:
+        return st, need.value
+    return L.nq_gemm_fp8_block(ctypes.byref(args), plan, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw, status", [
+    (dict(x_dtype=3), 8), (dict(out_dtype=3), 8), (dict(out_dtype=-1), 8), (dict(rows=-1), 4), (dict(N=0), 4), (dict(K=0), 4),
+    (dict(gated=2), 4), (dict(sorted=1), 4), (dict(K=192), 5), (dict(gated=1, N=384), 5), (dict(rows=2 ** 30 + 1), 7),
+    (dict(N=2 ** 31), 7), (dict(K=2 ** 31), 7), (dict(x_row_stride=-1), 4), (dict(x_row_stride=2 ** 60), 7),
+    (dict(rows=2 ** 30, N=2 ** 30), 7), (dict(x_scales=P, x_row_stride=264), 11)])
+def test_product_and_workspace_refuse(kw, status):
+    assert product(asked=True, **kw) == (status, 0)
+    assert product(**kw) == status
+
+
+@pytest.mark.parametrize("kw, status", [
+    (dict(x=0), 1), (dict(weight=0), 1), (dict(weight_scales=0), 1), (dict(out=0), 1), (dict(x=P + 1), 11), (dict(weight=P + 8), 11),
+    (dict(weight_scales=P + 2), 11), (dict(out=P + 4), 11), (dict(x_scales=P + 2), 11), (dict(x_scales=P, x=P + 8), 11),
+    (dict(ws=P + 8), 11), (dict(rows=300), 12), (dict(rows=300, ws=P, ws_bytes=4096), 12), (dict(rows=0, x=0, out=0), 0)])
+def test_product_refuses_pointers_and_workspace(kw, status):
+    assert product(**kw) == status
+
+
+@pytest.mark.parametrize("plan, kw, status", [
+    (dict(), dict(rows=5), 4), (dict(), dict(sorted=1), 4), (dict(tokens=-1), {}, 4), (dict(top=0), {}, 4), (dict(experts=0), {}, 4),
+    (dict(experts=1025), {}, 7), (dict(tokens=2 ** 29, top=4), {}, 7), (dict(offsets=0), {}, 1), (dict(order=0), {}, 1),
+    (dict(places=0), {}, 1), (dict(order=P + 2), {}, 11), (dict(offsets=P + 1), {}, 11)])
+def test_product_refuses_plans(plan, kw, status):
+    assert product(plan=plan, **kw) == status
+    assert product(plan=plan, asked=True, **kw)[0] == status
+
+
+def test_empty_plan_launches_nothing():
+    assert product(plan=dict(tokens=0, order=0, places=0), rows=0, x=0, out=0) == 0
+
+
+@pytest.mark.parametrize("kw, status", [
+    (dict(tokens=-1), 4), (dict(top=0), 4), (dict(experts=0), 4), (dict(experts=1025), 7), (dict(tokens=2 ** 30, top=2), 7),
+    (dict(wide=2), 8), (dict(ids=0), 1), (dict(order=0), 1), (dict(places=0), 1), (dict(offsets=0), 1), (dict(ids=P + 4, wide=1), 11),
+    (dict(ids=P + 2), 11), (dict(order=P + 2), 11), (dict(ws=P + 1), 11), (dict(tokens=5000), 12), (dict(tokens=5000, ws=P, ws_bytes=12), 12)])
+def test_sort_refuses(kw, status):
+    a = dict(ids=P, wide=0, tokens=9, top=2, experts=8, order=P, places=P, offsets=P, ws=0, ws_bytes=0)
+    a.update(kw)
+    assert nq.library().nq_moe_sort(*a.values(), None) == status
+
+
+@pytest.mark.parametrize("plan, kw, status", [
+    ({}, dict(dtype=3), 8), ({}, dict(cols=-1), 4), ({}, dict(cols=2 ** 31), 7), ({}, dict(stride=-1), 4), ({}, dict(stride=2 ** 60), 7),
+    ({}, dict(rows=0), 1), ({}, dict(out=0), 1), ({}, dict(rows=P + 2), 11), ({}, dict(weights=P + 2), 11), ({}, dict(out=P + 1), 11),
+    (dict(tokens=0, order=0, places=0), {}, 0), ({}, dict(cols=0), 0), (dict(places=0), {}, 1)])
+def test_combine_refuses(plan, kw, status):
+    d = nq.MoePlanDesc(*{**PLAN, **plan}.values())
+    a = dict(rows=P, stride=64, dtype=0, cols=64, weights=P, out=P)
+    a.update(kw)
+    L = nq.library()
+    assert L.nq_moe_combine(ctypes.byref(d), *a.values(), None) == status
+    if not kw.get("cols") == 0:
+        st = L.nq_moe_combine_grad(ctypes.byref(d), P, a["stride"], a["rows"], a["stride"], a["dtype"], a["cols"], a["weights"],
+                                   a["out"], P, None)
+        assert st == status
+
+
+@pytest.mark.parametrize("plan, kw, status", [
+    ({}, dict(nbytes=-1), 4), ({}, dict(nbytes=2 ** 33), 7), ({}, dict(stride=-4), 4), ({}, dict(x=0), 1), ({}, dict(out=0), 1),
+    ({}, dict(nbytes=0, x=0), 0), (dict(experts=0), {}, 4)])
+def test_gather_refuses(plan, kw, status):
+    d = nq.MoePlanDesc(*{**PLAN, **plan}.values())
+    a = dict(x=P, nbytes=64, stride=64, out=P)
+    a.update(kw)
+    assert nq.library().nq_moe_gather(ctypes.byref(d), *a.values(), None) == status
+
+
+def test_null_arguments():
+    L = nq.library()
+    need = ctypes.c_uint64(5)
+    assert L.nq_gemm_fp8_block_workspace(None, None, need) == 1 and need.value == 0
+    assert L.nq_gemm_fp8_block(None, None, None, 0, None) == 1
+    assert L.nq_moe_sort_workspace(1, 1, 1, None) == 1
+    assert L.nq_moe_gather(None, P, 4, 4, P, None) == 1
+    assert L.nq_moe_combine(None, P, 4, 0, 4, None, P, None) == 1
+
+
+# --- the binding ------------------------------------------------------------------------------------------------
+
+def block_calls(index):
+    f8 = lambda *shape: Tensor(shape, torch.float8_e4m3fn, index)  # noqa: E731
+    f32 = lambda *shape: Tensor(shape, torch.float32, index)  # noqa: E731
+    i32 = lambda *shape: Tensor(shape, torch.int32, index)  # noqa: E731
+    one, many = nq.Fp8Weight(f8(256, 128), f32(2, 1)), nq.Fp8Weight(f8(4, 256, 128), f32(4, 2, 1))
+    plan = nq.MoePlan(i32(6), i32(3, 2), i32(5))
+    x = Tensor((3, 128), torch.bfloat16, index)
+    rows = f32(6, 8)
+    return [
+        lambda **kw: nq.quantize_fp8_block(x, **kw), lambda **kw: nq.dequantize_fp8_block(f8(3, 128), f32(3, 1), **kw),
+        lambda **kw: nq.gemm_fp8_block(one, x, **kw), lambda **kw: nq.moe_gemm_fp8_block(many, x, plan, **kw),
+        lambda **kw: nq.moe_gather(x, plan, **kw), lambda **kw: nq.moe_combine(rows, plan, f32(3, 2), **kw),
+        lambda **kw: nq.moe_combine_grad(f32(3, 8), rows, plan, f32(3, 2), **kw)]
+
+
+@pytest.mark.parametrize("index", [0, 1])
+def test_calls_run_on_their_tensors_device(gpus, index):  # noqa: F811
+    Tensor.element_size = lambda self: 4
+    for call in block_calls(index):
+        gpus.calls.clear()
+        call()
+        assert gpus.calls and all(device == index for _, device in gpus.calls), gpus.calls
+        assert gpus.device == 0
+
+
+def test_a_stream_is_of_the_tensors_device(gpus):  # noqa: F811
+    Tensor.element_size = lambda self: 4
+    for call in block_calls(1):
+        gpus.calls.clear()
+        call(stream=types.SimpleNamespace(device=torch.device("cuda", 1)))
+        assert gpus.calls and all(device == 1 for _, device in gpus.calls)
+        gpus.calls.clear()
+        with pytest.raises(ValueError, match="stream"):
+            call(stream=types.SimpleNamespace(device=torch.device("cuda", 0)))
+        assert not gpus.calls and gpus.device == 0
+
+
+# --- the tile rule ----------------------------------------------------------------------------------------------
+
+@pytest.fixture(scope="module")
+def emu():
+    src = os.path.join(HERE, "emu", "nq_fp8_emu.hip")
+    deps = [src, os.path.join(CSRC, "nq_fp8b.h")]
+    with open(EMU + ".lock", "w") as lk:
+        fcntl.flock(lk, fcntl.LOCK_EX)
+        if not os.path.exists(EMU) or any(os.path.getmtime(d) > os.path.getmtime(EMU) for d in deps):
+            from emu_lib import SAN_FLAGS
+            tmp = f"{EMU}.{os.getpid()}.tmp"
+            subprocess.run(["hipcc", "-x", "hip", "--offload-host-only", "-O1", "-std=c++17", "-fPIC", "-shared",
+                            "-fvisibility=hidden", *(SAN_FLAGS if SAN else []), src, "-o", tmp], check=True)
+            os.replace(tmp, EMU)
+    L = ctypes.CDLL(EMU)
+    L.nq_fp8_emu_tiles.restype = ctypes.c_int64
+    L.nq_fp8_emu_tiles.argtypes = [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p]
+    return L
+
+
+def tiles(emu, offsets, rows, bm):
+    """How often each row is in a tile and of which expert; -1 is behind the last."""
+    hits, expert = np.zeros(rows + 1, np.int32), np.full(rows + 1, -9, np.int32)
+    o = np.array(offsets, np.int32)
+    bad = emu.nq_fp8_emu_tiles(o.ctypes.data, o.size - 1, rows, bm, hits.ctypes.data, expert.ctypes.data)
+    return bad, hits, expert
+
+
+@pytest.mark.parametrize("bm", [16, 32, 64, 128, 256])
+def test_tiles_cover_each_row_once(emu, bm):
+    rng = np.random.default_rng(bm)
+    for trial in range(60):
+        experts = int(rng.choice([1, 2, 5, 63, 64, 65, 200]))
+        counts = rng.choice([0, 0, 1, bm - 1, bm, bm + 1, 3 * bm + 5], experts)
+        offsets = np.concatenate([[0], np.cumsum(counts)])
+        rows = int(offsets[-1]) + int(rng.choice([0, 0, 1, bm, 2 * bm + 3]))
+        if rows == 0:
+            continue
+        bad, hits, expert = tiles(emu, offsets, rows, bm)
+        assert bad == 0 and (hits[:rows] == 1).all() and hits[rows] == 0
+        want = np.repeat(np.arange(experts), counts)
+        assert np.array_equal(expert[: offsets[-1]], want) and (expert[offsets[-1]:rows] == -1).all()
+
+
+def test_tiles_of_any_offsets_stay_inside(emu):
+    rng = np.random.default_rng(0)
+    for trial in range(300):
+        experts, rows = int(rng.choice([1, 3, 64, 70])), int(rng.choice([1, 17, 300]))
+        offsets = rng.choice([-2 ** 31, -5, 0, 1, rows - 1, rows, rows + 1, 2 ** 31 - 1], experts + 1)
+        assert tiles(emu, offsets, rows, int(rng.choice([16, 64, 256])))[0] == 0
