@@ -31,14 +31,14 @@ struct XPart {
 };
 
 template <int XT>
-__device__ __forceinline__ void read_x(const Fp8GemmLaunch &a, const uint8_t *row, const float *scale, int32_t kb, int g, XPart<XT> &p) {
+__device__ __forceinline__ void read_x(const uint8_t *row, const float *scale, int32_t kb, int g, XPart<XT> &p) {
     constexpr int ESZ = XT == 0 ? 4 : XT == FB_CODES ? 1 : 2, N = 16 * ESZ / 16;
     const uint8_t *at = row + ((int64_t)kb * FB + 16 * g) * ESZ;
 #pragma unroll
     for (int h = 0; h < 2; h++)
 #pragma unroll
         for (int i = 0; i < N; i++) p.v[h * N + i] = ((const kv_u4 *)(at + h * 64 * ESZ))[i];
-    if constexpr (XT == FB_CODES) p.scale = scale[(int64_t)kb * a.x_scale_col];
+    if constexpr (XT == FB_CODES) p.scale = scale[kb];
 }
 
 // The row's scale of the block, and the lane's 32 codes of it as binary16.
@@ -127,7 +127,7 @@ __global__ __launch_bounds__(64 * MAX_WAVES) void k_fp8_few(Fp8GemmLaunch a) {
         const int m = 16 * i + j;
         const int64_t r = fb_source_row(a, t.first + (m < t.count ? m : t.count - 1));
         x[i] = (const uint8_t *)a.x + r * a.x_stride * (XT == 0 ? 4 : XT == FB_CODES ? 1 : 2);
-        xs[i] = XT == FB_CODES ? a.x_scales + r * a.x_scale_row : nullptr;
+        xs[i] = XT == FB_CODES ? a.x_scales + r * (a.K / FB) : nullptr;
     }
     kv_f4 acc[RT][NT];
 #pragma unroll
@@ -148,7 +148,7 @@ __global__ __launch_bounds__(64 * MAX_WAVES) void k_fp8_few(Fp8GemmLaunch a) {
             p.ws[i] = ws[i][kb];
         }
 #pragma unroll
-        for (int r = 0; r < RT; r++) read_x<XT>(a, x[r], xs[r], kb, g, p.x[r]);
+        for (int r = 0; r < RT; r++) read_x<XT>(x[r], xs[r], kb, g, p.x[r]);
     };
     const auto multiply = [&](const Part &p) {
         kv_h8 xc[RT][4];
@@ -208,7 +208,7 @@ __global__ __launch_bounds__(64 * MAX_WAVES) void k_fp8_few(Fp8GemmLaunch a) {
         if constexpr (GATED) {
             const kv_f4 up = total(i + PER);
 #pragma unroll
-            for (int k = 0; k < 4; k++) f[k] = fb_silu(f[k]) * up[k];
+            for (int k = 0; k < 4; k++) f[k] = fb_silu<0>(f[k]) * up[k];
         }
         const int m = 16 * r + (at & 15), n = n0 + 16 * i + 4 * (at >> 4);
         if (m >= t.count) continue;

@@ -34,7 +34,7 @@ __global__ __launch_bounds__(TB) void k_fp8_quant_rows(Fp8QuantLaunch a) {
         }
         const float scale = fmaxf(__builtin_bit_cast(float, top) / 448.0f, FB_TINY), inv = 1.0f / scale;
         *(kv_u2 *)(a.codes + r * a.cols + b * FB + 8 * lane) = fb_codes8(f, inv);
-        if (lane == 0) a.scales[r * a.scale_row + b * a.scale_col] = scale;
+        if (lane == 0) a.scales[i] = scale;
     }
 }
 
@@ -78,7 +78,7 @@ __global__ __launch_bounds__(TB) void k_fp8_quant_tile(Fp8QuantLaunch a) {
             for (int k = 0; k < 8; k++) fb_mark_not_finite(f[k]);
         }
         const float scale = fmaxf(__builtin_bit_cast(float, top) / 448.0f, FB_TINY), inv = 1.0f / scale;
-        if (tid == 0) a.scales[band * a.scale_row + b * a.scale_col] = scale;
+        if (tid == 0) a.scales[i] = scale;
 #pragma unroll
         for (int k = 0; k < 8; k++) {
             const int r = r0 + 16 * k;

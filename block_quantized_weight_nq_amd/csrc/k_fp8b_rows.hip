@@ -7,43 +7,72 @@
 // whose scale is one register, and the weight's scale is one for all lanes.
 #include "nq_fp8b_codes.h"
 
+#include <type_traits>
+
 namespace nq {
 
 typedef int fb_i8 __attribute__((ext_vector_type(8)));
 
 namespace {
 
+typedef __attribute__((address_space(1))) const void *fb_global;
+typedef __attribute__((address_space(3))) void *fb_lds;
+
 // LDS holds rows of 128 bytes as eight pieces of 16; piece c of row r lies at c ^ (r / 2 % 8), so that sixteen lanes
 // that read one piece of sixteen rows spread over all banks.
-__device__ __forceinline__ uint32_t lds_at(int row, int piece) { return (uint32_t)(row * FB + ((piece ^ (row >> 1 & 7)) << 4)); }
+__device__ __forceinline__ int swizzle(int row, int piece) { return piece ^ (row >> 1 & 7); }
+
+// All loads to LDS and registers are done, and all reads of LDS: what the waves of a workgroup meet on.
+__device__ __forceinline__ void fb_meet() {
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+}
+
+// Workgroup b's tile.  Workgroups go to the eight XCDs in turn; `span` consecutive tiles stay on one, and run along GM
+// row tiles first, so that an XCD's L2 has few weight rows and rows of x at a time.
+constexpr int32_t XCDS = 8, MOST_SPAN = 32, GM = 8;
+__device__ __forceinline__ void place_tile(int64_t b, int32_t span, int64_t tiles_m, int64_t tiles_n, int64_t *m, int64_t *n) {
+    const int64_t turn = b / XCDS, t = (turn / span * XCDS + b % XCDS) * span + turn % span;
+    const int64_t band = t / (GM * tiles_n), in = t - band * GM * tiles_n, left = tiles_m - band * GM, high = left < GM ? left : GM;
+    *m = high > 0 ? band * GM + in % high : tiles_m;
+    *n = high > 0 ? in / high : 0;
+}
 
 }  // namespace
 
-template <int WN, int WM, int TN, int TM, bool WIDE, bool GATED>
-__global__ __launch_bounds__(64 * WN * WM) void k_fp8_rows(Fp8GemmLaunch a) {
-    constexpr int BN = 16 * WN * TN, BM = 16 * WM * TM, THREADS = 64 * WN * WM, STAGE = (BN + BM) * 8 / THREADS;
+// OT: type of the outputs; binary32 ones are products of binary16 matrix instructions.  AT: of a byte's place in x, 32
+// bits where they do.
+template <int WN, int WM, int TN, int TM, int OT, bool GATED, typename AT>
+__global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
+    constexpr bool WIDE = OT == 0;
+    constexpr int BN = 16 * WN * TN, BM = 16 * WM * TM, WAVES = WN * WM;
     constexpr int H = TN / 2;  // a wave's tiles are two halves, each within one row of blocks
-    __shared__ __align__(16) uint8_t lds[2 * (BN + BM) * FB];
+    constexpr int NW = BN / 8 / WAVES, NX = BM / 8 / WAVES;  // loads to LDS of a wave and block: 8 rows each
+    constexpr int SB = 16, NS = BM / 4 / WAVES;  // blocks whose scales are loaded at a time, 4 rows a load
+    __shared__ __align__(1024) uint8_t even[(BN + BM) * FB], odd[(BN + BM) * FB], scales[2 * BM * SB * 4];
     const int tid = threadIdx.x, lane = tid & 63, j = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave % WN, wm = wave / WN;
     const int32_t KB = a.K / FB, NO = GATED ? a.N / 2 : a.N;
-    const int32_t tiles_n = (int32_t)fb_ceil(a.N, BN);
-    const int64_t tile = blockIdx.x;
-    const int32_t tn = (int32_t)(tile % tiles_n);
+    int64_t tile_m, tile_n;
+    place_tile(blockIdx.x, a.span, a.tiles_m, fb_ceil(a.N, BN), &tile_m, &tile_n);
+    if (tile_m >= a.tiles_m) return;
     Fp8Tile t;
     if (a.experts > 0) {
-        t = fb_find_tile(a.offsets, a.experts, a.out_rows, BM, tile / tiles_n);
+        t = fb_find_tile(a.offsets, a.experts, a.out_rows, BM, tile_m);
+        t.expert = __builtin_amdgcn_readfirstlane(t.expert);
+        t.first = __builtin_amdgcn_readfirstlane((int)t.first);  // (rows are at most 2^30)
+        t.count = __builtin_amdgcn_readfirstlane(t.count);
     } else {
         t.expert = 0;
-        t.first = tile / tiles_n * BM;
+        t.first = tile_m * BM;
         t.count = (int32_t)(a.out_rows - t.first < BM ? a.out_rows - t.first : BM);
     }
     if (t.count == 0) return;
     constexpr int OC = GATED ? BN / 2 : BN;
-    const int32_t n0 = tn * OC;
+    const int32_t n0 = (int32_t)tile_n * OC;
     if (t.expert < 0) {
-        for (int i = tid; i < t.count * OC; i += THREADS)
-            if (n0 + i % OC < NO) fb_write1(a.out, (t.first + i / OC) * NO + n0 + i % OC, 0.0f, a.out_dtype);
+        for (int i = tid; i < t.count * OC; i += 64 * WAVES)
+            if (n0 + i % OC < NO) fb_write1(a.out, (t.first + i / OC) * NO + n0 + i % OC, 0.0f, OT);
         return;
     }
     // weight row of row r of the tile (of a wave's rows, the first half are gates and the second up, where GATED)
@@ -55,27 +84,25 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_rows(Fp8GemmLaunch a) {
             return n0 + r;
         }
     };
-    const uint8_t *const w = a.w + (int64_t)t.expert * a.N * a.K;
-    const uint8_t *from[STAGE];
-    uint32_t to[STAGE];
+    const auto source = [&](int m) { return fb_source_row(a, t.first + (m < t.count ? m : t.count - 1)); };
+    // A load takes 8 rows of 128 bytes, 16 bytes a lane.  Weight rows are within 32 bits of the tile's first (K is at most
+    // 2^23), so the address is a scalar and an offset of the lane's; all eight of a load are gates or all are up.
+    const uint8_t *w_base[NW];
+    uint32_t w_at[NW];
 #pragma unroll
-    for (int i = 0; i < STAGE; i++) {
-        const int r = (tid + i * THREADS) >> 3, c = tid & 7;
-        to[i] = lds_at(r, c);
-        if (r < BN) {
-            const int32_t n = weight_row(r);
-            from[i] = w + (int64_t)(n < a.N ? n : a.N - 1) * a.K + 16 * c;
-        } else {
-            const int m = r - BN;
-            from[i] = (const uint8_t *)a.x + fb_source_row(a, t.first + (m < t.count ? m : t.count - 1)) * a.x_stride + 16 * c;
-        }
+    for (int i = 0; i < NW; i++) {
+        const int r0 = 8 * (i * WAVES + wave), r = r0 + (lane >> 3);
+        const int32_t first = weight_row(r0), from = first < a.N ? first : a.N - 1, n = weight_row(r);
+        w_base[i] = a.w + ((int64_t)t.expert * a.N + from) * a.K;
+        w_at[i] = (uint32_t)((n < a.N ? n : a.N - 1) - from) * (uint32_t)a.K + 16 * swizzle(r, lane & 7);
     }
-    const float *xs[TM], *ws[2];
+    AT x_at[NX];
 #pragma unroll
-    for (int i = 0; i < TM; i++) {
-        const int m = 16 * (wm * TM + i) + j;
-        xs[i] = a.x_scales + fb_source_row(a, t.first + (m < t.count ? m : t.count - 1)) * a.x_scale_row;
+    for (int i = 0; i < NX; i++) {
+        const int m = 8 * (i * WAVES + wave) + (lane >> 3);
+        x_at[i] = (AT)(source(m) * a.x_stride + 16 * swizzle(m, lane & 7));
     }
+    const float *ws[2];
 #pragma unroll
     for (int h = 0; h < 2; h++) {
         const int32_t n = weight_row(16 * (wn * TN + h * H));
@@ -88,63 +115,128 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_rows(Fp8GemmLaunch a) {
     for (int i = 0; i < TN; i++)
 #pragma unroll
         for (int k = 0; k < TM; k++) acc[i][k] = kv_f4{0.0f, 0.0f, 0.0f, 0.0f};
-    kv_u4 stage[STAGE];
-    const auto read = [&](int32_t kb) {
-#pragma unroll
-        for (int i = 0; i < STAGE; i++) stage[i] = *(const kv_u4 *)(from[i] + (int64_t)kb * FB);
+    struct {
+        float v[2];
+    } w0, w1;
+    // Load i of a block's, and the two scales of the weight.
+    const auto load = [&](uint8_t *b, int32_t kb, int i) {
+        if (i < NX) {
+            const uint8_t *x = (const uint8_t *)a.x + (int64_t)kb * FB;
+            asm("" : "+s"(x));  // a scalar and an offset, not a sum of 64 bits for each load that is kept in registers
+            __builtin_amdgcn_global_load_lds((fb_global)(x + x_at[i]), (fb_lds)(b + BN * FB + (i * WAVES + wave) * 1024), 16, 0, 0);
+        } else {
+            i -= NX;
+            const uint8_t *w = w_base[i] + (int64_t)kb * FB;
+            asm("" : "+s"(w));
+            __builtin_amdgcn_global_load_lds((fb_global)(w + w_at[i]), (fb_lds)(b + (i * WAVES + wave) * 1024), 16, 0, 0);
+        }
     };
-    const auto put = [&](uint8_t *b) {
+    const auto load_weight_scales = [&](auto &sw, int32_t kb) { sw.v[0] = ws[0][kb], sw.v[1] = ws[1][kb]; };
+    // Scales of SB blocks from `kb` on, one of two places in turn: [row][block], a row's blocks exchanged by its number so
+    // that sixteen rows' scales of a block lie in sixteen banks.
+    const auto load_scales = [&](int32_t kb) {
+        uint8_t *const to = scales + ((kb - kb0) / SB & 1) * BM * SB * 4;
+        int l = lane;
+        asm("" : "+v"(l));  // the addresses are made here each time: kept, they would take 2 * NS registers
 #pragma unroll
-        for (int i = 0; i < STAGE; i++) *(kv_u4 *)(b + to[i]) = stage[i];
+        for (int i = 0; i < NS; i++) {
+            const int m = 4 * (i * WAVES + wave) + (l >> 4);
+            const int32_t b = kb + ((l & 15) ^ (m >> 2 & 3));
+            const float *const from = a.x_scales + source(m) * KB + (b < KB ? b : KB - 1);
+            __builtin_amdgcn_global_load_lds((fb_global)from, (fb_lds)(to + (i * WAVES + wave) * 256), 4, 0, 0);
+        }
     };
-    const auto fetch = [&](const uint8_t *b, int row, fb_i8 *v) {
-        const kv_u4 lo = *(const kv_u4 *)(b + lds_at(row + j, g)), hi = *(const kv_u4 *)(b + lds_at(row + j, g + 4));
+    const int p0 = swizzle(j, g) << 4, p1 = swizzle(j, g + 4) << 4;  // (16 rows further the swizzle is the same)
+    const auto fetch = [&](const uint8_t *b, int row) {
+        const uint8_t *const at = b + (row + j) * FB;
+        const kv_u4 lo = *(const kv_u4 *)(at + p0), hi = *(const kv_u4 *)(at + p1);
+        fb_i8 v;
 #pragma unroll
-        for (int i = 0; i < 4; i++) (*v)[i] = (int)lo[i], (*v)[4 + i] = (int)hi[i];
+        for (int i = 0; i < 4; i++) v[i] = (int)lo[i], v[4 + i] = (int)hi[i];
+        return v;
     };
-    read(kb0);
-    put(lds);
-    __syncthreads();
-    for (int32_t kb = kb0; kb < kb1; kb++) {
-        const uint8_t *const b = lds + ((kb - kb0) & 1) * (BN + BM) * FB;
-        if (kb + 1 < kb1) read(kb + 1);
-        float sx[TM], sw[2];
-#pragma unroll
-        for (int i = 0; i < TM; i++) sx[i] = xs[i][(int64_t)kb * a.x_scale_col];
-        sw[0] = ws[0][kb], sw[1] = ws[1][kb];
+    constexpr int SPREAD = TN > 8 ? TN / 8 : 1, PER = (NW + NX + SPREAD - 1) / SPREAD;
+    const auto multiply = [&](auto more, const uint8_t *b, const auto &sw, int32_t kb, uint8_t *b_next, auto &sw_next, int32_t kb_next) {
         fb_i8 xf[TM];
+        float sx[TM];
+        const int at = (kb - kb0) & (SB - 1);
+        const uint8_t *const s = scales + ((kb - kb0) / SB & 1) * BM * SB * 4 + (16 * wm * TM + j) * SB * 4 + ((at ^ (j >> 2 & 3)) << 2);
 #pragma unroll
-        for (int i = 0; i < TM; i++) fetch(b, BN + 16 * (wm * TM + i), &xf[i]);
+        for (int k = 0; k < TM; k++) sx[k] = *(const float *)(s + k * 16 * SB * 4);
 #pragma unroll
-        for (int i = 0; i < TN; i++) {
-            fb_i8 wf;
-            fetch(b, 16 * (wn * TN + i), &wf);
+        for (int k = 0; k < TM; k++) xf[k] = fetch(b, BN + 16 * (wm * TM + k));
+        // products of tile i, and beside them the scaling of tile i - 1's
+        fb_i8 wf = fetch(b, 16 * wn * TN);
+        kv_f4 d[2][TM];
+        float f[TM];
 #pragma unroll
-            for (int k = 0; k < TM; k++) {
-                kv_f4 d = {0.0f, 0.0f, 0.0f, 0.0f};
-                if constexpr (WIDE) {
+        for (int i = 0; i <= TN; i++) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (i < TN) {
+                if constexpr (more()) {
+                    if (i == 0) load_weight_scales(sw_next, kb_next);
 #pragma unroll
-                    for (int q = 0; q < 4; q++)
-                        d = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb_half8((uint32_t)wf[2 * q], (uint32_t)wf[2 * q + 1]),
-                                                                   fb_half8((uint32_t)xf[k][2 * q], (uint32_t)xf[k][2 * q + 1]), d, 0, 0, 0);
-                } else {
-                    d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf[k], d, 0, 0, 0, 0, 0, 0);
+                    for (int l = PER * i; l < PER * (i + 1) && l < NW + NX; l++) load(b_next, kb_next, l);
                 }
-                const float s = sx[k] * sw[i >= H];
+                const fb_i8 now = wf;
+                if (i + 1 < TN) wf = fetch(b, 16 * (wn * TN + i + 1));
 #pragma unroll
-                for (int q = 0; q < 4; q++) acc[i][k][q] = __builtin_fmaf(d[q], s, acc[i][k][q]);
+                for (int k = 0; k < TM; k++) {
+                    kv_f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+                    if constexpr (WIDE) {
+#pragma unroll
+                        for (int q = 0; q < 4; q++)
+                            v = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb_half8((uint32_t)now[2 * q], (uint32_t)now[2 * q + 1]),
+                                                                       fb_half8((uint32_t)xf[k][2 * q], (uint32_t)xf[k][2 * q + 1]), v, 0, 0, 0);
+                    } else {
+                        v = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(now, xf[k], v, 0, 0, 0, 0, 0, 0);
+                    }
+                    d[i & 1][k] = v;
+                }
+            }
+            if (i > 0) {
+                if ((i - 1) % H == 0) {
+#pragma unroll
+                    for (int k = 0; k < TM; k++) f[k] = sx[k] * sw.v[(i - 1) / H];
+                }
+#pragma unroll
+                for (int k = 0; k < TM; k++)
+#pragma unroll
+                    for (int q = 0; q < 4; q++) acc[i - 1][k][q] = __builtin_fmaf(d[~i & 1][k][q], f[k], acc[i - 1][k][q]);
+            }
+            if constexpr (!WIDE) {
+                if (i < TN) {
+#pragma unroll
+                    for (int k = 0; k < TM; k++) {
+                        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // matrix
+                        if (k == 0) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS reads
+                        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);  // vector
+                    }
+                }
             }
         }
-        if (kb + 1 < kb1) put(lds + ((kb + 1 - kb0) & 1) * (BN + BM) * FB);
-        __syncthreads();
-    }
-    // lane (j, g): outputs 4 g .. 4 g + 3 of each tile of weight rows, of row j
-    const bool whole = a.splits > 1;
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    load_scales(kb0);
+    load_weight_scales(w0, kb0);
 #pragma unroll
-    for (int k = 0; k < TM; k++) {
-        const int m = 16 * (wm * TM + k) + j;
-        if (m >= t.count) continue;
-        if (whole) {
+    for (int l = 0; l < NW + NX; l++) load(even, kb0, l);
+    fb_meet();
+    int32_t kb = kb0;
+    for (; kb + 1 < kb1; kb += 2) {
+        if (((kb - kb0) & (SB - 1)) == 0 && kb + SB < kb1) load_scales(kb + SB);
+        multiply(std::true_type(), even, w0, kb, odd, w1, kb + 1);
+        fb_meet();
+        multiply(std::true_type(), odd, w1, kb + 1, even, w0, kb + 2 < kb1 ? kb + 2 : kb + 1);  // (the last loads are not used)
+        fb_meet();
+    }
+    if (kb < kb1) multiply(std::false_type(), even, w0, kb, odd, w1, kb);
+    // lane (j, g): outputs 4 g .. 4 g + 3 of each tile of weight rows, of row j
+    if (a.splits > 1) {
+#pragma unroll
+        for (int k = 0; k < TM; k++) {
+            const int m = 16 * (wm * TM + k) + j;
+            if (m >= t.count) continue;
             float *const part = a.part + ((int64_t)blockIdx.y * a.out_rows + t.first + m) * a.N;
 #pragma unroll
             for (int i = 0; i < TN; i++) {
@@ -156,21 +248,51 @@ __global__ __launch_bounds__(64 * WN * WM) void k_fp8_rows(Fp8GemmLaunch a) {
                     for (int q = 0; q < 4; q++)
                         if (n + q < a.N) part[n + q] = acc[i][k][q];
             }
-            continue;
         }
+        return;
+    }
+    if (OT != 0 && NO % 8 == 0 && n0 + OC <= NO) {
+        // Rows of V times 16 bytes through LDS, so that a store writes whole rows of the wave's tile (32 bytes of sixteen
+        // rows each otherwise); a row's pieces are exchanged by its number.
+        constexpr int TILES = GATED ? H : TN, V = 2 * TILES, ROW = 16 * V;
+        fb_meet();
+        uint8_t *const own = (wave < WAVES / 2 ? even : odd) + wave % (WAVES / 2) * 16 * TM * ROW;
+#pragma unroll
+        for (int k = 0; k < TM; k++)
+#pragma unroll
+            for (int i = 0; i < TILES; i++) {
+                float f[4];
+#pragma unroll
+                for (int q = 0; q < 4; q++) f[q] = GATED ? fb_silu<OT>(acc[i][k][q]) * acc[GATED ? i + H : i][k][q] : acc[i][k][q];
+                kv_write4<OT>(own + (16 * k + j) * ROW + (((2 * i + (g >> 1)) ^ (j & (V - 1))) << 4), 4 * (g & 1), f);
+            }
+        constexpr int RT = 64 / V;  // rows of a store
+        const int n = weight_row(16 * wn * TN) + 8 * (lane % V);
+#pragma unroll
+        for (int r0 = 0; r0 < 16 * TM; r0 += RT) {
+            const int r = r0 + lane / V, m = 16 * wm * TM + r;
+            const kv_u4 v = *(const kv_u4 *)(own + r * ROW + (((lane % V) ^ (r & (V - 1))) << 4));
+            if (m < t.count) *(kv_u4 *)((uint16_t *)a.out + (t.first + m) * NO + n) = v;
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < TM; k++) {
+        const int m = 16 * (wm * TM + k) + j;
+        if (m >= t.count) continue;
 #pragma unroll
         for (int i = 0; i < (GATED ? H : TN); i++) {
             const int32_t n = weight_row(16 * (wn * TN + i)) + 4 * g;
             float f[4];
 #pragma unroll
-            for (int q = 0; q < 4; q++) f[q] = GATED ? fb_silu(acc[i][k][q]) * acc[GATED ? i + H : i][k][q] : acc[i][k][q];
+            for (int q = 0; q < 4; q++) f[q] = GATED ? fb_silu<OT>(acc[i][k][q]) * acc[GATED ? i + H : i][k][q] : acc[i][k][q];
             const int64_t o = (t.first + m) * NO + n;
             if (NO % 4 == 0 && n + 3 < NO) {
-                fb_write4(a.out, o, f, a.out_dtype);
+                kv_write4<OT>(a.out, o, f);
             } else {
 #pragma unroll
                 for (int q = 0; q < 4; q++)
-                    if (n + q < NO) fb_write1(a.out, o + q, f[q], a.out_dtype);
+                    if (n + q < NO) fb_write1(a.out, o + q, f[q], OT);
             }
         }
     }
@@ -188,15 +310,18 @@ __global__ __launch_bounds__(256) void k_fp8_join(Fp8GemmLaunch a) {
             y += p[s * piece];
             if (a.gated) up += p[s * piece + NO];
         }
-        fb_write1(a.out, i, a.gated ? fb_silu(y) * up : y, a.out_dtype);
+        fb_write1(a.out, i, a.gated ? fb_silu<0>(y) * up : y, a.out_dtype);
     }
 }
 
-template <int WN, int WM, int TN, int TM, bool WIDE, bool GATED>
-static int rows(const Fp8GemmLaunch &L, hipStream_t s) {
-    constexpr int BN = 16 * WN * TN, BM = 16 * WM * TM;
-    const dim3 grid((uint32_t)(fb_ceil(L.N, BN) * L.tiles_m), (uint32_t)L.splits);
-    hipLaunchKernelGGL((k_fp8_rows<WN, WM, TN, TM, WIDE, GATED>), grid, dim3(64 * WN * WM), 0, s, L);
+template <int WN, int WM, int TN, int TM, int OT, bool GATED, typename AT = uint32_t>
+static int rows(Fp8GemmLaunch L, hipStream_t s) {
+    constexpr int BN = 16 * WN * TN;
+    const int64_t tiles = fb_ceil(L.N, BN) * L.tiles_m, part = tiles / (4 * XCDS);
+    L.span = part < 1 ? 1 : part > MOST_SPAN ? MOST_SPAN : (int32_t)part;
+    const int64_t round = XCDS * L.span;  // whole turns of the XCDs: place_tile's tiles are all there
+    const dim3 grid((uint32_t)(fb_ceil(tiles, round) * round), (uint32_t)L.splits);
+    hipLaunchKernelGGL((k_fp8_rows<WN, WM, TN, TM, OT, GATED, AT>), grid, dim3(64 * WN * WM), 0, s, L);
     if (hipGetLastError() != hipSuccess) return 9;  // NQ_ERR_HIP
     if (L.splits > 1) {
         const int64_t units = fb_ceil(L.out_rows * (GATED ? L.N / 2 : L.N), 256), most = (int64_t)device_compute_units() * 16;
@@ -206,20 +331,30 @@ static int rows(const Fp8GemmLaunch &L, hipStream_t s) {
     return 0;
 }
 
-template <bool WIDE, bool GATED>
+template <int OT, bool GATED>
 static int rows_of(const Fp8GemmLaunch &L, int config, hipStream_t s) {
     switch (config) {
-    case 0: return rows<4, 1, 2, 4, WIDE, GATED>(L, s);
-    case 1: return rows<2, 2, 4, 4, WIDE, GATED>(L, s);
-    default: return rows<2, 4, 8, 4, WIDE, GATED>(L, s);
+    case 0: return rows<4, 1, 2, 4, OT, GATED>(L, s);
+    case 1: return rows<2, 2, 4, 4, OT, GATED>(L, s);
+    case 2:
+        if constexpr (OT != 0) return rows<2, 4, 8, 4, OT, GATED>(L, s);
+        return 7;  // (the plan makes none)
+    default: return rows<2, 2, 4, 4, OT, GATED, uint64_t>(L, s);
+    }
+}
+
+template <bool GATED>
+static int rows_out(const Fp8GemmLaunch &L, int config, hipStream_t s) {
+    switch (L.out_dtype) {
+    case 0: return rows_of<0, GATED>(L, config, s);
+    case 1: return rows_of<1, GATED>(L, config, s);
+    default: return rows_of<2, GATED>(L, config, s);
     }
 }
 
 int launch_fp8_rows(const Fp8GemmLaunch &L, int config, hipStream_t s) {
     if (L.tiles_m == 0 || L.N == 0) return 0;
-    const bool wide = L.out_dtype == 0;
-    if (L.gated) return wide ? rows_of<true, true>(L, config, s) : rows_of<false, true>(L, config, s);
-    return wide ? rows_of<true, false>(L, config, s) : rows_of<false, false>(L, config, s);
+    return L.gated ? rows_out<true>(L, config, s) : rows_out<false>(L, config, s);
 }
 
 }  // namespace nq

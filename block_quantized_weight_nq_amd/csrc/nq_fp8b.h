@@ -17,8 +17,7 @@ struct Fp8QuantLaunch {
     int64_t row_stride;
     int64_t rows, cols, matrices;
     uint8_t *codes;
-    float *scales;      // scale of (i, r / tile, c / 128) at ((i * ceil(rows / tile) + r / tile) * row + c / 128 * col) of its strides
-    int64_t scale_row, scale_col;
+    float *scales;      // [matrices, ceil(rows / tile), cols / 128]
     int32_t in_dtype, tile;
 };
 
@@ -33,8 +32,7 @@ struct Fp8ValuesLaunch {
 struct Fp8GemmLaunch {
     const void *x;
     int64_t x_stride;                // elements
-    const float *x_scales;           // of row r and block b at r * x_scale_row + b * x_scale_col
-    int64_t x_scale_row, x_scale_col;
+    const float *x_scales;           // [x_rows, K / 128]
     const uint8_t *w;                // [experts,] N, K
     const float *w_scales;           // [experts,] ceil(N / 128), K / 128
     void *out;                       // [out_rows, N], gated: [out_rows, N / 2]
@@ -45,21 +43,22 @@ struct Fp8GemmLaunch {
     int32_t N, K, experts, top;      // experts 0: one weight for all rows
     int32_t x_type, out_dtype, gated;
     int32_t waves, splits, per_split;  // few rows: waves of a workgroup; many rows: pieces of K and blocks of each
+    int32_t span;                      // many rows: consecutive tiles of an XCD
 };
 
 // What the host decides from the sizes alone.
 struct Fp8Plan {
     int32_t few;        // 1: the kernel for few rows of a weight, 16 * row_tiles of them a workgroup
     int32_t row_tiles;
-    int32_t config;     // many rows: 0 is 64, 1 is 128, 2 is 256 rows a workgroup
+    int32_t config;     // many rows: 0 is 64, 1 is 128, 2 is 256 rows a workgroup; 3 is 128, and x takes more than 32 bits
     int32_t waves, splits, per_split;
     int32_t quantize;   // 1: a launch of its own makes codes of the rows first
     int64_t tiles_m;
     uint64_t codes_bytes, scales_bytes, part_bytes;  // of the workspace, in this order, each a multiple of 256
 };
 
-constexpr int fb_config_rows[3] = {64, 128, 256};     // rows (tokens) of a workgroup's tile
-constexpr int fb_config_cols[3] = {128, 128, 256};    // weight rows of it
+constexpr int fb_config_rows[4] = {64, 128, 256, 128};     // rows (tokens) of a workgroup's tile
+constexpr int fb_config_cols[4] = {128, 128, 256, 128};    // weight rows of it
 
 __host__ __device__ inline int64_t fb_ceil(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -98,9 +97,10 @@ inline Fp8Tile fb_find_tile_host(At at, int32_t experts, int64_t rows, int32_t b
 constexpr int64_t FB_FEW_ROWS = 64;  // most rows of a tile of the few-rows kernel
 
 // The launch of a product.  `rows`: output rows; `raw`: the rows of x are values that the few-rows kernel can read 16
-// bytes at a time.
+// bytes at a time; `wide`: binary32 outputs; `far`: codes that are given
+// lie further than 32 bits from the first.
 inline Fp8Plan fb_plan(int64_t x_rows, int64_t rows, int64_t experts, int64_t N, int64_t K, bool gated, bool codes, bool raw,
-                       int64_t cus) {
+                       bool wide, bool far, int64_t cus) {
     Fp8Plan p = {};
     const int64_t KB = K / FB;
     const int64_t each = experts > 0 ? fb_ceil(rows, experts) : rows;  // rows of a weight, if all have the same
@@ -116,7 +116,8 @@ inline Fp8Plan fb_plan(int64_t x_rows, int64_t rows, int64_t experts, int64_t N,
     } else {
         p.config = each <= 64 ? 0 : each <= 256 ? 1 : 2;
         const int64_t wgs = fb_ceil(N, fb_config_cols[2]) * fb_row_tiles(rows, experts, 256);
-        if (p.config == 2 && wgs < cus) p.config = 1;
+        if (p.config == 2 && (wide || wgs < cus)) p.config = 1;
+        if (codes ? far : x_rows * K >= 1ll << 32) p.config = 3;
         p.tiles_m = fb_row_tiles(rows, experts, fb_config_rows[p.config]);
         if (experts == 0) {
             const int64_t groups = fb_ceil(N, fb_config_cols[p.config]) * p.tiles_m;

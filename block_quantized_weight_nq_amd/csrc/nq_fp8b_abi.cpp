@@ -7,7 +7,8 @@
 
 namespace {
 
-constexpr int64_t MOST = 1ll << 30;        // rows, pairs, N and K
+constexpr int64_t MOST = 1ll << 30;        // rows, pairs, N, and scales of rows
+constexpr int64_t MOST_K = 1ll << 23;
 constexpr int64_t MOST_EXPERTS = 1024;
 constexpr int64_t THREADS = (1ll << 32) - 1;  // of a grid along an axis
 
@@ -49,7 +50,7 @@ int check_gemm(const nq_fp8_block_args *x, const nq_moe_plan *plan, nq::Fp8Plan 
     if (x->rows < 0 || x->N < 1 || x->K < 1 || (x->gated != 0 && x->gated != 1) || (x->sorted != 0 && x->sorted != 1))
         return NQ_ERR_BAD_DIM;
     if (x->K % nq::FB != 0 || (x->gated && x->N % (2 * nq::FB) != 0)) return NQ_ERR_NOT_BLOCK_ALIGNED;
-    if (x->rows > MOST || x->N > MOST || x->K > MOST) return NQ_ERR_OVERFLOW;
+    if (x->rows > MOST || x->N > MOST || x->K > MOST_K || x->rows > MOST / (x->K / nq::FB)) return NQ_ERR_OVERFLOW;
     int64_t out_rows = x->rows, experts = 0;
     if (plan) {
         const int st = check_plan(plan);
@@ -66,7 +67,8 @@ int check_gemm(const nq_fp8_block_args *x, const nq_moe_plan *plan, nq::Fp8Plan 
     const int64_t esz = codes ? 1 : element_size(x->x_dtype);
     if (codes && x->x_row_stride % 16 != 0) return NQ_ERR_MISALIGNED;
     const bool raw = (uintptr_t)x->x % 16 == 0 && x->x_row_stride * esz % 16 == 0;
-    *p = nq::fb_plan(x->rows, out_rows, experts, x->N, x->K, x->gated != 0, codes, raw, nq::device_compute_units());
+    *p = nq::fb_plan(x->rows, out_rows, experts, x->N, x->K, x->gated != 0, codes, raw, x->out_dtype == NQ_F32,
+                     x->rows > 0 && (x->rows - 1) * x->x_row_stride + x->K > 1ll << 32, nq::device_compute_units());
     const int64_t groups = p->few ? nq::fb_ceil(x->gated ? x->N / 2 : x->N, x->gated ? 16 : 32) * p->waves * 64
                                   : nq::fb_ceil(x->N, nq::fb_config_cols[p->config]) * 512;
     if (p->few ? groups > THREADS || p->tiles_m > 65535 : p->tiles_m > 0 && groups > THREADS / p->tiles_m) return NQ_ERR_OVERFLOW;
@@ -105,7 +107,6 @@ NQ_API int nq_quantize_fp8_block(const void *x, int32_t in_dtype, int64_t matric
     L.rows = rows, L.cols = cols, L.matrices = matrices;
     L.codes = (uint8_t *)codes;
     L.scales = scales;
-    L.scale_row = cols / nq::FB, L.scale_col = 1;
     L.in_dtype = in_dtype, L.tile = tile;
     return nq::launch_fp8_quantize(L, stream);
 }
@@ -155,7 +156,6 @@ NQ_API int nq_gemm_fp8_block(const nq_fp8_block_args *args, const nq_moe_plan *p
     L.x = x.x;
     L.x_stride = x.x_row_stride;
     L.x_scales = x.x_scales;
-    L.x_scale_row = x.K / nq::FB, L.x_scale_col = 1;
     L.x_type = codes ? nq::FB_CODES : x.x_dtype;
     L.w = (const uint8_t *)x.weight;
     L.w_scales = x.weight_scales;
@@ -178,12 +178,11 @@ NQ_API int nq_gemm_fp8_block(const nq_fp8_block_args *args, const nq_moe_plan *p
         q.rows = x.rows, q.cols = x.K, q.matrices = 1;
         q.codes = (uint8_t *)workspace;
         q.scales = (float *)((uint8_t *)workspace + p.codes_bytes);
-        q.scale_row = 1, q.scale_col = x.rows;  // a block's scales of all rows side by side: the kernels read a tile's rows
         q.in_dtype = x.x_dtype, q.tile = 1;
         const int qs = nq::launch_fp8_quantize(q, stream);
         if (qs != NQ_OK) return qs;
         L.x = q.codes, L.x_stride = x.K, L.x_type = nq::FB_CODES;
-        L.x_scales = q.scales, L.x_scale_row = 1, L.x_scale_col = x.rows;
+        L.x_scales = q.scales;
     }
     return p.few ? nq::launch_fp8_few(L, p.row_tiles, stream) : nq::launch_fp8_rows(L, p.config, stream);
 }

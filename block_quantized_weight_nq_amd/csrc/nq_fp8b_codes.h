@@ -126,7 +126,15 @@ __device__ __forceinline__ int64_t fb_source_row(const Fp8GemmLaunch &a, int64_t
     return r < a.x_rows ? r : a.x_rows - 1;
 }
 
-__device__ __forceinline__ float fb_silu(float g) { return g / (1.0f + expf(-g)); }
+// g / (1 + e^-g).  For 16-bit outputs the hardware's exponential and reciprocal, each within 1 ulp of binary32; the
+// argument's rounding makes the exponential off by |g| * 2^-24 of itself at most, 2^-17 at the ends of binary32.
+template <int OT>
+__device__ __forceinline__ float fb_silu(float g) {
+    if constexpr (OT == 0)
+        return g / (1.0f + expf(-g));
+    else
+        return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f));
+}
 
 // One value of type ot.
 __device__ __forceinline__ void fb_write1(void *y, int64_t i, float f, int32_t ot) {

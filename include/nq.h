@@ -487,7 +487,8 @@ int nq_kv_attention(const nq_kv_cache *cache, const nq_kv_attention_args *args, 
  * (a weight for each expert) follow each other, codes and scales alike.
  *
  * Data types are NQ_F32, NQ_F16 and NQ_BF16 (NQ_ERR_BAD_DTYPE).  Rows, cols,
- * N, K and pairs are at most 2^30 (NQ_ERR_OVERFLOW).  Strides are in elements
+ * N and pairs are at most 2^30, a product's K 2^23 and its rows * K / 128 2^30
+ * (NQ_ERR_OVERFLOW).  Strides are in elements
  * unless named otherwise, not negative (NQ_ERR_BAD_DIM), and rows that are
  * only read may overlap.  Codes are 16-byte aligned, scales 4-byte, other
  * tensors to their element unless named (NQ_ERR_MISALIGNED).  Empty inputs
