@@ -1058,7 +1058,7 @@ def gemm_fp8_block(weight, x, x_scales=None, gated=False, out_dtype=None, stream
     the call; or codes float8_e4m3fn with x_scales float32 [rows, K / 128], as quantize_fp8_block returns them.
     gated: the weight's first N / 2 rows are gates, the others up (N a multiple of 256); returns silu(gate) * up,
     [rows, N / 2].  out_dtype: default x's type (float32 for codes).  Sums are binary32; binary32 outputs and calls of up
-    to 64 rows multiply exactly, others on the 8-bit matrix instructions (include/nq.h states the difference).
+    to 16 rows multiply exactly, others on the 8-bit matrix instructions (include/nq.h states the difference).
     """
     if weight.experts:
         raise ValueError("an [experts, N, K] weight takes moe_gemm_fp8_block")

@@ -13,8 +13,9 @@
 // are binary32's, whereas the 8-bit one drops what lies 2^-13 below the largest of eight products.  The conversion (16
 // instructions for 2 KB of weight) hides behind memory.
 //
-// Rows that are not codes yet are rounded here, each wave the blocks that it multiplies (k_fp8b_quant.hip's rule):
-// the four lanes of a row hold its block, so the scale takes 32 values a lane and two exchanges.
+// Rows that are not codes yet are rounded here (k_fp8b_quant.hip's rule), by the whole workgroup into LDS, as many blocks
+// at a time as have room; the first weight codes are on their way meanwhile.  (Each wave for itself, in the registers
+// that multiply: 150 vector instructions a block of 128, which bound it at 3.5 TB/s.)
 #include "nq_fp8b_codes.h"
 
 namespace nq {
@@ -23,81 +24,34 @@ namespace {
 
 constexpr int MAX_WAVES = 8;
 
-// What a lane reads of one block of 128 columns of a row of x.
-template <int XT>
-struct XPart {
-    kv_u4 v[XT == 0 ? 8 : XT == FB_CODES ? 2 : 4];
-    float scale;
-};
-
-template <int XT>
-__device__ __forceinline__ void read_x(const uint8_t *row, const float *scale, int32_t kb, int g, XPart<XT> &p) {
-    constexpr int ESZ = XT == 0 ? 4 : XT == FB_CODES ? 1 : 2, N = 16 * ESZ / 16;
-    const uint8_t *at = row + ((int64_t)kb * FB + 16 * g) * ESZ;
-#pragma unroll
-    for (int h = 0; h < 2; h++)
-#pragma unroll
-        for (int i = 0; i < N; i++) p.v[h * N + i] = ((const kv_u4 *)(at + h * 64 * ESZ))[i];
-    if constexpr (XT == FB_CODES) p.scale = scale[kb];
+// Blocks of a wave on their way.
+template <int NT>
+constexpr int few_depth() {
+    return NT > 2 ? 2 : 3;
 }
 
-// The row's scale of the block, and the lane's 32 codes of it as binary16.
-template <int XT>
-__device__ __forceinline__ float x_codes(const XPart<XT> &p, kv_h8 (&c)[4]) {
-    if constexpr (XT == FB_CODES) {
-#pragma unroll
-        for (int i = 0; i < 4; i++) c[i] = fb_half8(p.v[i >> 1][2 * (i & 1)], p.v[i >> 1][2 * (i & 1) + 1]);
-        return p.scale;
-    } else {
-        float f[32];
-        if constexpr (XT == 0) {
-#pragma unroll
-            for (int i = 0; i < 32; i++) f[i] = __builtin_bit_cast(float, (uint32_t)p.v[i >> 2][i & 3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; i++) {
-                const uint32_t w = p.v[i >> 3][(i >> 1) & 3], h = i & 1 ? w >> 16 : w & 0xFFFFu;
-                f[i] = XT == 1 ? f16(h) : i & 1 ? bits_f32(w & 0xFFFF0000u) : bits_f32(w << 16);
-            }
-        }
-        const auto row_max = [](uint32_t m) {
-            uint32_t o = __shfl_xor(m, 16, 64);
-            m = o > m ? o : m;
-            o = __shfl_xor(m, 32, 64);
-            return o > m ? o : m;
-        };
-        uint32_t top = row_max(fb_amax<32>(f, 0));
-        if (__any(top >= 0x7F800000u)) {
-            top = row_max(fb_amax_finite<32>(f, 0));
-            fb_mark_not_finite<32>(f);
-        }
-        const float scale = fmaxf(__builtin_bit_cast(float, top) / 448.0f, FB_TINY), inv = 1.0f / scale;
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const float(&q)[32] = f;
-            const uint32_t lo = fb_codes4(q[8 * i] * inv, q[8 * i + 1] * inv, q[8 * i + 2] * inv, q[8 * i + 3] * inv);
-            const uint32_t hi = fb_codes4(q[8 * i + 4] * inv, q[8 * i + 5] * inv, q[8 * i + 6] * inv, q[8 * i + 7] * inv);
-            c[i] = fb_half8(lo, hi);
-        }
-        return scale;
-    }
+// Where 16 bytes of a block of row r lie in LDS: blocks of `rows` rows of 128 bytes, whose pieces are exchanged by the
+// row's number, so that sixteen rows' pieces spread over all banks.
+__device__ __forceinline__ int x_place(int block, int rows, int r, int piece) {
+    return (block * rows + r) * FB + ((piece ^ (r >> 1 & 7)) << 4);
 }
 
 }  // namespace
 
-// RT tiles of 16 rows of x, NT of 16 weight rows (GATED: half of them gate, half up).
-template <int XT, int RT, int NT, bool GATED>
+// 16 rows of x, NT tiles of 16 weight rows (GATED: half of them gate, half up).
+template <int XT, int NT, bool GATED>
 __global__ __launch_bounds__(64 * MAX_WAVES) void k_fp8_few(Fp8GemmLaunch a) {
-    extern __shared__ kv_f4 red[];  // [wave][RT][NT][lane]
+    // codes of x, a block's rows together, and their scales; in the end the waves' sums, [wave][NT][lane]
+    extern __shared__ __align__(16) uint8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63, j = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = a.waves;
     Fp8Tile t;
     if (a.experts > 0) {
-        t = fb_find_tile(a.offsets, a.experts, a.out_rows, 16 * RT, blockIdx.y);
+        t = fb_find_tile(a.offsets, a.experts, a.out_rows, 16, blockIdx.y);
     } else {
         t.expert = 0;
-        t.first = (int64_t)blockIdx.y * 16 * RT;
-        t.count = (int32_t)(a.out_rows - t.first < 16 * RT ? a.out_rows - t.first : 16 * RT);
+        t.first = (int64_t)blockIdx.y * 16;
+        t.count = (int32_t)(a.out_rows - t.first < 16 ? a.out_rows - t.first : 16);
     }
     if (t.count == 0) return;
     constexpr int OC = GATED ? 8 * NT : 16 * NT;  // output columns of the workgroup
@@ -120,26 +74,24 @@ __global__ __launch_bounds__(64 * MAX_WAVES) void k_fp8_few(Fp8GemmLaunch a) {
             ws[i] = a.w_scales + (e * nb + (base < a.N ? base : a.N - 1) / FB) * KB;
         }
     }
-    const uint8_t *x[RT];
-    const float *xs[RT];
-#pragma unroll
-    for (int i = 0; i < RT; i++) {
-        const int m = 16 * i + j;
-        const int64_t r = fb_source_row(a, t.first + (m < t.count ? m : t.count - 1));
-        x[i] = (const uint8_t *)a.x + r * a.x_stride * (XT == 0 ? 4 : XT == FB_CODES ? 1 : 2);
-        xs[i] = XT == FB_CODES ? a.x_scales + r * (a.K / FB) : nullptr;
+    constexpr bool RAW = XT != FB_CODES;
+    const int row = j < t.count ? j : t.count - 1;
+    const uint8_t *x = nullptr;
+    const float *xs = nullptr;
+    if constexpr (!RAW) {
+        const int64_t r = fb_source_row(a, t.first + row);
+        x = (const uint8_t *)a.x + r * a.x_stride + 16 * g;
+        xs = a.x_scales + r * KB;
     }
-    kv_f4 acc[RT][NT];
+    constexpr int DEPTH = few_depth<NT>();
+    kv_f4 acc[NT];
 #pragma unroll
-    for (int r = 0; r < RT; r++)
-#pragma unroll
-        for (int i = 0; i < NT; i++) acc[r][i] = kv_f4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < NT; i++) acc[i] = kv_f4{0.0f, 0.0f, 0.0f, 0.0f};
 
     struct Part {
-        kv_u4 w[NT][2];
-        float ws[NT];
-        XPart<XT> x[RT];
-    } part[2];
+        kv_u4 w[NT][2], x[2];
+        float ws[NT], xs;
+    } part[DEPTH];
     const auto read = [&](Part &p, int32_t kb) {
 #pragma unroll
         for (int i = 0; i < NT; i++) {
@@ -147,57 +99,98 @@ __global__ __launch_bounds__(64 * MAX_WAVES) void k_fp8_few(Fp8GemmLaunch a) {
             p.w[i][1] = *(const kv_u4 *)(w[i] + (int64_t)kb * FB + 64);
             p.ws[i] = ws[i][kb];
         }
-#pragma unroll
-        for (int r = 0; r < RT; r++) read_x<XT>(x[r], xs[r], kb, g, p.x[r]);
+        if constexpr (!RAW) {
+            p.x[0] = *(const kv_u4 *)(x + (int64_t)kb * FB);
+            p.x[1] = *(const kv_u4 *)(x + (int64_t)kb * FB + 64);
+            p.xs = xs[kb];
+        }
     };
-    const auto multiply = [&](const Part &p) {
-        kv_h8 xc[RT][4];
-        float sx[RT];
+    // codes of blocks from c0 on, as many as a.chunk, into LDS: four lanes take a row's block, 32 values each
+    float *const scales = (float *)(lds + (int64_t)a.chunk * t.count * FB);
+    const auto refill = [&](int32_t c0) {
+        const int pairs = t.count * (KB - c0 < a.chunk ? KB - c0 : a.chunk), l = tid & 3;
+        __syncthreads();
+        for (int q = tid >> 2; q < pairs; q += 16 * waves) {
+            const int b = q / t.count, m = q - b * t.count;
+            const int64_t at = fb_source_row(a, t.first + m) * a.x_stride + (int64_t)(c0 + b) * FB + 32 * l;
+            float f[4][8];
 #pragma unroll
-        for (int r = 0; r < RT; r++) sx[r] = x_codes<XT>(p.x[r], xc[r]);
+            for (int u = 0; u < 4; u++) fb_read8<RAW ? XT : 0, true>(a.x, at + 8 * u, f[u]);
+            uint32_t top = 0;
+#pragma unroll
+            for (int u = 0; u < 4; u++) top = fb_amax8(f[u], top);
+            top = fb_max4(top);
+            if (top >= 0x7F800000u) {
+                top = 0;
+#pragma unroll
+                for (int u = 0; u < 4; u++) top = fb_amax8_finite(f[u], top);
+                top = fb_max4(top);
+#pragma unroll
+                for (int u = 0; u < 4; u++) fb_mark_not_finite(f[u]);
+            }
+            const float scale = fmaxf(__builtin_bit_cast(float, top) / 448.0f, FB_TINY), inv = 1.0f / scale;
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const kv_u2 lo = fb_codes8(f[2 * h], inv), hi = fb_codes8(f[2 * h + 1], inv);
+                *(kv_u4 *)(lds + x_place(b, t.count, m, 2 * l + h)) = kv_u4{lo[0], lo[1], hi[0], hi[1]};
+            }
+            if (l == 0) scales[q] = scale;
+        }
+        __syncthreads();
+    };
+    const auto multiply = [&](const Part &p, int32_t block) {
+        kv_u4 v[2];
+        float sx;
+        if constexpr (RAW) {
+            v[0] = *(const kv_u4 *)(lds + x_place(block, t.count, row, g));
+            v[1] = *(const kv_u4 *)(lds + x_place(block, t.count, row, g + 4));
+            sx = scales[block * t.count + row];
+        } else {
+            v[0] = p.x[0], v[1] = p.x[1];
+            sx = p.xs;
+        }
+        kv_h8 xc[4];
+#pragma unroll
+        for (int q = 0; q < 4; q++) xc[q] = fb_half8(v[q >> 1][2 * (q & 1)], v[q >> 1][2 * (q & 1) + 1]);
 #pragma unroll
         for (int i = 0; i < NT; i++) {
-            kv_h8 wc[4];
+            kv_f4 d = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int q = 0; q < 4; q++) wc[q] = fb_half8(p.w[i][q >> 1][2 * (q & 1)], p.w[i][q >> 1][2 * (q & 1) + 1]);
+            for (int q = 0; q < 4; q++)
+                d = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb_half8(p.w[i][q >> 1][2 * (q & 1)], p.w[i][q >> 1][2 * (q & 1) + 1]), xc[q], d, 0, 0, 0);
+            const float s = sx * p.ws[i];
 #pragma unroll
-            for (int r = 0; r < RT; r++) {
-                kv_f4 d = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int q = 0; q < 4; q++) d = __builtin_amdgcn_mfma_f32_16x16x32_f16(wc[q], xc[r][q], d, 0, 0, 0);
-                const float s = sx[r] * p.ws[i];
-#pragma unroll
-                for (int k = 0; k < 4; k++) acc[r][i][k] = __builtin_fmaf(d[k], s, acc[r][i][k]);
-            }
+            for (int k = 0; k < 4; k++) acc[i][k] = __builtin_fmaf(d[k], s, acc[i][k]);
         }
     };
-    if (wave < KB) {
-        int32_t kb = wave;
-        read(part[0], kb);
-        while (true) {
-            int32_t next = kb + waves;
-            if (next < KB) read(part[1], next);
-            multiply(part[0]);
-            if (next >= KB) break;
-            kb = next, next = kb + waves;
-            if (next < KB) read(part[0], next);
-            multiply(part[1]);
-            if (next >= KB) break;
-            kb = next;
+    // a.chunk is a multiple of DEPTH * waves
+#pragma unroll
+    for (int d = 0; d < DEPTH; d++)
+        if (wave + d * waves < KB) read(part[d], wave + d * waves);
+    for (int32_t c0 = 0; c0 < KB; c0 += a.chunk) {
+        if constexpr (RAW) refill(c0);
+        const int32_t end = KB - c0 < a.chunk ? KB - c0 : a.chunk;
+        for (int32_t b = wave; b < end; b += DEPTH * waves) {
+#pragma unroll
+            for (int d = 0; d < DEPTH; d++) {
+                const int32_t now = b + d * waves, next = c0 + now + DEPTH * waves;
+                if (now < end) multiply(part[d], now);
+                if (next < KB) read(part[d], next);
+            }
         }
     }
+    if constexpr (RAW) __syncthreads();
+    kv_f4 *const red = (kv_f4 *)lds;
 #pragma unroll
-    for (int r = 0; r < RT; r++)
-#pragma unroll
-        for (int i = 0; i < NT; i++) red[((wave * RT + r) * NT + i) * 64 + lane] = acc[r][i];
+    for (int i = 0; i < NT; i++) red[(wave * NT + i) * 64 + lane] = acc[i];
     __syncthreads();
     constexpr int PER = GATED ? NT / 2 : NT;
-    for (int q = tid; q < RT * PER * 64; q += 64 * waves) {
-        const int at = q & 63, i = (q >> 6) % PER, r = (q >> 6) / PER;
+    for (int q = tid; q < PER * 64; q += 64 * waves) {
+        const int at = q & 63, i = q >> 6;
         const auto total = [&](int tile) {
-            kv_f4 y = red[(r * NT + tile) * 64 + at];
+            kv_f4 y = red[tile * 64 + at];
             for (int v = 1; v < waves; v++) {
-                const kv_f4 o = red[((v * RT + r) * NT + tile) * 64 + at];
+                const kv_f4 o = red[(v * NT + tile) * 64 + at];
 #pragma unroll
                 for (int k = 0; k < 4; k++) y[k] += o[k];
             }
@@ -210,7 +203,7 @@ __global__ __launch_bounds__(64 * MAX_WAVES) void k_fp8_few(Fp8GemmLaunch a) {
 #pragma unroll
             for (int k = 0; k < 4; k++) f[k] = fb_silu<0>(f[k]) * up[k];
         }
-        const int m = 16 * r + (at & 15), n = n0 + 16 * i + 4 * (at >> 4);
+        const int m = at & 15, n = n0 + 16 * i + 4 * (at >> 4);
         if (m >= t.count) continue;
         const int64_t o = (t.first + m) * NO + n;
         if (NO % 4 == 0 && n + 3 < NO) {
@@ -223,32 +216,37 @@ __global__ __launch_bounds__(64 * MAX_WAVES) void k_fp8_few(Fp8GemmLaunch a) {
     }
 }
 
-template <int XT, int RT, int NT, bool GATED>
-static int few(const Fp8GemmLaunch &L, hipStream_t s) {
-    const int32_t oc = GATED ? 8 * NT : 16 * NT, no = GATED ? L.N / 2 : L.N;
-    const dim3 grid((uint32_t)fb_ceil(no, oc), (uint32_t)L.tiles_m);
-    hipLaunchKernelGGL((k_fp8_few<XT, RT, NT, GATED>), grid, dim3(64 * L.waves), (uint32_t)L.waves * RT * NT * 1024, s, L);
+template <int XT, int NT, bool GATED>
+static int few(Fp8GemmLaunch L, hipStream_t s) {
+    const int32_t no = GATED ? L.N / 2 : L.N;
+    const dim3 grid((uint32_t)fb_ceil(no, fb_few_cols(NT, GATED)), (uint32_t)L.tiles_m);
+    uint32_t room = 0;
+    L.chunk = L.K / FB;
+    if (XT != FB_CODES) {
+        // blocks of codes at a time: a turn of all waves, and all of them where few rows leave room in 16 KB
+        const int32_t rows = L.out_rows < 16 ? (int32_t)L.out_rows : 16, turn = few_depth<NT>() * L.waves;
+        const int32_t fit = 16384 / FB / rows;
+        L.chunk = fit > turn ? fit / turn * turn : turn;
+        room = (uint32_t)(L.chunk * rows * (FB + 4));
+    }
+    const uint32_t sums = (uint32_t)L.waves * NT * 1024;
+    hipLaunchKernelGGL((k_fp8_few<XT, NT, GATED>), grid, dim3(64 * L.waves), room > sums ? room : sums, s, L);
     return hipGetLastError() == hipSuccess ? 0 : 9;  // NQ_ERR_HIP
 }
 
-template <int XT, int RT>
-static int few_form(const Fp8GemmLaunch &L, hipStream_t s) {
-    return L.gated ? few<XT, RT, 2, true>(L, s) : few<XT, RT, 2, false>(L, s);
+template <int XT>
+static int few_form(const Fp8GemmLaunch &L, int weight_tiles, hipStream_t s) {
+    if (L.gated) return weight_tiles == 4 ? few<XT, 4, true>(L, s) : few<XT, 2, true>(L, s);
+    return weight_tiles == 1 ? few<XT, 1, false>(L, s) : few<XT, 2, false>(L, s);
 }
 
-int launch_fp8_few(const Fp8GemmLaunch &L, int row_tiles, hipStream_t s) {
+int launch_fp8_few(const Fp8GemmLaunch &L, int weight_tiles, hipStream_t s) {
     if (L.tiles_m == 0 || L.N == 0) return 0;
-    if (L.x_type == FB_CODES) {
-        switch (row_tiles) {
-        case 1: return few_form<FB_CODES, 1>(L, s);
-        case 2: return few_form<FB_CODES, 2>(L, s);
-        default: return few_form<FB_CODES, 4>(L, s);
-        }
-    }
     switch (L.x_type) {
-    case 0: return few_form<0, 1>(L, s);
-    case 1: return few_form<1, 1>(L, s);
-    default: return few_form<2, 1>(L, s);
+    case 0: return few_form<0>(L, weight_tiles, s);
+    case 1: return few_form<1>(L, weight_tiles, s);
+    case 2: return few_form<2>(L, weight_tiles, s);
+    default: return few_form<FB_CODES>(L, weight_tiles, s);
     }
 }
 

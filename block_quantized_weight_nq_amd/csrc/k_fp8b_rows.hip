@@ -333,8 +333,8 @@ static int rows(Fp8GemmLaunch L, hipStream_t s) {
 
 template <int OT, bool GATED>
 static int rows_of(const Fp8GemmLaunch &L, int config, hipStream_t s) {
-    switch (config) {
-    case 0: return rows<4, 1, 2, 4, OT, GATED>(L, s);
+    switch (config) {  // (fb_configs)
+    case 0: return rows<2, 2, 2, 2, OT, GATED>(L, s);
     case 1: return rows<2, 2, 4, 4, OT, GATED>(L, s);
     case 2:
         if constexpr (OT != 0) return rows<2, 4, 8, 4, OT, GATED>(L, s);

@@ -44,21 +44,19 @@ struct Fp8GemmLaunch {
     int32_t x_type, out_dtype, gated;
     int32_t waves, splits, per_split;  // few rows: waves of a workgroup; many rows: pieces of K and blocks of each
     int32_t span;                      // many rows: consecutive tiles of an XCD
+    int32_t chunk;                     // few rows: blocks whose codes are in LDS at a time
 };
 
 // What the host decides from the sizes alone.
 struct Fp8Plan {
-    int32_t few;        // 1: the kernel for few rows of a weight, 16 * row_tiles of them a workgroup
-    int32_t row_tiles;
-    int32_t config;     // many rows: 0 is 64, 1 is 128, 2 is 256 rows a workgroup; 3 is 128, and x takes more than 32 bits
+    int32_t few;           // 1: the kernel for few rows of a weight, 16 of them a workgroup
+    int32_t weight_tiles;  // few rows: tiles of 16 weight rows of a workgroup
+    int32_t config;        // many rows: the tile (fb_configs)
     int32_t waves, splits, per_split;
     int32_t quantize;   // 1: a launch of its own makes codes of the rows first
     int64_t tiles_m;
     uint64_t codes_bytes, scales_bytes, part_bytes;  // of the workspace, in this order, each a multiple of 256
 };
-
-constexpr int fb_config_rows[4] = {64, 128, 256, 128};     // rows (tokens) of a workgroup's tile
-constexpr int fb_config_cols[4] = {128, 128, 256, 128};    // weight rows of it
 
 __host__ __device__ inline int64_t fb_ceil(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -94,37 +92,73 @@ inline Fp8Tile fb_find_tile_host(At at, int32_t experts, int64_t rows, int32_t b
     return {-1, 0, 0};
 }
 
-constexpr int64_t FB_FEW_ROWS = 64;  // most rows of a tile of the few-rows kernel
+// The tiles of the many-rows kernel: rows of x and of the weight, workgroups that a compute unit holds, and the time of
+// one block of 128 columns in us, where a compute unit has one workgroup and where it has all (measured at K = 4096,
+// 256 to 28672 weight rows; times 1.6 for binary32 outputs).  The last is the second for x beyond 32 bits.
+struct Fp8Config {
+    int32_t rows, cols, held;
+    float alone, full;
+};
+constexpr Fp8Config fb_configs[4] = {{64, 64, 4, 0.42f, 1.0f}, {128, 128, 2, 0.75f, 1.3f}, {256, 256, 1, 1.84f, 1.84f}, {128, 128, 2, 0.75f, 1.3f}};
+constexpr int FB_FAR = 3;
+
+constexpr int64_t FB_FEW_ROWS = 16;       // most rows of a weight, on average, that the few-rows kernel takes
+constexpr int64_t FB_RAW_VALUES = 16384;  // most values of them that its workgroups make codes of, each for itself
+
+// Output columns of a workgroup of the few-rows kernel.
+inline int64_t fb_few_cols(int32_t weight_tiles, bool gated) { return gated ? 8 * weight_tiles : 16 * weight_tiles; }
 
 // The launch of a product.  `rows`: output rows; `raw`: the rows of x are values that the few-rows kernel can read 16
-// bytes at a time; `wide`: binary32 outputs; `far`: codes that are given
-// lie further than 32 bits from the first.
+// bytes at a time; `wide`: binary32 outputs; `far`: codes that are given lie further than 32 bits from the first.
 inline Fp8Plan fb_plan(int64_t x_rows, int64_t rows, int64_t experts, int64_t N, int64_t K, bool gated, bool codes, bool raw,
                        bool wide, bool far, int64_t cus) {
     Fp8Plan p = {};
     const int64_t KB = K / FB;
-    const int64_t each = experts > 0 ? fb_ceil(rows, experts) : rows;  // rows of a weight, if all have the same
+    const int64_t busy = experts > 0 ? (rows < experts ? rows : experts) : 1;  // weights that have rows, at most
+    const int64_t each = busy > 0 ? fb_ceil(rows, busy) : 0;                   // rows of a weight, if all have the same
     p.splits = 1, p.per_split = (int32_t)KB;
-    if (each <= FB_FEW_ROWS) {
+    if ((experts > 0 ? fb_ceil(rows, experts) : rows) <= FB_FEW_ROWS) {
         p.few = 1;
-        p.row_tiles = each <= 16 ? 1 : each <= 32 ? 2 : 4;
-        p.tiles_m = fb_row_tiles(rows, experts, 16 * p.row_tiles);
-        const int64_t groups = fb_ceil(gated ? N / 2 : N, gated ? 16 : 32) * (experts > 0 ? (rows < experts ? rows : experts) : p.tiles_m);
-        p.waves = 2;
-        while (p.waves < 8 && p.waves < KB && groups * p.waves < cus * 12) p.waves *= 2;
-        p.quantize = !codes && (!raw || p.row_tiles > 1);
+        p.tiles_m = fb_row_tiles(rows, experts, 16);
+        // weight rows of a workgroup: few where more would leave compute units idle ([4096, 14336]: 14.8 us with 16, 18.9
+        // with 32), many where there are enough workgroups (gated [28672, 4096]: 26.0 us with 64, 27.4 with 32)
+        const int64_t cols = gated ? N / 2 : N;
+        p.weight_tiles = 2;
+        if (!gated && fb_ceil(cols, 16) * busy <= cus) p.weight_tiles = 1;
+        if (gated && fb_ceil(cols, 32) * busy >= cus + cus / 2) p.weight_tiles = 4;
+        const int64_t groups = fb_ceil(cols, fb_few_cols(p.weight_tiles, gated)) * busy;
+        p.waves = 4 * groups <= 5 * cus ? 8 : groups <= 3 * cus ? 4 : 2;
+        while (p.waves > 1 && p.waves > KB) p.waves /= 2;
+        // one row of [28672, 4096] 27.1 us with codes made in each workgroup, 28.7 with a launch before; four rows of
+        // [4096, 14336] 20.7 and 17.2
+        p.quantize = !codes && (!raw || each * K > FB_RAW_VALUES);
     } else {
-        p.config = each <= 64 ? 0 : each <= 256 ? 1 : 2;
-        const int64_t wgs = fb_ceil(N, fb_config_cols[2]) * fb_row_tiles(rows, experts, 256);
-        if (p.config == 2 && (wide || wgs < cus)) p.config = 1;
-        if (codes ? far : x_rows * K >= 1ll << 32) p.config = 3;
-        p.tiles_m = fb_row_tiles(rows, experts, fb_config_rows[p.config]);
-        if (experts == 0) {
-            const int64_t groups = fb_ceil(N, fb_config_cols[p.config]) * p.tiles_m;
-            while (groups * p.splits < cus && KB / (2 * p.splits) >= 4 && p.splits < 16) p.splits *= 2;
-            p.per_split = (int32_t)fb_ceil(KB, p.splits);
-            p.splits = (int32_t)fb_ceil(KB, p.per_split);
+        // the least of: rounds of workgroups, with the time of a block between that of a workgroup alone and of a full
+        // compute unit, or the weight's bytes, and where K is split a launch more and each piece's sums written and read
+        float least = 0.0f;
+        const bool beyond = codes ? far : x_rows * K > 1ll << 32;
+        for (int c = 0; c < 4; c++) {
+            if (beyond ? c != FB_FAR : c == FB_FAR || (wide && c == 2)) continue;
+            const Fp8Config &f = fb_configs[c];
+            const int64_t tiles = fb_ceil(N, f.cols) * (experts > 0 ? busy * fb_ceil(2 * each + f.rows, 2 * f.rows) : fb_ceil(rows, f.rows));
+            for (int s = 1; s <= 16; s *= 2) {
+                if (s > 1 && (experts > 0 || KB / s < 4)) break;
+                const int64_t slots = cus * f.held, rounds = fb_ceil(tiles * s, slots);
+                const float load = (float)(tiles * s) / (float)(rounds * slots);
+                float t = (float)(rounds * fb_ceil(KB, s)) * (f.alone + (f.full - f.alone) * load) * (wide ? 1.6f : 1.0f) + 2.0f * (float)rounds;
+                const float bytes = (float)(busy * N) * (float)K / 4.8e6f;
+                if (t < bytes) t = bytes;
+                if (s > 1) t += 3.5f + (float)(s * rows) * (float)N * 8.0f / 5e6f;
+                if (least == 0.0f || t < least) {
+                    least = t;
+                    p.config = c;
+                    p.splits = s;
+                }
+            }
         }
+        p.tiles_m = fb_row_tiles(rows, experts, fb_configs[p.config].rows);
+        p.per_split = (int32_t)fb_ceil(KB, p.splits);
+        p.splits = (int32_t)fb_ceil(KB, p.per_split);
         p.quantize = !codes;
     }
     const auto room = [](uint64_t n) { return (n + 255) / 256 * 256; };
@@ -161,7 +195,7 @@ struct MoeRowsLaunch {
 uint32_t device_compute_units();
 int launch_fp8_quantize(const Fp8QuantLaunch &L, hipStream_t s);
 int launch_fp8_values(const Fp8ValuesLaunch &L, hipStream_t s);
-int launch_fp8_few(const Fp8GemmLaunch &L, int row_tiles, hipStream_t s);
+int launch_fp8_few(const Fp8GemmLaunch &L, int weight_tiles, hipStream_t s);
 int launch_fp8_rows(const Fp8GemmLaunch &L, int config, hipStream_t s);
 int launch_moe_sort(const MoeSortLaunch &L, hipStream_t s);
 int launch_moe_gather(const MoeRowsLaunch &L, hipStream_t s);

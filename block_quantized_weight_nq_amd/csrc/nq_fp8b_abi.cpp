@@ -69,8 +69,8 @@ int check_gemm(const nq_fp8_block_args *x, const nq_moe_plan *plan, nq::Fp8Plan 
     const bool raw = (uintptr_t)x->x % 16 == 0 && x->x_row_stride * esz % 16 == 0;
     *p = nq::fb_plan(x->rows, out_rows, experts, x->N, x->K, x->gated != 0, codes, raw, x->out_dtype == NQ_F32,
                      x->rows > 0 && (x->rows - 1) * x->x_row_stride + x->K > 1ll << 32, nq::device_compute_units());
-    const int64_t groups = p->few ? nq::fb_ceil(x->gated ? x->N / 2 : x->N, x->gated ? 16 : 32) * p->waves * 64
-                                  : nq::fb_ceil(x->N, nq::fb_config_cols[p->config]) * 512;
+    const int64_t groups = p->few ? nq::fb_ceil(x->gated ? x->N / 2 : x->N, nq::fb_few_cols(p->weight_tiles, x->gated != 0)) * p->waves * 64
+                                  : (nq::fb_ceil(x->N, nq::fb_configs[p->config].cols) + 256) * 512;
     if (p->few ? groups > THREADS || p->tiles_m > 65535 : p->tiles_m > 0 && groups > THREADS / p->tiles_m) return NQ_ERR_OVERFLOW;
     return NQ_OK;
 }
@@ -184,7 +184,7 @@ NQ_API int nq_gemm_fp8_block(const nq_fp8_block_args *args, const nq_moe_plan *p
         L.x = q.codes, L.x_stride = x.K, L.x_type = nq::FB_CODES;
         L.x_scales = q.scales;
     }
-    return p.few ? nq::launch_fp8_few(L, p.row_tiles, stream) : nq::launch_fp8_rows(L, p.config, stream);
+    return p.few ? nq::launch_fp8_few(L, p.weight_tiles, stream) : nq::launch_fp8_rows(L, p.config, stream);
 }
 
 NQ_API int nq_moe_sort_workspace(int64_t tokens, int64_t top, int64_t experts, uint64_t *bytes) {

@@ -59,11 +59,18 @@ __device__ __forceinline__ void fb_mark_not_finite(float (&f)[N]) {
         if ((__builtin_bit_cast(uint32_t, f[i]) & 0x7FFFFFFFu) >= 0x7F800000u) f[i] = bits_f32(0x7FC00000u);
 }
 
+// The largest of four lanes' words, in each of them.
+__device__ __forceinline__ uint32_t fb_max4(uint32_t m) {
+    uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xF, 0xF, true);  // lane ^ 1
+    m = o > m ? o : m;
+    o = (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xF, 0xF, true);  // lane ^ 2
+    return o > m ? o : m;
+}
+
 // The largest of sixteen lanes' words, in each of them.
 __device__ __forceinline__ uint32_t fb_max16(uint32_t m) {
+    m = fb_max4(m);
     const auto other = [&](uint32_t o) { m = o > m ? o : m; };
-    other((uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xF, 0xF, true));   // lane ^ 1
-    other((uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xF, 0xF, true));   // lane ^ 2
     other((uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x141, 0xF, 0xF, true));  // mirrored in eight
     other((uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x140, 0xF, 0xF, true));  // mirrored in sixteen
     return m;

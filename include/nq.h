@@ -542,14 +542,14 @@ int nq_moe_sort(const void *ids, int32_t wide, int64_t tokens, int64_t top, int6
  * rounded once to out_dtype, out [rows, N].  gated: the weight's first N / 2
  * rows are gates g and the others u, out is [rows, N / 2] of g / (1 + e^-g) * u,
  * and N % 256 == 0 (NQ_ERR_NOT_BLOCK_ALIGNED).
- * Sums are binary32.  Up to 64 rows, and for binary32 outputs, products of
+ * Sums are binary32.  Up to 16 rows, and for binary32 outputs, products of
  * codes are exact; for 16-bit outputs of more rows the 8-bit matrix
  * instruction adds eight products at a time and drops what lies 2^-13 below
  * the largest of the eight.
  * plan NULL: one weight [N, K] for all rows.  Otherwise weight is [experts, N,
  * K] and output row p is the product of the expert whose place p is: of row p
  * of x where `sorted` is 1 (rows = tokens * top), else of row order[p] / top
- * (rows = tokens); rows behind the last place are 0.  "Up to 64 rows" is then
+ * (rows = tokens); rows behind the last place are 0.  "Up to 16 rows" is then
  * tokens * top / experts.
  * The workspace is 16-byte aligned, not used by another call until this one's
  * work is done, and holds nq_gemm_fp8_block_workspace bytes (a function of the

@@ -100,7 +100,7 @@ def sort(ids, experts):
 
 def few_rows(rows, experts=0):
     """Whether a call's products are exact whatever its output type (include/nq.h states the rule)."""
-    return (-(-rows // experts) if experts else rows) <= 64
+    return (-(-rows // experts) if experts else rows) <= 16
 
 
 def experts_product(xw, xs, ww, ws, order, offsets, top, sorted_rows, wide_sums, gated):
