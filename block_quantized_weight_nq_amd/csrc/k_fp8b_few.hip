@@ -47,7 +47,7 @@ __global__ __launch_bounds__(64 * MAX_WAVES) void k_fp8_few(Fp8GemmLaunch a) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = a.waves;
     Fp8Tile t;
     if (a.experts > 0) {
-        t = fb_find_tile(a.offsets, a.experts, a.out_rows, 16, blockIdx.y);
+        t = fb_find_tile(a.offsets, a.experts, a.out_rows, 16, (int32_t)blockIdx.y);
     } else {
         t.expert = 0;
         t.first = (int64_t)blockIdx.y * 16;

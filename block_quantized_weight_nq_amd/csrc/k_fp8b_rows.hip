@@ -30,12 +30,13 @@ __device__ __forceinline__ void fb_meet() {
 
 // Workgroup b's tile.  Workgroups go to the eight XCDs in turn; `span` consecutive tiles stay on one, and run along GM
 // row tiles first, so that an XCD's L2 has few weight rows and rows of x at a time.
-constexpr int32_t XCDS = 8, MOST_SPAN = 32, GM = 8;
-__device__ __forceinline__ void place_tile(int64_t b, int32_t span, int64_t tiles_m, int64_t tiles_n, int64_t *m, int64_t *n) {
-    const int64_t turn = b / XCDS, t = (turn / span * XCDS + b % XCDS) * span + turn % span;
-    const int64_t band = t / (GM * tiles_n), in = t - band * GM * tiles_n, left = tiles_m - band * GM, high = left < GM ? left : GM;
-    *m = high > 0 ? band * GM + in % high : tiles_m;
+constexpr uint32_t XCDS = 8, MOST_SPAN = 32, GM = 8;
+__device__ __forceinline__ void place_tile(uint32_t b, uint32_t span, uint32_t tiles_m, uint32_t tiles_n, uint32_t *m, uint32_t *n) {
+    const uint32_t turn = b / XCDS, q = turn / span, t = (q * XCDS + b % XCDS) * span + (turn - q * span);
+    const uint32_t band = t / (GM * tiles_n), in = t - band * GM * tiles_n, first = band * GM;
+    const uint32_t high = first >= tiles_m ? 0 : tiles_m - first < GM ? tiles_m - first : GM;
     *n = high > 0 ? in / high : 0;
+    *m = high > 0 ? first + in - *n * high : tiles_m;
 }
 
 }  // namespace
@@ -53,18 +54,15 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
     const int tid = threadIdx.x, lane = tid & 63, j = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave % WN, wm = wave / WN;
     const int32_t KB = a.K / FB, NO = GATED ? a.N / 2 : a.N;
-    int64_t tile_m, tile_n;
-    place_tile(blockIdx.x, a.span, a.tiles_m, fb_ceil(a.N, BN), &tile_m, &tile_n);
-    if (tile_m >= a.tiles_m) return;
+    uint32_t tile_m, tile_n;
+    place_tile(blockIdx.x, (uint32_t)a.span, (uint32_t)a.tiles_m, (uint32_t)(a.N + BN - 1) / BN, &tile_m, &tile_n);
+    if (tile_m >= (uint32_t)a.tiles_m) return;
     Fp8Tile t;
     if (a.experts > 0) {
-        t = fb_find_tile(a.offsets, a.experts, a.out_rows, BM, tile_m);
-        t.expert = __builtin_amdgcn_readfirstlane(t.expert);
-        t.first = __builtin_amdgcn_readfirstlane((int)t.first);  // (rows are at most 2^30)
-        t.count = __builtin_amdgcn_readfirstlane(t.count);
+        t = fb_find_tile(a.offsets, a.experts, a.out_rows, BM, (int32_t)tile_m);
     } else {
         t.expert = 0;
-        t.first = tile_m * BM;
+        t.first = (int64_t)tile_m * BM;
         t.count = (int32_t)(a.out_rows - t.first < BM ? a.out_rows - t.first : BM);
     }
     if (t.count == 0) return;
@@ -318,8 +316,8 @@ template <int WN, int WM, int TN, int TM, int OT, bool GATED, typename AT = uint
 static int rows(Fp8GemmLaunch L, hipStream_t s) {
     constexpr int BN = 16 * WN * TN;
     const int64_t tiles = fb_ceil(L.N, BN) * L.tiles_m, part = tiles / (4 * XCDS);
-    L.span = part < 1 ? 1 : part > MOST_SPAN ? MOST_SPAN : (int32_t)part;
-    const int64_t round = XCDS * L.span;  // whole turns of the XCDs: place_tile's tiles are all there
+    L.span = part < 1 ? 1 : part > MOST_SPAN ? (int32_t)MOST_SPAN : (int32_t)part;
+    const int64_t round = (int64_t)XCDS * L.span;  // whole turns of the XCDs: place_tile's tiles are all there
     const dim3 grid((uint32_t)(fb_ceil(tiles, round) * round), (uint32_t)L.splits);
     hipLaunchKernelGGL((k_fp8_rows<WN, WM, TN, TM, OT, GATED, AT>), grid, dim3(64 * WN * WM), 0, s, L);
     if (hipGetLastError() != hipSuccess) return 9;  // NQ_ERR_HIP

@@ -94,33 +94,38 @@ __device__ __forceinline__ kv_h8 fb_half8(uint32_t lo, uint32_t hi) {
     return kv_codes8_f16<KV_E4M3>(w);
 }
 
+// The sum of the lanes' numbers up to each.
+__device__ __forceinline__ int32_t fb_scan(int32_t v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // from 1, 2, 4 and 8 lanes before, in rows of sixteen
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // the end of a row to the next, of rows 0 and 2
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // the end of row 1 to rows 2 and 3
+    return v;
+}
+
 // The row tile of a workgroup (fb_find_tile_host's rule), by a wave: a lane looks at one expert.
-__device__ __forceinline__ Fp8Tile fb_find_tile(const int32_t *offsets, int32_t experts, int64_t rows, int32_t bm, int64_t t) {
+__device__ __forceinline__ Fp8Tile fb_find_tile(const int32_t *offsets, int32_t experts, int64_t rows, int32_t bm, int32_t t) {
     const int lane = threadIdx.x & 63;
+    const int32_t most = (int32_t)rows;  // (at most 2^30)
     for (int32_t e0 = 0; e0 <= experts; e0 += 64) {
         const int32_t e = e0 + lane;
-        int64_t lo = 0, hi = 0;
+        int32_t lo = 0, hi = 0;
         if (e <= experts) {
-            lo = fb_clamp(offsets[e], rows);
-            hi = e < experts ? fb_clamp(offsets[e + 1], rows) : rows;
+            lo = (int32_t)fb_clamp(offsets[e], most);
+            hi = e < experts ? (int32_t)fb_clamp(offsets[e + 1], most) : most;
         }
-        const int32_t n = hi > lo ? (int32_t)((hi - lo + bm - 1) / bm) : 0;
-        int32_t sum = n;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int32_t o = __shfl_up(sum, d, 64);
-            if (lane >= d) sum += o;
-        }
+        const int32_t n = hi > lo ? (int32_t)((uint32_t)(hi - lo + bm - 1) / (uint32_t)bm) : 0, sum = fb_scan(n);
         const uint64_t past = __ballot(sum > t);
         if (past) {
             const int at = __builtin_ctzll(past);
-            const int64_t from = __shfl((int)lo, at, 64), end = __shfl((int)hi, at, 64);
-            const int64_t first = from + (t - (__shfl(sum, at, 64) - __shfl(n, at, 64))) * bm;
+            const int32_t from = __builtin_amdgcn_readlane(lo, at), end = __builtin_amdgcn_readlane(hi, at);
+            const int64_t first = from + (int64_t)(t - (__builtin_amdgcn_readlane(sum, at) - __builtin_amdgcn_readlane(n, at))) * bm;
             if (first < from || first >= end) break;  // offsets that no sort gives: their sum may have left 32 bits
-            const int32_t expert = e0 + at < experts ? e0 + at : -1;
-            return {expert, first, (int32_t)(end - first < bm ? end - first : bm)};
+            return {e0 + at < experts ? e0 + at : -1, first, (int32_t)(end - first < bm ? end - first : bm)};
         }
-        t -= __shfl(sum, 63, 64);
+        t -= __builtin_amdgcn_readlane(sum, 63);
     }
     return {-1, 0, 0};
 }
