@@ -155,16 +155,16 @@ def _lib():
                                             c.c_void_p, c.c_void_p, c.c_void_p]
         L.nq_dequantize_fp8_block.argtypes = [c.c_void_p, c.c_void_p, c.c_int64, c.c_int64, c.c_int64, c.c_int32,
                                               c.c_int32, c.c_void_p, c.c_void_p]
-        # (the arguments: an Fp8BlockArgs by reference, or its bytes)
-        L.nq_gemm_fp8_block_workspace.argtypes = [c.c_void_p, c.POINTER(MoePlanDesc), c.POINTER(c.c_uint64)]
-        L.nq_gemm_fp8_block.argtypes = [c.c_void_p, c.POINTER(MoePlanDesc), c.c_void_p, c.c_uint64, c.c_void_p]
+        # (arguments and plans: an Fp8BlockArgs and a MoePlanDesc by reference, or their bytes)
+        L.nq_gemm_fp8_block_workspace.argtypes = [c.c_void_p, c.c_void_p, c.POINTER(c.c_uint64)]
+        L.nq_gemm_fp8_block.argtypes = [c.c_void_p, c.c_void_p, c.c_void_p, c.c_uint64, c.c_void_p]
         L.nq_moe_sort_workspace.argtypes = [c.c_int64, c.c_int64, c.c_int64, c.POINTER(c.c_uint64)]
         L.nq_moe_sort.argtypes = [c.c_void_p, c.c_int32, c.c_int64, c.c_int64, c.c_int64, c.c_void_p, c.c_void_p,
                                   c.c_void_p, c.c_void_p, c.c_uint64, c.c_void_p]
-        L.nq_moe_gather.argtypes = [c.POINTER(MoePlanDesc), c.c_void_p, c.c_int64, c.c_int64, c.c_void_p, c.c_void_p]
-        L.nq_moe_combine.argtypes = [c.POINTER(MoePlanDesc), c.c_void_p, c.c_int64, c.c_int32, c.c_int64, c.c_void_p,
+        L.nq_moe_gather.argtypes = [c.c_void_p, c.c_void_p, c.c_int64, c.c_int64, c.c_void_p, c.c_void_p]
+        L.nq_moe_combine.argtypes = [c.c_void_p, c.c_void_p, c.c_int64, c.c_int32, c.c_int64, c.c_void_p,
                                      c.c_void_p, c.c_void_p]
-        L.nq_moe_combine_grad.argtypes = [c.POINTER(MoePlanDesc), c.c_void_p, c.c_int64, c.c_void_p, c.c_int64, c.c_int32,
+        L.nq_moe_combine_grad.argtypes = [c.c_void_p, c.c_void_p, c.c_int64, c.c_void_p, c.c_int64, c.c_int32,
                                           c.c_int64, c.c_void_p, c.c_void_p, c.c_void_p, c.c_void_p]
         L.nq_status_string.argtypes = [c.c_int]
         L.nq_status_string.restype = c.c_char_p
@@ -873,8 +873,9 @@ def kv_attention(cache, q, token_start, lengths, table, scale=None, window=0, ma
 
 # --- E4M3 blocks of 128, and rows sorted by expert ----------------------------------------------------------------
 
-_BLOCK_ARGS = struct.Struct("@PqPPPPqqqiiii")
-assert _BLOCK_ARGS.size == ctypes.sizeof(Fp8BlockArgs)
+_BLOCK_ARGS, _PLAN_ARGS = struct.Struct("@PqPPPPqqqiiii"), struct.Struct("@PPPqqq")
+assert _BLOCK_ARGS.size == ctypes.sizeof(Fp8BlockArgs) and _PLAN_ARGS.size == ctypes.sizeof(MoePlanDesc)
+_SORT_WORKSPACES = {}
 
 
 def _block_shapes(shape, tile):
@@ -904,7 +905,11 @@ def quantize_fp8_block(x, tile=1, stream=None):
         with _at(index):
             return quantize_fp8_block(x, tile)
     shape, strides = x.shape, x.stride()
-    matrices, rows, cols, scales_shape = _block_shapes(shape, tile)
+    if tile == 1 and len(shape) == 2:  # (activations: a call in every layer)
+        matrices, (rows, cols) = 1, shape
+        scales_shape = (rows, cols // FP8_BLOCK)
+    else:
+        matrices, rows, cols, scales_shape = _block_shapes(shape, tile)
     if strides[-1] != 1 and x.numel() or (len(shape) == 3 and matrices > 1 and strides[0] != rows * strides[1]):
         raise ValueError("x must have contiguous columns, and matrices must follow each other row by row")
     codes = x.new_empty(shape, dtype=_F8)
@@ -983,11 +988,18 @@ class MoePlan:
         _refuse_other(self.index, (("order", order, _I32), ("places", places, _I32), ("offsets", offsets, _I32)))
         if places.dim() != 2 or order.numel() != places.numel() or not 2 <= offsets.numel() <= MOE_MAX_EXPERTS + 1:
             raise ValueError("places must be [tokens, top], order one entry for each pair, offsets experts + 1")
+        tokens, top = places.shape
+        self._take(order, places, offsets, order.data_ptr(), places.data_ptr(), offsets.data_ptr(), tokens, top,
+                   offsets.numel() - 1)
+
+    def _take(self, order, places, offsets, order_at, places_at, offsets_at, tokens, top, experts):
         self.order, self.places, self.offsets = order, places, offsets
-        self.tokens, self.top = places.shape
-        self.pairs, self.experts, self.device = order.numel(), offsets.numel() - 1, order.device
-        self._ref = ctypes.byref(MoePlanDesc(order.data_ptr(), places.data_ptr(), offsets.data_ptr(), self.tokens,
-                                             self.top, self.experts))
+        self.tokens, self.top, self.pairs, self.experts = tokens, top, tokens * top, experts
+        self._ref = _PLAN_ARGS.pack(order_at, places_at, offsets_at, tokens, top, experts)
+
+    @property
+    def device(self):
+        return self.order.device
 
 
 def _refuse_other(index, ints):
@@ -1105,18 +1117,30 @@ def moe_sort(ids, experts, stream=None):
     if not 1 <= experts <= MOE_MAX_EXPERTS or top < 1:
         raise ValueError(f"experts must be 1 to {MOE_MAX_EXPERTS} and top at least 1")
     pairs, lib = tokens * top, _LIB or _lib()
-    asked = ctypes.c_uint64()
-    st = lib.nq_moe_sort_workspace(tokens, top, experts, asked)
-    need = asked.value
-    words = ids.new_empty(2 * pairs + experts + 1 + need // 4, dtype=_I32)
-    p = words.data_ptr()
+    need, st = _SORT_WORKSPACES.get((pairs, experts)), NQ_OK  # a function of these alone: asked for once for each
+    if need is None:
+        asked = ctypes.c_uint64()
+        st = lib.nq_moe_sort_workspace(tokens, top, experts, asked)
+        need = asked.value
+        if st == NQ_OK:
+            if len(_SORT_WORKSPACES) >= 1024:
+                _SORT_WORKSPACES.clear()
+            _SORT_WORKSPACES[pairs, experts] = need
     if st == NQ_OK:
-        st = lib.nq_moe_sort(ids.data_ptr(), ids.dtype is _I64, tokens, top, experts, p, p + 4 * pairs, p + 8 * pairs,
-                             p + 8 * pairs + 4 * (experts + 1) if need else None, need, _STREAM(index))
+        # one allocation: order, places, offsets, workspace
+        words = ids.new_empty(2 * pairs + experts + 1 + need // 4, dtype=_I32)
+        order_at = words.data_ptr()
+        places_at = order_at + 4 * pairs
+        offsets_at = places_at + 4 * pairs
+        st = lib.nq_moe_sort(ids.data_ptr(), ids.dtype is _I64, tokens, top, experts, order_at, places_at, offsets_at,
+                             offsets_at + 4 * (experts + 1) if need else None, need, _STREAM(index))
     if st != NQ_OK:
         raise NqError(st, f"ids {list(ids.shape)}, {experts} experts")
-    order, places, offsets = words[:2 * pairs + experts + 1].split_with_sizes((pairs, pairs, experts + 1))
-    return MoePlan(order, places.view(tokens, top), offsets)
+    parts = words.split_with_sizes((pairs, pairs, experts + 1, need // 4) if need else (pairs, pairs, experts + 1))
+    plan = MoePlan.__new__(MoePlan)
+    plan.index = index
+    plan._take(parts[0], parts[1].view(tokens, top), parts[2], order_at, places_at, offsets_at, tokens, top, experts)
+    return plan
 
 
 def moe_gather(x, plan, stream=None):

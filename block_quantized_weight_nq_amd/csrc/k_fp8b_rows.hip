@@ -221,14 +221,28 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
     for (int l = 0; l < NW + NX; l++) load(even, kb0, l);
     fb_meet();
     int32_t kb = kb0;
-    for (; kb + 1 < kb1; kb += 2) {
-        if (((kb - kb0) & (SB - 1)) == 0 && kb + SB < kb1) load_scales(kb + SB);
-        multiply(std::true_type(), even, w0, kb, odd, w1, kb + 1);
-        fb_meet();
-        multiply(std::true_type(), odd, w1, kb + 1, even, w0, kb + 2 < kb1 ? kb + 2 : kb + 1);  // (the last loads are not used)
-        fb_meet();
+    if (16 * wm * TM >= t.count) {  // none of the wave's rows is there: it loads for the others
+        const auto load_all = [&](uint8_t *b, int32_t k) {
+#pragma unroll
+            for (int l = 0; l < NW + NX; l++) load(b, k, l);
+        };
+        for (; kb + 1 < kb1; kb += 2) {
+            if (((kb - kb0) & (SB - 1)) == 0 && kb + SB < kb1) load_scales(kb + SB);
+            load_all(odd, kb + 1);
+            fb_meet();
+            load_all(even, kb + 2 < kb1 ? kb + 2 : kb + 1);
+            fb_meet();
+        }
+    } else {
+        for (; kb + 1 < kb1; kb += 2) {
+            if (((kb - kb0) & (SB - 1)) == 0 && kb + SB < kb1) load_scales(kb + SB);
+            multiply(std::true_type(), even, w0, kb, odd, w1, kb + 1);
+            fb_meet();
+            multiply(std::true_type(), odd, w1, kb + 1, even, w0, kb + 2 < kb1 ? kb + 2 : kb + 1);  // (the last loads are not used)
+            fb_meet();
+        }
+        if (kb < kb1) multiply(std::false_type(), even, w0, kb, odd, w1, kb);
     }
-    if (kb < kb1) multiply(std::false_type(), even, w0, kb, odd, w1, kb);
     // lane (j, g): outputs 4 g .. 4 g + 3 of each tile of weight rows, of row j
     if (a.splits > 1) {
 #pragma unroll
