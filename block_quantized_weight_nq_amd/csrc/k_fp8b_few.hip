@@ -113,25 +113,26 @@ __global__ __launch_bounds__(64 * MAX_WAVES) void k_fp8_few(Fp8GemmLaunch a) {
         for (int q = tid >> 2; q < pairs; q += 16 * waves) {
             const int b = q / t.count, m = q - b * t.count;
             const int64_t at = fb_source_row(a, t.first + m) * a.x_stride + (int64_t)(c0 + b) * FB + 32 * l;
-            float f[4][8];
+            constexpr int IN = RAW ? XT : 0;
+            FbRaw<IN> v[4];
 #pragma unroll
-            for (int u = 0; u < 4; u++) fb_read8<RAW ? XT : 0, true>(a.x, at + 8 * u, f[u]);
-            uint32_t top = 0;
+            for (int u = 0; u < 4; u++) v[u] = fb_raw8<IN, true>(a.x, at + 8 * u);
+            uint32_t words = 0;
 #pragma unroll
-            for (int u = 0; u < 4; u++) top = fb_amax8(f[u], top);
-            top = fb_max4(top);
-            if (top >= 0x7F800000u) {
+            for (int u = 0; u < 4; u++) words = fb_amax8<IN>(v[u], words);
+            uint32_t top = fb_max4(fb_amax_word<IN>(words));
+            const bool bad = top >= 0x7F800000u;
+            if (bad) {
                 top = 0;
 #pragma unroll
-                for (int u = 0; u < 4; u++) top = fb_amax8_finite(f[u], top);
+                for (int u = 0; u < 4; u++) top = fb_amax8_finite<IN>(v[u], top);
                 top = fb_max4(top);
-#pragma unroll
-                for (int u = 0; u < 4; u++) fb_mark_not_finite(f[u]);
             }
-            const float scale = fmaxf(__builtin_bit_cast(float, top) / 448.0f, FB_TINY), inv = 1.0f / scale;
+            const float scale = fb_scale(top), inv = 1.0f / scale;
 #pragma unroll
             for (int h = 0; h < 2; h++) {
-                const kv_u2 lo = fb_codes8(f[2 * h], inv), hi = fb_codes8(f[2 * h + 1], inv);
+                const kv_u2 lo = bad ? fb_codes8<IN, true>(v[2 * h], inv) : fb_codes8<IN, false>(v[2 * h], inv);
+                const kv_u2 hi = bad ? fb_codes8<IN, true>(v[2 * h + 1], inv) : fb_codes8<IN, false>(v[2 * h + 1], inv);
                 *(kv_u4 *)(lds + x_place(b, t.count, m, 2 * l + h)) = kv_u4{lo[0], lo[1], hi[0], hi[1]};
             }
             if (l == 0) scales[q] = scale;

@@ -23,91 +23,101 @@ __global__ __launch_bounds__(TB) void k_fp8_quant_rows(Fp8QuantLaunch a) {
     const int64_t blocks = a.cols / FB, all = a.rows * blocks, step = (int64_t)gridDim.x * (TB / 16);
     for (int64_t i = (int64_t)blockIdx.x * (TB / 16) + (threadIdx.x >> 4); i < all; i += step) {
         const int64_t r = i / blocks, b = i - r * blocks;
-        float f[8];
-        fb_read8<IN, VEC>(a.x, r * a.row_stride + b * FB + 8 * lane, f);
-        uint32_t top = fb_amax8(f, 0);
-        top = fb_max16(top);
+        const FbRaw<IN> v = fb_raw8<IN, VEC>(a.x, r * a.row_stride + b * FB + 8 * lane);
+        uint32_t top = fb_max16(fb_amax_word<IN>(fb_amax8<IN>(v, 0)));
         const bool bad = top >= 0x7F800000u;
-        if (bad) {
-            top = fb_max16(fb_amax8_finite(f, 0));
-            fb_mark_not_finite(f);
-        }
-        const float scale = fmaxf(__builtin_bit_cast(float, top) / 448.0f, FB_TINY), inv = 1.0f / scale;
-        *(kv_u2 *)(a.codes + r * a.cols + b * FB + 8 * lane) = fb_codes8(f, inv);
+        if (bad) top = fb_max16(fb_amax8_finite<IN>(v, 0));
+        const float scale = fb_scale(top), inv = 1.0f / scale;
+        *(kv_u2 *)(a.codes + r * a.cols + b * FB + 8 * lane) = bad ? fb_codes8<IN, true>(v, inv) : fb_codes8<IN, false>(v, inv);
         if (lane == 0) a.scales[i] = scale;
     }
 }
 
-// 128 rows and 128 columns a block: a workgroup, each thread eight columns of every sixteenth row.
+// 128 rows and 128 columns a block: a workgroup, each thread eight columns of ROWS rows, which it holds as they are (16-bit
+// values in half the registers of binary32 ones; held as binary32, 56.8 us for [14336, 4096] bfloat16).
 template <int IN, bool VEC>
-__global__ __launch_bounds__(TB) void k_fp8_quant_tile(Fp8QuantLaunch a) {
-    __shared__ uint32_t wmax[TB / 64];
+__global__ __launch_bounds__(IN == 0 ? 2 * TB : TB) void k_fp8_quant_tile(Fp8QuantLaunch a) {
+    constexpr int THREADS = IN == 0 ? 2 * TB : TB, STEP = THREADS / 16, ROWS = FB / STEP;
+    __shared__ uint32_t wmax[2][THREADS / 64];
     const int tid = threadIdx.x, c = 8 * (tid & 15), r0 = tid >> 4;
     const int64_t blocks = a.cols / FB, bands = fb_ceil(a.rows, FB), all = a.matrices * bands * blocks;
+    int turn = 0;
     for (int64_t i = blockIdx.x; i < all; i += gridDim.x) {
-        const int64_t b = i % blocks, band = i / blocks, m = band / bands, rb = (band - m * bands) * FB;
+        const int64_t band = i / blocks, b = i - band * blocks, m = band / bands, rb = (band - m * bands) * FB;
         const int rows = (int)(a.rows - rb < FB ? a.rows - rb : FB);
         const int64_t row0 = m * a.rows + rb;
-        float f[8][8];
-        uint32_t top = 0;
+        FbRaw<IN> v[ROWS];
 #pragma unroll
-        for (int k = 0; k < 8; k++) {
-            const int r = r0 + 16 * k;
-#pragma unroll
-            for (int j = 0; j < 8; j++) f[k][j] = 0.0f;
-            if (r < rows) fb_read8<IN, VEC>(a.x, (row0 + r) * a.row_stride + b * FB + c, f[k]);
+        for (int k = 0; k < ROWS; k++) {
+            const int r = r0 + STEP * k;
+            v[k] = fb_raw8<IN, VEC>(a.x, (row0 + (r < rows ? r : rows - 1)) * a.row_stride + b * FB + c);  // (a row twice changes no maximum)
         }
-        const auto largest = [&](bool finite) {
-            top = 0;
-#pragma unroll
-            for (int k = 0; k < 8; k++) top = finite ? fb_amax8_finite(f[k], top) : fb_amax8(f[k], top);
+        const auto largest = [&](uint32_t top) {
             top = fb_max16(top);
             for (int d = 16; d < 64; d <<= 1) {
                 const uint32_t other = __shfl_xor(top, d, 64);
                 top = other > top ? other : top;
             }
+            turn ^= 1;  // the words of the turn before may still be read
+            if ((tid & 63) == 0) wmax[turn][tid >> 6] = top;
             __syncthreads();
-            if ((tid & 63) == 0) wmax[tid >> 6] = top;
-            __syncthreads();
-            for (int w = 0; w < TB / 64; w++) top = wmax[w] > top ? wmax[w] : top;
+            for (int w = 0; w < THREADS / 64; w++) top = wmax[turn][w] > top ? wmax[turn][w] : top;
+            return top;
         };
-        largest(false);
-        if (top >= 0x7F800000u) {
-            largest(true);
+        uint32_t words = 0;
 #pragma unroll
-            for (int k = 0; k < 8; k++) fb_mark_not_finite(f[k]);
+        for (int k = 0; k < ROWS; k++) words = fb_amax8<IN>(v[k], words);
+        uint32_t top = largest(fb_amax_word<IN>(words));
+        const bool bad = top >= 0x7F800000u;
+        if (bad) {
+            top = 0;
+#pragma unroll
+            for (int k = 0; k < ROWS; k++) top = fb_amax8_finite<IN>(v[k], top);
+            top = largest(top);
         }
-        const float scale = fmaxf(__builtin_bit_cast(float, top) / 448.0f, FB_TINY), inv = 1.0f / scale;
+        const float scale = fb_scale(top), inv = 1.0f / scale;
         if (tid == 0) a.scales[i] = scale;
 #pragma unroll
-        for (int k = 0; k < 8; k++) {
-            const int r = r0 + 16 * k;
-            if (r < rows) *(kv_u2 *)(a.codes + (row0 + r) * a.cols + b * FB + c) = fb_codes8(f[k], inv);
+        for (int k = 0; k < ROWS; k++) {
+            const int r = r0 + STEP * k;
+            if (r < rows)
+                *(kv_u2 *)(a.codes + (row0 + r) * a.cols + b * FB + c) = bad ? fb_codes8<IN, true>(v[k], inv) : fb_codes8<IN, false>(v[k], inv);
         }
     }
 }
 
-// Sixteen codes a thread and turn.
+// A thread and turn: four accesses of 16 bytes of values, side by side with its neighbours'.
 template <int OT>
 __global__ __launch_bounds__(TB) void k_fp8_values(Fp8ValuesLaunch a) {
-    const int64_t per = a.cols / 16, blocks = a.cols / FB, bands = fb_ceil(a.rows, a.tile);
-    const int64_t all = a.matrices * a.rows * per, step = (int64_t)gridDim.x * TB;
-    for (int64_t i = (int64_t)blockIdx.x * TB + threadIdx.x; i < all; i += step) {
-        const int64_t row = i / per, c = i - row * per;
-        int64_t band = row;
-        if (a.tile != 1) {
-            const int64_t m = row / a.rows;
-            band = m * bands + (row - m * a.rows) / FB;
+    constexpr int PER = OT == 0 ? 4 : 8, TURNS = 4;
+    const int64_t per = a.cols / PER, blocks = a.cols / FB, bands = fb_ceil(a.rows, a.tile);
+    const int64_t all = a.matrices * a.rows * per, step = (int64_t)gridDim.x * TB * TURNS;
+    for (int64_t i0 = (int64_t)blockIdx.x * TB * TURNS + threadIdx.x; i0 < all; i0 += step) {
+        uint32_t w[TURNS][PER / 4];
+        float scale[TURNS];
+#pragma unroll
+        for (int k = 0; k < TURNS; k++) {
+            const int64_t i = i0 + k * TB < all ? i0 + k * TB : i0, row = i / per, c = i - row * per;
+            int64_t band = row;
+            if (a.tile != 1) {
+                const int64_t m = row / a.rows;
+                band = m * bands + (row - m * a.rows) / FB;
+            }
+            scale[k] = a.scales[band * blocks + c / (FB / PER)];
+#pragma unroll
+            for (int e = 0; e < PER / 4; e++) w[k][e] = ((const uint32_t *)a.codes)[i * (PER / 4) + e];
         }
-        const float scale = a.scales[band * blocks + c / 8];
-        const kv_u4 w = *(const kv_u4 *)(a.codes + 16 * i);
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-            float f[4];
-            kv_codes4_f32<KV_E4M3>(w[e], f);
+        for (int k = 0; k < TURNS; k++) {
+            if (i0 + k * TB >= all) break;
 #pragma unroll
-            for (int k = 0; k < 4; k++) f[k] = f[k] * scale;
-            kv_write4<OT>(a.out, 16 * i + 4 * e, f);
+            for (int e = 0; e < PER / 4; e++) {
+                float f[4];
+                kv_codes4_f32<KV_E4M3>(w[k][e], f);
+#pragma unroll
+                for (int j = 0; j < 4; j++) f[j] = f[j] * scale[k];
+                kv_write4<OT>(a.out, (i0 + k * TB) * PER + 4 * e, f);
+            }
         }
     }
 }
@@ -128,10 +138,11 @@ static int quantize_in(const Fp8QuantLaunch &L, hipStream_t s) {
         else
             hipLaunchKernelGGL((k_fp8_quant_rows<IN, false>), grid, dim3(TB), 0, s, a);
     } else {
+        const dim3 threads(IN == 0 ? 2 * TB : TB);
         if (vec)
-            hipLaunchKernelGGL((k_fp8_quant_tile<IN, true>), grid, dim3(TB), 0, s, a);
+            hipLaunchKernelGGL((k_fp8_quant_tile<IN, true>), grid, threads, 0, s, a);
         else
-            hipLaunchKernelGGL((k_fp8_quant_tile<IN, false>), grid, dim3(TB), 0, s, a);
+            hipLaunchKernelGGL((k_fp8_quant_tile<IN, false>), grid, threads, 0, s, a);
     }
     return hipGetLastError() == hipSuccess ? 0 : 9;  // NQ_ERR_HIP
 }
@@ -146,7 +157,7 @@ int launch_fp8_quantize(const Fp8QuantLaunch &L, hipStream_t s) {
 }
 
 int launch_fp8_values(const Fp8ValuesLaunch &L, hipStream_t s) {
-    const int64_t units = fb_ceil(L.matrices * L.rows * (L.cols / 16), TB), most = (int64_t)device_compute_units() * 32;
+    const int64_t units = fb_ceil(L.matrices * L.rows * (L.cols / (L.out_dtype == 0 ? 4 : 8)), 4 * TB), most = (int64_t)device_compute_units() * 32;
     if (units == 0) return 0;
     const dim3 grid((uint32_t)(units < most ? units : most));
     switch (L.out_dtype) {

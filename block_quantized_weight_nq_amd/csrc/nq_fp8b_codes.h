@@ -29,34 +29,76 @@ __device__ __forceinline__ void fb_read8(const void *x, int64_t i, float (&f)[8]
     }
 }
 
-// The largest magnitude of N values and m, as words: integers in the same order, infinities and NaN above all.
-template <int N>
-__device__ __forceinline__ uint32_t fb_amax(const float (&f)[N], uint32_t m) {
+// Eight consecutive elements as they are.
+template <int IN>
+struct FbRaw {
+    uint32_t w[IN == 0 ? 8 : 4];
+};
+
+template <int IN, bool VEC>
+__device__ __forceinline__ FbRaw<IN> fb_raw8(const void *x, int64_t i) {
+    FbRaw<IN> r;
+    if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < N; i++) {
-        const uint32_t x = __builtin_bit_cast(uint32_t, f[i]) & 0x7FFFFFFFu;
-        m = x > m ? x : m;
+        for (int v = 0; v < (IN == 0 ? 2 : 1); v++) {
+            const kv_u4 w = ((const kv_u4 *)((const uint8_t *)x + i * (IN == 0 ? 4 : 2)))[v];
+#pragma unroll
+            for (int j = 0; j < 4; j++) r.w[4 * v + j] = w[j];
+        }
+    } else if constexpr (IN == 0) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) r.w[j] = ((const uint32_t *)x)[i + j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++) r.w[j] = ((const uint16_t *)x)[i + 2 * j] | (uint32_t)((const uint16_t *)x)[i + 2 * j + 1] << 16;
     }
-    return m;
+    return r;
 }
-template <int N>
-__device__ __forceinline__ uint32_t fb_amax_finite(const float (&f)[N], uint32_t m) {
+
+template <int IN>
+__device__ __forceinline__ float fb_value(const FbRaw<IN> &r, int j) {
+    if constexpr (IN == 0) return __builtin_bit_cast(float, r.w[j]);
+    const uint32_t w = r.w[j >> 1];
+    if constexpr (IN == 1) return f16(j & 1 ? w >> 16 : w & 0xFFFFu);
+    return bits_f32(j & 1 ? w & 0xFFFF0000u : w << 16);
+}
+
+// The largest magnitude of eight elements and m, in the type's own words (two 16-bit ones side by side): integers in the
+// same order, infinities and NaN above all.
+template <int IN>
+__device__ __forceinline__ uint32_t fb_amax8(const FbRaw<IN> &r, uint32_t m) {
+    if constexpr (IN == 0) {
 #pragma unroll
-    for (int i = 0; i < N; i++) {
-        const uint32_t x = __builtin_bit_cast(uint32_t, f[i]) & 0x7FFFFFFFu;
+        for (int i = 0; i < 8; i++) {
+            const uint32_t x = r.w[i] & 0x7FFFFFFFu;
+            m = x > m ? x : m;
+        }
+        return m;
+    } else {
+        typedef uint16_t u2 __attribute__((ext_vector_type(2)));
+        u2 t = __builtin_bit_cast(u2, m);
+#pragma unroll
+        for (int i = 0; i < 4; i++) t = __builtin_elementwise_max(t, __builtin_bit_cast(u2, r.w[i] & 0x7FFF7FFFu));
+        return __builtin_bit_cast(uint32_t, t);
+    }
+}
+// ... as a binary32 word, what is not finite above all that is.
+template <int IN>
+__device__ __forceinline__ uint32_t fb_amax_word(uint32_t m) {
+    if constexpr (IN == 0) return m;
+    const uint32_t h = (m >> 16) > (m & 0xFFFFu) ? m >> 16 : m & 0xFFFFu;
+    if constexpr (IN == 2) return h << 16;
+    return h >= 0x7C00u ? 0x7F800000u : __builtin_bit_cast(uint32_t, f16(h));
+}
+// The largest finite magnitude of eight elements and m, as a binary32 word.
+template <int IN>
+__device__ __forceinline__ uint32_t fb_amax8_finite(const FbRaw<IN> &r, uint32_t m) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const uint32_t x = __builtin_bit_cast(uint32_t, fb_value<IN>(r, i)) & 0x7FFFFFFFu;
         m = x > m && x < 0x7F800000u ? x : m;
     }
     return m;
-}
-__device__ __forceinline__ uint32_t fb_amax8(const float (&f)[8], uint32_t m) { return fb_amax<8>(f, m); }
-__device__ __forceinline__ uint32_t fb_amax8_finite(const float (&f)[8], uint32_t m) { return fb_amax_finite<8>(f, m); }
-
-// Infinities become NaN, so that their codes are.
-template <int N>
-__device__ __forceinline__ void fb_mark_not_finite(float (&f)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; i++)
-        if ((__builtin_bit_cast(uint32_t, f[i]) & 0x7FFFFFFFu) >= 0x7F800000u) f[i] = bits_f32(0x7FC00000u);
 }
 
 // The largest of four lanes' words, in each of them.
@@ -81,12 +123,22 @@ __device__ __forceinline__ uint32_t fb_codes4(float a, float b, float c, float d
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
 }
 
-// Eight codes of RN32(f * inv).
-__device__ __forceinline__ kv_u2 fb_codes8(const float (&f)[8], float inv) {
-    kv_u2 w = {fb_codes4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
-               fb_codes4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv)};
+// Eight codes of RN32(x * inv); BAD: some may not be finite, and become NaN.
+template <int IN, bool BAD>
+__device__ __forceinline__ kv_u2 fb_codes8(const FbRaw<IN> &r, float inv) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const float v = fb_value<IN>(r, i);
+        f[i] = v * inv;
+        if (BAD && !(v - v == 0.0f)) f[i] = bits_f32(0x7FC00000u);
+    }
+    kv_u2 w = {fb_codes4(f[0], f[1], f[2], f[3]), fb_codes4(f[4], f[5], f[6], f[7])};
     return w;
 }
+
+// The scale of a block whose largest magnitude is the binary32 word `top`.
+__device__ __forceinline__ float fb_scale(uint32_t top) { return fmaxf(__builtin_bit_cast(float, top) / 448.0f, FB_TINY); }
 
 // Two dwords of codes as eight binary16 numbers (exact).
 __device__ __forceinline__ kv_h8 fb_half8(uint32_t lo, uint32_t hi) {
