@@ -310,19 +310,38 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
     }
 }
 
-// The pieces' sums in order, and the epilogue.
+// The pieces' sums in order, and the epilogue; four columns a thread where they are a multiple of four.
+template <int PER>
 __global__ __launch_bounds__(256) void k_fp8_join(Fp8GemmLaunch a) {
-    const int32_t NO = a.gated ? a.N / 2 : a.N;
-    const int64_t all = a.out_rows * NO, step = (int64_t)gridDim.x * 256, piece = a.out_rows * a.N;
+    const int32_t NO = a.gated ? a.N / 2 : a.N, per = NO / PER;
+    const int64_t all = a.out_rows * per, step = (int64_t)gridDim.x * 256, piece = a.out_rows * a.N;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += step) {
-        const int64_t m = i / NO, n = i - m * NO;
-        const float *p = a.part + m * a.N + n;
-        float y = p[0], up = a.gated ? p[NO] : 0.0f;
-        for (int s = 1; s < a.splits; s++) {
-            y += p[s * piece];
-            if (a.gated) up += p[s * piece + NO];
+        const int64_t m = i / per, n = (i - m * per) * PER;
+        const float *const p = a.part + m * a.N + n;
+        float y[PER], up[PER];
+        const auto add = [&](const float *from, float (&to)[PER], bool first) {
+            float v[PER];
+            if constexpr (PER == 4) {
+                const kv_f4 w = *(const kv_f4 *)from;
+#pragma unroll
+                for (int q = 0; q < 4; q++) v[q] = w[q];
+            } else {
+                v[0] = from[0];
+            }
+#pragma unroll
+            for (int q = 0; q < PER; q++) to[q] = first ? v[q] : to[q] + v[q];
+        };
+        for (int s = 0; s < a.splits; s++) {
+            add(p + s * piece, y, s == 0);
+            if (a.gated) add(p + s * piece + NO, up, s == 0);
         }
-        fb_write1(a.out, i, a.gated ? fb_silu<0>(y) * up : y, a.out_dtype);
+        if (a.gated)
+#pragma unroll
+            for (int q = 0; q < PER; q++) y[q] = fb_silu<0>(y[q]) * up[q];
+        if constexpr (PER == 4)
+            fb_write4(a.out, m * NO + n, y, a.out_dtype);
+        else
+            fb_write1(a.out, m * NO + n, y[0], a.out_dtype);
     }
 }
 
@@ -336,8 +355,14 @@ static int rows(Fp8GemmLaunch L, hipStream_t s) {
     hipLaunchKernelGGL((k_fp8_rows<WN, WM, TN, TM, OT, GATED, AT>), grid, dim3(64 * WN * WM), 0, s, L);
     if (hipGetLastError() != hipSuccess) return 9;  // NQ_ERR_HIP
     if (L.splits > 1) {
-        const int64_t units = fb_ceil(L.out_rows * (GATED ? L.N / 2 : L.N), 256), most = (int64_t)device_compute_units() * 16;
-        hipLaunchKernelGGL(k_fp8_join, dim3((uint32_t)(units < most ? units : most)), dim3(256), 0, s, L);
+        const int32_t no = GATED ? L.N / 2 : L.N;
+        const bool four = L.N % 4 == 0 && no % 4 == 0;
+        const int64_t units = fb_ceil(L.out_rows * no, four ? 1024 : 256), most = (int64_t)device_compute_units() * 16;
+        const dim3 join((uint32_t)(units < most ? units : most));
+        if (four)
+            hipLaunchKernelGGL(k_fp8_join<4>, join, dim3(256), 0, s, L);
+        else
+            hipLaunchKernelGGL(k_fp8_join<1>, join, dim3(256), 0, s, L);
         if (hipGetLastError() != hipSuccess) return 9;
     }
     return 0;

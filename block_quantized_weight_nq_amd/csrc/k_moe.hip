@@ -82,10 +82,15 @@ __global__ __launch_bounds__(64 * WAVES) void k_moe_place(MoeSortLaunch a) {
             all = mine;
             if constexpr (!ONE) {
                 all = 0;
-                for (int c = 0; c < a.chunks; c++) {
-                    const int32_t n = a.counts[(int64_t)c * E + e];
-                    before += c < (int)blockIdx.x ? n : 0;
-                    all += n;
+                for (int c0 = 0; c0 < a.chunks; c0 += 16) {  // sixteen loads on their way (one at a time: 15.4 us for 32 chunks)
+                    int32_t n[16];
+#pragma unroll
+                    for (int k = 0; k < 16; k++) n[k] = c0 + k < a.chunks ? a.counts[(int64_t)(c0 + k) * E + e] : 0;
+#pragma unroll
+                    for (int k = 0; k < 16; k++) {
+                        before += c0 + k < (int)blockIdx.x ? n[k] : 0;
+                        all += n[k];
+                    }
                 }
             }
         }
