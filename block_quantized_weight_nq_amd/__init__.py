@@ -910,11 +910,12 @@ def quantize_fp8_block(x, tile=1, stream=None):
         scales_shape = (rows, cols // FP8_BLOCK)
     else:
         matrices, rows, cols, scales_shape = _block_shapes(shape, tile)
-    if strides[-1] != 1 and x.numel() or (len(shape) == 3 and matrices > 1 and strides[0] != rows * strides[1]):
+    if strides[-1] != 1 and x.numel() or (matrices > 1 and strides[0] != rows * strides[1]):
         raise ValueError("x must have contiguous columns, and matrices must follow each other row by row")
+    code = _KV_DTYPES.get(x.dtype)
     codes = x.new_empty(shape, dtype=_F8)
     scales = x.new_empty(scales_shape, dtype=_F32)
-    st = (_LIB or _lib()).nq_quantize_fp8_block(x.data_ptr(), _kv_dtype(x.dtype), matrices, rows, cols, strides[-2], tile,
+    st = (_LIB or _lib()).nq_quantize_fp8_block(x.data_ptr(), _dtype_code(x.dtype) if code is None else code, matrices, rows, cols, strides[-2], tile,
                                                 codes.data_ptr(), scales.data_ptr(), _STREAM(index))
     if st != NQ_OK:
         raise NqError(st, f"x {list(shape)} {x.dtype}, tile {tile}")
@@ -1163,9 +1164,9 @@ def moe_gather(x, plan, stream=None):
 
 
 def _weights_of(weights, plan):
-    if weights is None:
-        return None
-    _scales_of("weights", weights, (plan.tokens, plan.top), plan.index)
+    if weights.dtype is not _F32 or weights.shape != plan.places.shape or weights.get_device() != plan.index or \
+            not weights.is_contiguous():
+        _scales_of("weights", weights, (plan.tokens, plan.top), plan.index)
     return weights.data_ptr()
 
 
@@ -1179,11 +1180,15 @@ def moe_combine(rows, plan, weights=None, stream=None):
     if _DEVICE() != index:
         with _at(index):
             return moe_combine(rows, plan, weights)
-    _rows_of("rows", rows, plan.pairs, None, index)
-    cols = rows.shape[1]
-    out = rows.new_empty((plan.tokens, cols))
-    st = (_LIB or _lib()).nq_moe_combine(plan._ref, rows.data_ptr(), rows.stride(0), _kv_dtype(rows.dtype), cols,
-                                         _weights_of(weights, plan), out.data_ptr(), _STREAM(index))
+    shape, strides, tokens = rows.shape, rows.stride(), plan.tokens
+    if len(shape) != 2 or shape[0] != plan.pairs or rows.get_device() != index or strides[1] != 1:
+        _rows_of("rows", rows, plan.pairs, None, index)
+    code = _KV_DTYPES.get(rows.dtype)
+    cols = shape[1]
+    out = rows.new_empty((tokens, cols))
+    st = (_LIB or _lib()).nq_moe_combine(plan._ref, rows.data_ptr(), strides[0], _dtype_code(rows.dtype) if code is None else code,
+                                         cols, None if weights is None else _weights_of(weights, plan), out.data_ptr(),
+                                         _STREAM(index))
     if st != NQ_OK:
         raise NqError(st, f"rows {list(rows.shape)} {rows.dtype}")
     return out
@@ -1206,7 +1211,7 @@ def moe_combine_grad(grad, rows, plan, weights=None, stream=None):
     if grad.dtype is not rows.dtype:
         raise ValueError("grad must have the rows' type")
     out = rows.new_empty((plan.pairs, cols))
-    pointer = _weights_of(weights, plan)
+    pointer = None if weights is None else _weights_of(weights, plan)
     out_weights = weights.new_empty(weights.shape) if weights is not None else None
     st = (_LIB or _lib()).nq_moe_combine_grad(plan._ref, grad.data_ptr(), grad.stride(0), rows.data_ptr(), rows.stride(0),
                                               _kv_dtype(rows.dtype), cols, pointer, out.data_ptr(),

@@ -159,12 +159,12 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
         float sx[TM];
         const int at = (kb - kb0) & (SB - 1);
         const uint8_t *const s = scales + ((kb - kb0) / SB & 1) * BM * SB * 4 + (16 * wm * TM + j) * SB * 4 + ((at ^ (j >> 2 & 3)) << 2);
-#pragma unroll
-        for (int k = 0; k < TM; k++) sx[k] = *(const float *)(s + k * 16 * SB * 4);
+        fb_i8 wf = fetch(b, 16 * wn * TN);
 #pragma unroll
         for (int k = 0; k < TM; k++) xf[k] = fetch(b, BN + 16 * (wm * TM + k));
+#pragma unroll
+        for (int k = 0; k < TM; k++) sx[k] = *(const float *)(s + k * 16 * SB * 4);
         // products of tile i, and beside them the scaling of tile i - 1's
-        fb_i8 wf = fetch(b, 16 * wn * TN);
         kv_f4 d[2][TM];
         float f[TM];
 #pragma unroll

@@ -15,6 +15,7 @@ namespace nq {
 namespace {
 
 constexpr int MOST_EXPERTS = 1024;
+constexpr int64_t FAR_BYTES = 32 << 20;  // eight L2s of 4 MB
 
 __device__ __forceinline__ int32_t moe_id(const MoeSortLaunch &a, int64_t i) {
     if (a.wide) {
@@ -159,7 +160,8 @@ int launch_moe_sort(const MoeSortLaunch &L, hipStream_t s) {
 
 // Rows of bytes to the places of their token's pairs: a row is read once, whatever the number of its places.  Places
 // behind the last get zeros.
-template <typename V>
+// FAR: more bytes than the L2s hold, which go past them (268 MB 52 us, 64 us through them).
+template <typename V, bool FAR>
 __global__ __launch_bounds__(256) void k_moe_gather(MoeRowsLaunch a) {
     const int64_t n = a.cols / (int64_t)sizeof(V);
     V *const out = (V *)a.out;
@@ -169,7 +171,11 @@ __global__ __launch_bounds__(256) void k_moe_gather(MoeRowsLaunch a) {
             const V v = x[c];
             for (int k = 0; k < a.top; k++) {
                 const int32_t p = a.places[t * a.top + k];
-                if (p >= 0 && p < a.pairs) out[(int64_t)p * n + c] = v;
+                if (p < 0 || p >= a.pairs) continue;
+                if constexpr (FAR)
+                    __builtin_nontemporal_store(v, out + (int64_t)p * n + c);
+                else
+                    out[(int64_t)p * n + c] = v;
             }
         }
     }
@@ -185,18 +191,29 @@ __device__ __forceinline__ void moe_read(const void *x, int64_t i, float (&f)[N]
         fb_read8<DT, true>(x, i, f);
 }
 
-template <int DT, int N>
+// FAR: more bytes than the L2s hold, which go past them.
+template <int DT, int N, bool FAR = false>
 __device__ __forceinline__ void moe_write(void *y, int64_t i, const float (&f)[N]) {
     if constexpr (N == 1) {
         fb_write1(y, i, f[0], DT);
     } else {
-        const float a[4] = {f[0], f[1], f[2], f[3]}, b[4] = {f[4], f[5], f[6], f[7]};
-        kv_write4<DT>(y, i, a);
-        kv_write4<DT>(y, i + 4, b);
+        kv_u4 w[DT == 0 ? 2 : 1];
+        const float lo[4] = {f[0], f[1], f[2], f[3]}, hi[4] = {f[4], f[5], f[6], f[7]};
+        kv_write4<DT>(w, 0, lo);
+        kv_write4<DT>(w, 4, hi);
+        kv_u4 *const to = (kv_u4 *)((uint8_t *)y + i * (DT == 0 ? 4 : 2));
+#pragma unroll
+        for (int k = 0; k < (DT == 0 ? 2 : 1); k++) {
+            if constexpr (FAR)
+                __builtin_nontemporal_store(w[k], to + k);
+            else
+                to[k] = w[k];
+        }
     }
 }
 
-// out[t] = sum over choices of weight * row, in their order, in binary32.  N columns a thread and turn.
+// out[t] = sum over choices of weight * row, in their order, in binary32.  N columns a thread and turn (four
+// or eight rows on their way in each thread: no faster, and slower).
 template <int DT, int N>
 __global__ __launch_bounds__(256) void k_moe_combine(MoeRowsLaunch a) {
     for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
@@ -220,7 +237,7 @@ __global__ __launch_bounds__(256) void k_moe_combine(MoeRowsLaunch a) {
 
 // grad_rows[p] = weight * grad[token], grad_weights = <grad[token], rows[p]>; 0 behind the last place and where a pair
 // is left out.
-template <int DT, int N>
+template <int DT, int N, bool FAR>
 __global__ __launch_bounds__(256) void k_moe_combine_grad(MoeRowsLaunch a) {
     __shared__ float part[4];
     const int tid = threadIdx.x;
@@ -241,7 +258,7 @@ __global__ __launch_bounds__(256) void k_moe_combine_grad(MoeRowsLaunch a) {
                     }
 #pragma unroll
                     for (int i = 0; i < N; i++) g[i] *= w;
-                    moe_write<DT, N>(a.out, (int64_t)p * a.cols + c, g);
+                    moe_write<DT, N, FAR>(a.out, (int64_t)p * a.cols + c, g);
                 }
             }
             if (!a.out_weights) continue;
@@ -268,12 +285,14 @@ int launch_moe_gather(const MoeRowsLaunch &L, hipStream_t s) {
     if (L.tokens == 0 || L.cols == 0) return 0;
     const uintptr_t all = (uintptr_t)L.x | (uintptr_t)L.out | (uintptr_t)L.x_stride | (uintptr_t)L.cols;
     const dim3 grid = token_grid(L);
-    if (all % 16 == 0)
-        hipLaunchKernelGGL((k_moe_gather<kv_u4>), grid, dim3(256), 0, s, L);
+    if (all % 16 == 0 && L.pairs * L.cols > FAR_BYTES)
+        hipLaunchKernelGGL((k_moe_gather<kv_u4, true>), grid, dim3(256), 0, s, L);
+    else if (all % 16 == 0)
+        hipLaunchKernelGGL((k_moe_gather<kv_u4, false>), grid, dim3(256), 0, s, L);
     else if (all % 4 == 0)
-        hipLaunchKernelGGL((k_moe_gather<uint32_t>), grid, dim3(256), 0, s, L);
+        hipLaunchKernelGGL((k_moe_gather<uint32_t, false>), grid, dim3(256), 0, s, L);
     else
-        hipLaunchKernelGGL((k_moe_gather<uint8_t>), grid, dim3(256), 0, s, L);
+        hipLaunchKernelGGL((k_moe_gather<uint8_t, false>), grid, dim3(256), 0, s, L);
     return hipGetLastError() == hipSuccess ? 0 : 9;  // NQ_ERR_HIP
 }
 
@@ -288,10 +307,12 @@ static int combine_in(const MoeRowsLaunch &L, hipStream_t s) {
 
 template <int DT>
 static int grad_in(const MoeRowsLaunch &L, hipStream_t s) {
-    if (L.vec)
-        hipLaunchKernelGGL((k_moe_combine_grad<DT, 8>), token_grid(L), dim3(256), 0, s, L);
+    if (L.vec && L.pairs * L.cols * (DT == 0 ? 4 : 2) > FAR_BYTES)
+        hipLaunchKernelGGL((k_moe_combine_grad<DT, 8, true>), token_grid(L), dim3(256), 0, s, L);
+    else if (L.vec)
+        hipLaunchKernelGGL((k_moe_combine_grad<DT, 8, false>), token_grid(L), dim3(256), 0, s, L);
     else
-        hipLaunchKernelGGL((k_moe_combine_grad<DT, 1>), token_grid(L), dim3(256), 0, s, L);
+        hipLaunchKernelGGL((k_moe_combine_grad<DT, 1, false>), token_grid(L), dim3(256), 0, s, L);
     return hipGetLastError() == hipSuccess ? 0 : 9;  // NQ_ERR_HIP
 }
 
