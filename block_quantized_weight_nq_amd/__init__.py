@@ -1045,7 +1045,7 @@ def _block_product(weight, x, x_scales, plan, sorted_rows, gated, out_dtype):
     args = _BLOCK_ARGS.pack(pointer, stride, xs, weight.codes.data_ptr(), weight.scales.data_ptr(), out.data_ptr(), rows, n, k,
                             code, out_code, gated, sorted_rows)
     # the workspace is a function of these alone: asked for once for each
-    sizes = (rows, out_rows, code, out_code, gated, stride & 15, pointer & 15, sorted_rows)
+    sizes = (rows, out_rows, code, out_code, gated, stride, pointer & 15, sorted_rows)
     need = weight._workspaces.get(sizes)
     st = NQ_OK
     if need is None:

@@ -24,11 +24,6 @@ namespace {
 
 constexpr int MAX_WAVES = 8;
 
-// Blocks of a wave on their way.
-template <int NT>
-constexpr int few_depth() {
-    return NT > 2 ? 2 : 3;
-}
 
 // Where 16 bytes of a block of row r lie in LDS: blocks of `rows` rows of 128 bytes, whose pieces are exchanged by the
 // row's number, so that sixteen rows' pieces spread over all banks.
@@ -83,7 +78,7 @@ __global__ __launch_bounds__(64 * MAX_WAVES) void k_fp8_few(Fp8GemmLaunch a) {
         x = (const uint8_t *)a.x + r * a.x_stride + 16 * g;
         xs = a.x_scales + r * KB;
     }
-    constexpr int DEPTH = few_depth<NT>();
+    constexpr int DEPTH = fb_few_depth(NT);
     kv_f4 acc[NT];
 #pragma unroll
     for (int i = 0; i < NT; i++) acc[i] = kv_f4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -224,10 +219,8 @@ static int few(Fp8GemmLaunch L, hipStream_t s) {
     uint32_t room = 0;
     L.chunk = L.K / FB;
     if (XT != FB_CODES) {
-        // blocks of codes at a time: a turn of all waves, and all of them where few rows leave room in 16 KB
-        const int32_t rows = L.out_rows < 16 ? (int32_t)L.out_rows : 16, turn = few_depth<NT>() * L.waves;
-        const int32_t fit = 16384 / FB / rows;
-        L.chunk = fit > turn ? fit / turn * turn : turn;
+        const int32_t rows = L.out_rows < 16 ? (int32_t)L.out_rows : 16;
+        L.chunk = fb_few_chunk(L.out_rows, L.waves, NT);
         room = (uint32_t)(L.chunk * rows * (FB + 4));
     }
     const uint32_t sums = (uint32_t)L.waves * NT * 1024;

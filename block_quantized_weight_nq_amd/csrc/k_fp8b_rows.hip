@@ -28,17 +28,6 @@ __device__ __forceinline__ void fb_meet() {
     __builtin_amdgcn_s_barrier();
 }
 
-// Workgroup b's tile.  Workgroups go to the eight XCDs in turn; `span` consecutive tiles stay on one, and run along GM
-// row tiles first, so that an XCD's L2 has few weight rows and rows of x at a time.
-constexpr uint32_t XCDS = 8, MOST_SPAN = 32, GM = 8;
-__device__ __forceinline__ void place_tile(uint32_t b, uint32_t span, uint32_t tiles_m, uint32_t tiles_n, uint32_t *m, uint32_t *n) {
-    const uint32_t turn = b / XCDS, q = turn / span, t = (q * XCDS + b % XCDS) * span + (turn - q * span);
-    const uint32_t band = t / (GM * tiles_n), in = t - band * GM * tiles_n, first = band * GM;
-    const uint32_t high = first >= tiles_m ? 0 : tiles_m - first < GM ? tiles_m - first : GM;
-    *n = high > 0 ? in / high : 0;
-    *m = high > 0 ? first + in - *n * high : tiles_m;
-}
-
 }  // namespace
 
 // OT: type of the outputs; binary32 ones are products of binary16 matrix instructions.  AT: of a byte's place in x, 32
@@ -55,7 +44,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave % WN, wm = wave / WN;
     const int32_t KB = a.K / FB, NO = GATED ? a.N / 2 : a.N;
     uint32_t tile_m, tile_n;
-    place_tile(blockIdx.x, (uint32_t)a.span, (uint32_t)a.tiles_m, (uint32_t)(a.N + BN - 1) / BN, &tile_m, &tile_n);
+    fb_place_tile(blockIdx.x, (uint32_t)a.span, (uint32_t)a.tiles_m, (uint32_t)(a.N + BN - 1) / BN, &tile_m, &tile_n);
     if (tile_m >= (uint32_t)a.tiles_m) return;
     Fp8Tile t;
     if (a.experts > 0) {
@@ -348,9 +337,9 @@ __global__ __launch_bounds__(256) void k_fp8_join(Fp8GemmLaunch a) {
 template <int WN, int WM, int TN, int TM, int OT, bool GATED, typename AT = uint32_t>
 static int rows(Fp8GemmLaunch L, hipStream_t s) {
     constexpr int BN = 16 * WN * TN;
-    const int64_t tiles = fb_ceil(L.N, BN) * L.tiles_m, part = tiles / (4 * XCDS);
-    L.span = part < 1 ? 1 : part > MOST_SPAN ? (int32_t)MOST_SPAN : (int32_t)part;
-    const int64_t round = (int64_t)XCDS * L.span;  // whole turns of the XCDs: place_tile's tiles are all there
+    const int64_t tiles = fb_ceil(L.N, BN) * L.tiles_m;
+    L.span = (int32_t)fb_span(tiles);
+    const int64_t round = (int64_t)FB_XCDS * L.span;
     const dim3 grid((uint32_t)(fb_ceil(tiles, round) * round), (uint32_t)L.splits);
     hipLaunchKernelGGL((k_fp8_rows<WN, WM, TN, TM, OT, GATED, AT>), grid, dim3(64 * WN * WM), 0, s, L);
     if (hipGetLastError() != hipSuccess) return 9;  // NQ_ERR_HIP

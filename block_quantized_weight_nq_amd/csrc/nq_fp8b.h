@@ -96,14 +96,39 @@ inline Fp8Tile fb_find_tile_host(At at, int32_t experts, int64_t rows, int32_t b
 // one block of 128 columns in us, where a compute unit has one workgroup and where it has all (measured at K = 4096,
 // 256 to 28672 weight rows; times 1.6 for binary32 outputs).  The last is the second for x beyond 32 bits.
 struct Fp8Config {
-    int32_t rows, cols, held;
+    int32_t rows, cols, held, threads;
     float alone, full;
 };
-constexpr Fp8Config fb_configs[4] = {{64, 64, 4, 0.42f, 1.0f}, {128, 128, 2, 0.75f, 1.3f}, {256, 256, 1, 1.84f, 1.84f}, {128, 128, 2, 0.75f, 1.3f}};
+constexpr Fp8Config fb_configs[4] = {{64, 64, 4, 256, 0.42f, 1.0f}, {128, 128, 2, 256, 0.75f, 1.3f},
+                                     {256, 256, 1, 512, 1.84f, 1.84f}, {128, 128, 2, 256, 0.75f, 1.3f}};
 constexpr int FB_FAR = 3;
 
 constexpr int64_t FB_FEW_ROWS = 16;       // most rows of a weight, on average, that the few-rows kernel takes
 constexpr int64_t FB_RAW_VALUES = 16384;  // most values of them that its workgroups make codes of, each for itself
+
+// Workgroup b's tile in the many-rows kernel.  Workgroups go to the eight XCDs in turn; `span` consecutive tiles stay on
+// one, and run along FB_GM row tiles first, so that an XCD's L2 has few weight rows and rows of x at a time.  A grid of
+// whole turns (FB_XCDS * span) has every tile once; *m is tiles_m where there is none.
+constexpr uint32_t FB_XCDS = 8, FB_MOST_SPAN = 32, FB_GM = 8;
+inline uint32_t fb_span(int64_t tiles) {
+    const int64_t part = tiles / (4 * FB_XCDS);
+    return part < 1 ? 1 : part > FB_MOST_SPAN ? FB_MOST_SPAN : (uint32_t)part;
+}
+__host__ __device__ inline void fb_place_tile(uint32_t b, uint32_t span, uint32_t tiles_m, uint32_t tiles_n, uint32_t *m, uint32_t *n) {
+    const uint32_t turn = b / FB_XCDS, q = turn / span, t = (q * FB_XCDS + b % FB_XCDS) * span + (turn - q * span);
+    const uint32_t band = t / (FB_GM * tiles_n), in = t - band * FB_GM * tiles_n, first = band * FB_GM;
+    const uint32_t high = first >= tiles_m ? 0 : tiles_m - first < FB_GM ? tiles_m - first : FB_GM;
+    *n = high > 0 ? in / high : 0;
+    *m = high > 0 && *n < tiles_n ? first + in - *n * high : tiles_m;
+}
+
+// Blocks of a wave of the few-rows kernel that are on their way, and blocks whose codes its workgroups make at a time: a
+// turn of all waves, and all of them where few rows leave room in 16 KB.
+__host__ __device__ constexpr int32_t fb_few_depth(int32_t weight_tiles) { return weight_tiles > 2 ? 2 : 3; }
+inline int32_t fb_few_chunk(int64_t rows, int32_t waves, int32_t weight_tiles) {
+    const int32_t most = rows < 16 ? (int32_t)rows : 16, turn = fb_few_depth(weight_tiles) * waves, fit = 16384 / FB / most;
+    return fit > turn ? fit / turn * turn : turn;
+}
 
 // Output columns of a workgroup of the few-rows kernel.
 inline int64_t fb_few_cols(int32_t weight_tiles, bool gated) { return gated ? 8 * weight_tiles : 16 * weight_tiles; }

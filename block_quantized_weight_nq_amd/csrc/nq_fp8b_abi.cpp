@@ -69,9 +69,14 @@ int check_gemm(const nq_fp8_block_args *x, const nq_moe_plan *plan, nq::Fp8Plan 
     const bool raw = (uintptr_t)x->x % 16 == 0 && x->x_row_stride * esz % 16 == 0;
     *p = nq::fb_plan(x->rows, out_rows, experts, x->N, x->K, x->gated != 0, codes, raw, x->out_dtype == NQ_F32,
                      x->rows > 0 && (x->rows - 1) * x->x_row_stride + x->K > 1ll << 32, nq::device_compute_units());
-    const int64_t groups = p->few ? nq::fb_ceil(x->gated ? x->N / 2 : x->N, nq::fb_few_cols(p->weight_tiles, x->gated != 0)) * p->waves * 64
-                                  : (nq::fb_ceil(x->N, nq::fb_configs[p->config].cols) + 256) * 512;
-    if (p->few ? groups > THREADS || p->tiles_m > 65535 : p->tiles_m > 0 && groups > THREADS / p->tiles_m) return NQ_ERR_OVERFLOW;
+    if (p->few) {
+        const int64_t groups = nq::fb_ceil(x->gated ? x->N / 2 : x->N, nq::fb_few_cols(p->weight_tiles, x->gated != 0));
+        if (groups > THREADS / (64 * p->waves) || p->tiles_m > 65535) return NQ_ERR_OVERFLOW;
+    } else {
+        const nq::Fp8Config &c = nq::fb_configs[p->config];
+        const int64_t most = THREADS / c.threads - nq::FB_XCDS * nq::FB_MOST_SPAN;  // (the grid is whole turns of the XCDs)
+        if (nq::fb_ceil(x->N, c.cols) > most / (p->tiles_m > 0 ? p->tiles_m : 1)) return NQ_ERR_OVERFLOW;
+    }
     return NQ_OK;
 }
 

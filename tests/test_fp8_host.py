@@ -195,6 +195,10 @@ def emu():
     L = ctypes.CDLL(EMU)
     L.nq_fp8_emu_tiles.restype = ctypes.c_int64
     L.nq_fp8_emu_tiles.argtypes = [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p]
+    L.nq_fp8_emu_plan.argtypes = [ctypes.c_int64] * 5 + [ctypes.c_int] * 5 + [ctypes.c_int64, ctypes.c_void_p]
+    L.nq_fp8_emu_plan.restype = None
+    L.nq_fp8_emu_grid.restype = ctypes.c_int64
+    L.nq_fp8_emu_grid.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p]
     return L
 
 
@@ -228,3 +232,54 @@ def test_tiles_of_any_offsets_stay_inside(emu):
         experts, rows = int(rng.choice([1, 3, 64, 70])), int(rng.choice([1, 17, 300]))
         offsets = rng.choice([-2 ** 31, -5, 0, 1, rows - 1, rows, rows + 1, 2 ** 31 - 1], experts + 1)
         assert tiles(emu, offsets, rows, int(rng.choice([16, 64, 256])))[0] == 0
+
+
+# --- the plan ---------------------------------------------------------------------------------------------------
+
+PLAN_NAMES = ("few weight_tiles config waves splits per_split quantize tiles_m codes scales part chunk depth").split()
+
+
+def plan(emu, x_rows, rows, experts, N, K, gated=0, codes=0, raw=1, wide=0, far=0, cus=256):
+    out = np.zeros(len(PLAN_NAMES), np.int64)
+    emu.nq_fp8_emu_plan(x_rows, rows, experts, N, K, gated, codes, raw, wide, far, cus, out.ctypes.data)
+    return types.SimpleNamespace(**dict(zip(PLAN_NAMES, out.tolist())))
+
+
+def test_plans_cover_the_product(emu):
+    """Pieces of K, row tiles, LDS and workspace of plans over the range of sizes."""
+    rng = np.random.default_rng(1)
+    for trial in range(3000):
+        experts = int(rng.choice([0, 0, 1, 7, 64, 256, 1024]))
+        top = int(rng.choice([1, 2, 8])) if experts else 1
+        tokens = int(np.exp(rng.uniform(0, np.log(2e5))))
+        rows, K = tokens * top, 128 * int(np.exp(rng.uniform(0, np.log(256))))
+        N = int(np.exp(rng.uniform(0, np.log(4e4))))
+        gated, codes, raw, wide, far = (int(rng.integers(0, 2)) for _ in range(5))
+        N = max(256, N // 256 * 256) if gated else N
+        x_rows = rows if rng.integers(0, 2) else tokens
+        p = plan(emu, x_rows, rows, experts, N, K, gated, codes, raw, wide, far)
+        KB = K // 128
+        assert p.few == ((-(-rows // experts) if experts else rows) <= 16)
+        assert (p.splits - 1) * p.per_split < KB <= p.splits * p.per_split
+        assert p.splits == 1 or (not experts and not p.few)
+        bm = 16 if p.few else (64, 128, 256, 128)[p.config]
+        assert p.tiles_m >= -(-rows // bm) and (experts == 0 or p.tiles_m <= rows)
+        assert p.part == (-(-p.splits * rows * N * 4 // 256) * 256 if p.splits > 1 else 0)
+        assert (p.codes > 0) == (p.scales > 0) == bool(p.quantize) and p.codes >= p.quantize * x_rows * K
+        assert p.scales >= p.quantize * x_rows * KB * 4 and p.codes % 256 == p.scales % 256 == 0
+        assert not (codes and p.quantize) and (raw or codes or p.quantize)
+        if p.few:
+            assert 1 <= p.waves <= 8 and p.waves <= KB and p.weight_tiles in ((2, 4) if gated else (1, 2))
+            assert p.chunk % (p.depth * p.waves) == 0 and p.chunk > 0
+            assert max(p.chunk * min(rows, 16) * 132, p.waves * p.weight_tiles * 1024) <= 65536
+        else:
+            assert (p.config == 3) == bool(far if codes else x_rows * K > 2 ** 32) and not (wide and p.config == 2)
+
+
+def test_grids_have_each_tile_once(emu):
+    rng = np.random.default_rng(2)
+    for trial in range(400):
+        m, n = int(np.exp(rng.uniform(0, np.log(400)))), int(np.exp(rng.uniform(0, np.log(200))))
+        hits = np.zeros(m * n, np.int32)
+        assert emu.nq_fp8_emu_grid(m, n, hits.ctypes.data) == 0
+        assert (hits == 1).all(), (m, n)

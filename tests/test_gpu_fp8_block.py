@@ -248,6 +248,32 @@ def test_extreme_scales():
         fp8_ref.check(nq.gemm_fp8_block(handle(ww, ws), torch.as_tensor(x, device=DEV), out_dtype=out), *want, "extreme scales")
 
 
+def test_codes_beyond_32_bits_of_the_first():
+    """Rows of codes 16 MiB apart, the last of them past 2^32 bytes."""
+    rng = np.random.default_rng(9)
+    m, k, far = 300, 256, 1 << 24
+    ww, ws = weight(rng, 130, k)
+    w = handle(ww, ws)
+    base = torch.empty((m, far), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    codes, scales = nq.quantize_fp8_block(values(rng, m, k, "bf16", 0.5).to(DEV))
+    wide = base[:, 32:32 + k]
+    wide.copy_(codes)
+    for rows in (3, 100, 300):
+        for out in (torch.bfloat16, torch.float32):
+            announce(f"far codes {rows} {out}")
+            want = fp8_ref.product(codes[:rows].cpu().view(torch.uint8).numpy(), scales[:rows].cpu().numpy(), ww, ws,
+                                   out is torch.float32 or fp8_ref.few_rows(rows))
+            fp8_ref.check(nq.gemm_fp8_block(w, wide[:rows], scales[:rows], out_dtype=out), *want, f"far codes, {rows} rows")
+
+
+@pytest.mark.parametrize("m", [40, 140])
+def test_pieces_of_gated_products(m):
+    """K in pieces, few tiles, both halves of the weight in a piece's sums."""
+    rng = np.random.default_rng(m)
+    run(rng, m, 256, 8192, "bf16", "bf16", True, False)
+    run(rng, m, 768, 4096, "bf16", "f32", True, True)
+
+
 def test_no_rows():
     ww, ws = weight(np.random.default_rng(0), 256, 128)
     w = handle(ww, ws)

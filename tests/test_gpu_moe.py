@@ -108,6 +108,35 @@ def test_gather_combine_and_gradient(dtype, cols, kind):
     fp8_ref.check(g_rows, want_rows, 0 * want_rows, "gradient of rows, no weights")
 
 
+def test_rows_without_columns():
+    rng = np.random.default_rng(0)
+    plan = plan_of(choices(rng, 5, 2, 4, "half"), 4)
+    rows, w = torch.empty((10, 0), device=DEV), torch.ones((5, 2), device=DEV)
+    assert nq.moe_gather(torch.empty((5, 0), device=DEV), plan).shape == (10, 0)
+    assert nq.moe_combine(rows, plan, w).shape == (5, 0)
+    g, gw = nq.moe_combine_grad(torch.empty((5, 0), device=DEV), rows, plan, w)
+    assert g.shape == (10, 0) and not bool(gw.any())
+
+
+def test_more_bytes_than_the_l2s():
+    """Sizes whose rows go past the L2s, and pairs elsewhere."""
+    rng = np.random.default_rng(6)
+    tokens, top, cols = 3000, 4, 2048
+    ids = choices(rng, tokens, top, 20, "half")
+    plan = plan_of(ids, 20)
+    order, places, offsets = fp8_ref.sort(ids, 20)
+    x = torch.as_tensor(rng.normal(0, 1, (tokens, cols)), dtype=torch.bfloat16)
+    live = torch.as_tensor(order >= 0)[:, None]
+    token = torch.as_tensor(np.maximum(order, 0) // top)
+    assert torch.equal(nq.moe_gather(x.to(DEV), plan).cpu(), torch.where(live, x[token], torch.zeros((), dtype=x.dtype)))
+    w = torch.as_tensor(rng.random((tokens, top)), dtype=torch.float32)
+    rows = torch.zeros((tokens * top, cols), dtype=torch.bfloat16, device=DEV)
+    g, _ = nq.moe_combine_grad(x.to(DEV), rows, plan, w.to(DEV))
+    per = w.reshape(-1)[torch.as_tensor(np.maximum(order, 0)).long()][:, None]
+    want = torch.where(live, (x.float()[token] * per).to(torch.bfloat16), torch.zeros((), dtype=x.dtype))  # one product of two binary32 numbers, rounded twice
+    assert torch.equal(g.cpu(), want)
+
+
 def test_gradients_against_differences():
     """Combining is linear in rows and in weights: a step of any size gives its gradient, up to the sums' rounding."""
     rng = np.random.default_rng(0)
