@@ -22,24 +22,38 @@ typedef __attribute__((address_space(3))) void *fb_lds;
 // that read one piece of sixteen rows spread over all banks.
 __device__ __forceinline__ int swizzle(int row, int piece) { return piece ^ (row >> 1 & 7); }
 
-// All loads to LDS and registers are done, and all reads of LDS: what the waves of a workgroup meet on.
+// What the waves of a workgroup meet on: all loads (to LDS and to registers) but the last LEFT are done, and all reads of
+// LDS.  No access of memory moves over it.
+template <int LEFT>
 __device__ __forceinline__ void fb_meet() {
-    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((LEFT & 15) | (LEFT >> 4) << 14 | 0x0070);  // vmcnt(LEFT) lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
 }  // namespace
 
-// OT: type of the outputs; binary32 ones are products of binary16 matrix instructions.  AT: of a byte's place in x, 32
-// bits where they do.
-template <int WN, int WM, int TN, int TM, int OT, bool GATED, typename AT>
+// S: buffers in LDS, S - 1 of which are on their way.  OT: type of the outputs; binary32 ones are products of binary16
+// matrix instructions.  AT: of a byte's place in x, 32 bits where they do.
+template <int WN, int WM, int TN, int TM, int S, int OT, bool GATED, typename AT>
 __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
     constexpr bool WIDE = OT == 0;
     constexpr int BN = 16 * WN * TN, BM = 16 * WM * TM, WAVES = WN * WM;
     constexpr int H = TN / 2;  // a wave's tiles are two halves, each within one row of blocks
     constexpr int NW = BN / 8 / WAVES, NX = BM / 8 / WAVES;  // loads to LDS of a wave and block: 8 rows each
     constexpr int SB = 16, NS = BM / 4 / WAVES;  // blocks whose scales are loaded at a time, 4 rows a load
-    __shared__ __align__(1024) uint8_t even[(BN + BM) * FB], odd[(BN + BM) * FB], scales[2 * BM * SB * 4];
+    static_assert(S == 2 || S == 4, "buffers");
+    // (arrays of their own, so that reads of one do not wait for loads to the others)
+    __shared__ __align__(1024) uint8_t buffer0[(BN + BM) * FB], buffer1[(BN + BM) * FB];
+    __shared__ __align__(1024) uint8_t buffer2[S > 2 ? (BN + BM) * FB : 16], buffer3[S > 2 ? (BN + BM) * FB : 16];
+    __shared__ __align__(1024) uint8_t scales[2 * BM * SB * 4];
+    const auto buffer = [&](auto i) -> uint8_t * {
+        if constexpr (i() == 0) return buffer0;
+        if constexpr (i() == 1) return buffer1;
+        if constexpr (i() == 2) return buffer2;
+        return buffer3;
+    };
     const int tid = threadIdx.x, lane = tid & 63, j = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave % WN, wm = wave / WN;
     const int32_t KB = a.K / FB, NO = GATED ? a.N / 2 : a.N;
@@ -102,9 +116,9 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
     for (int i = 0; i < TN; i++)
 #pragma unroll
         for (int k = 0; k < TM; k++) acc[i][k] = kv_f4{0.0f, 0.0f, 0.0f, 0.0f};
-    struct {
+    struct WeightScales {
         float v[2];
-    } w0, w1;
+    } w_scale[S];
     // Load i of a block's, and the two scales of the weight.
     const auto load = [&](uint8_t *b, int32_t kb, int i) {
         if (i < NX) {
@@ -204,34 +218,64 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
         }
         __builtin_amdgcn_sched_barrier(0);
     };
+    constexpr int LOADS = NW + NX;
+    const auto load_all = [&](uint8_t *b, WeightScales &sw, int32_t k) {
+        load_weight_scales(sw, k);
+#pragma unroll
+        for (int l = 0; l < LOADS; l++) load(b, k, l);
+    };
+    // Step I of S: block kb + I from buffer I, while block kb + I + S - 1 goes to the buffer of the step before (past the
+    // last block the last one again, which is not used).
+    const auto step = [&](auto i, bool idle, int32_t k) {
+        constexpr int I = i(), NEXT = (I + S - 1) % S;
+        const int32_t ahead = k + S - 1 < kb1 ? k + S - 1 : kb1 - 1;
+        uint8_t *const to = buffer(std::integral_constant<int, NEXT>());
+        if (((k - kb0) & (SB - 1)) == 0 && k + SB < kb1) load_scales(k + SB);
+        if (idle)
+            load_all(to, w_scale[NEXT], ahead);
+        else
+            multiply(std::true_type(), buffer(i), w_scale[I], k, to, w_scale[NEXT], ahead);
+        fb_meet<(S - 2) * (LOADS + 2)>();
+    };
+    const auto last = [&](auto i, bool idle, int32_t k) {
+        constexpr int I = i();
+        if (k < kb1 && !idle) multiply(std::false_type(), buffer(i), w_scale[I], k, buffer(i), w_scale[I], k);
+    };
+    typedef std::integral_constant<int, 0> I0;
+    typedef std::integral_constant<int, 1> I1;
+    typedef std::integral_constant<int, 2> I2;
+    typedef std::integral_constant<int, 3> I3;
     load_scales(kb0);
-    load_weight_scales(w0, kb0);
-#pragma unroll
-    for (int l = 0; l < NW + NX; l++) load(even, kb0, l);
-    fb_meet();
-    int32_t kb = kb0;
-    if (16 * wm * TM >= t.count) {  // none of the wave's rows is there: it loads for the others
-        const auto load_all = [&](uint8_t *b, int32_t k) {
-#pragma unroll
-            for (int l = 0; l < NW + NX; l++) load(b, k, l);
-        };
-        for (; kb + 1 < kb1; kb += 2) {
-            if (((kb - kb0) & (SB - 1)) == 0 && kb + SB < kb1) load_scales(kb + SB);
-            load_all(odd, kb + 1);
-            fb_meet();
-            load_all(even, kb + 2 < kb1 ? kb + 2 : kb + 1);
-            fb_meet();
-        }
-    } else {
-        for (; kb + 1 < kb1; kb += 2) {
-            if (((kb - kb0) & (SB - 1)) == 0 && kb + SB < kb1) load_scales(kb + SB);
-            multiply(std::true_type(), even, w0, kb, odd, w1, kb + 1);
-            fb_meet();
-            multiply(std::true_type(), odd, w1, kb + 1, even, w0, kb + 2 < kb1 ? kb + 2 : kb + 1);  // (the last loads are not used)
-            fb_meet();
-        }
-        if (kb < kb1) multiply(std::false_type(), even, w0, kb, odd, w1, kb);
+    load_all(buffer0, w_scale[0], kb0);
+    if constexpr (S > 2) {
+        if (kb0 + 1 < kb1) load_all(buffer1, w_scale[1], kb0 + 1);
+        if (kb0 + 2 < kb1) load_all(buffer2, w_scale[2], kb0 + 2);
     }
+    if (S == 2 || kb0 + 2 < kb1)
+        fb_meet<(S - 2) * (LOADS + 2)>();
+    else
+        fb_meet<0>();
+    const auto blocks = [&](bool idle) {
+        int32_t kb = kb0;
+        for (; kb + S <= kb1; kb += S) {
+            step(I0(), idle, kb);
+            step(I1(), idle, kb + 1);
+            if constexpr (S > 2) {
+                step(I2(), idle, kb + 2);
+                step(I3(), idle, kb + 3);
+            }
+        }
+        if constexpr (S > 2) fb_meet<0>();
+        last(I0(), idle, kb);
+        if constexpr (S > 2) {
+            last(I1(), idle, kb + 1);
+            last(I2(), idle, kb + 2);
+        }
+    };
+    if (16 * wm * TM >= t.count)  // none of the wave's rows is there: it loads for the others
+        blocks(true);
+    else
+        blocks(false);
     // lane (j, g): outputs 4 g .. 4 g + 3 of each tile of weight rows, of row j
     if (a.splits > 1) {
 #pragma unroll
@@ -256,8 +300,8 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
         // Rows of V times 16 bytes through LDS, so that a store writes whole rows of the wave's tile (32 bytes of sixteen
         // rows each otherwise); a row's pieces are exchanged by its number.
         constexpr int TILES = GATED ? H : TN, V = 2 * TILES, ROW = 16 * V;
-        fb_meet();
-        uint8_t *const own = (wave < WAVES / 2 ? even : odd) + wave % (WAVES / 2) * 16 * TM * ROW;
+        fb_meet<0>();
+        uint8_t *const own = (wave < WAVES / 2 ? buffer0 : buffer1) + wave % (WAVES / 2) * 16 * TM * ROW;
 #pragma unroll
         for (int k = 0; k < TM; k++)
 #pragma unroll
@@ -334,14 +378,14 @@ __global__ __launch_bounds__(256) void k_fp8_join(Fp8GemmLaunch a) {
     }
 }
 
-template <int WN, int WM, int TN, int TM, int OT, bool GATED, typename AT = uint32_t>
+template <int WN, int WM, int TN, int TM, int S, int OT, bool GATED, typename AT = uint32_t>
 static int rows(Fp8GemmLaunch L, hipStream_t s) {
     constexpr int BN = 16 * WN * TN;
     const int64_t tiles = fb_ceil(L.N, BN) * L.tiles_m;
     L.span = (int32_t)fb_span(tiles);
     const int64_t round = (int64_t)FB_XCDS * L.span;
     const dim3 grid((uint32_t)(fb_ceil(tiles, round) * round), (uint32_t)L.splits);
-    hipLaunchKernelGGL((k_fp8_rows<WN, WM, TN, TM, OT, GATED, AT>), grid, dim3(64 * WN * WM), 0, s, L);
+    hipLaunchKernelGGL((k_fp8_rows<WN, WM, TN, TM, S, OT, GATED, AT>), grid, dim3(64 * WN * WM), 0, s, L);
     if (hipGetLastError() != hipSuccess) return 9;  // NQ_ERR_HIP
     if (L.splits > 1) {
         const int32_t no = GATED ? L.N / 2 : L.N;
@@ -360,12 +404,14 @@ static int rows(Fp8GemmLaunch L, hipStream_t s) {
 template <int OT, bool GATED>
 static int rows_of(const Fp8GemmLaunch &L, int config, hipStream_t s) {
     switch (config) {  // (fb_configs)
-    case 0: return rows<2, 2, 2, 2, OT, GATED>(L, s);
-    case 1: return rows<2, 2, 4, 4, OT, GATED>(L, s);
+    case 0: return rows<2, 2, 2, 2, 4, OT, GATED>(L, s);
+    case 1: return rows<2, 2, 4, 4, 2, OT, GATED>(L, s);
     case 2:
-        if constexpr (OT != 0) return rows<2, 4, 8, 4, OT, GATED>(L, s);
+        if constexpr (OT != 0) return rows<2, 4, 8, 4, 2, OT, GATED>(L, s);
         return 7;  // (the plan makes none)
-    default: return rows<2, 2, 4, 4, OT, GATED, uint64_t>(L, s);
+    case 3: return rows<2, 4, 4, 2, 4, OT, GATED>(L, s);
+    case 4: return rows<2, 2, 2, 2, 2, OT, GATED>(L, s);
+    default: return rows<2, 2, 4, 4, 2, OT, GATED, uint64_t>(L, s);
     }
 }
 

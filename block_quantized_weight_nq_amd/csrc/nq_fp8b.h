@@ -92,16 +92,20 @@ inline Fp8Tile fb_find_tile_host(At at, int32_t experts, int64_t rows, int32_t b
     return {-1, 0, 0};
 }
 
-// The tiles of the many-rows kernel: rows of x and of the weight, workgroups that a compute unit holds, and the time of
-// one block of 128 columns in us, where a compute unit has one workgroup and where it has all (measured at K = 4096,
-// 256 to 28672 weight rows; times 1.6 for binary32 outputs).  The last is the second for x beyond 32 bits.
+// The tiles of the many-rows kernel: rows of x and of the weight, workgroups that a compute unit holds, their threads, and
+// the time of one block of 128 columns in us, where compute units have few workgroups and where they have all (measured at
+// K = 4096, 1024 to 28672 weight rows, 48 to 8192 rows; times 1.6 for binary32 outputs).  The first and the fourth keep
+// three blocks on their way instead of one, which is what calls of few tiles wait for: 77 rows of [4096, 14336] 21.6 us
+// with the fourth, 26.0 with the second; 1024 rows of [28672, 4096] 173 and 151 (119 with the third).  The fifth has more
+// workgroups at a time, for many experts of few rows (1800 rows of 64 [2048, 1408] 43 us, 51 with the first).  The last is
+// the second for x beyond 32 bits.
 struct Fp8Config {
     int32_t rows, cols, held, threads;
     float alone, full;
 };
-constexpr Fp8Config fb_configs[4] = {{64, 64, 4, 256, 0.42f, 1.0f}, {128, 128, 2, 256, 0.75f, 1.3f},
-                                     {256, 256, 1, 512, 1.84f, 1.84f}, {128, 128, 2, 256, 0.75f, 1.3f}};
-constexpr int FB_FAR = 3;
+constexpr Fp8Config fb_configs[6] = {{64, 64, 2, 256, 0.36f, 0.45f}, {128, 128, 2, 256, 0.6f, 1.15f}, {256, 256, 1, 512, 1.4f, 1.84f},
+                                     {128, 128, 1, 512, 0.38f, 0.57f}, {64, 64, 4, 256, 0.42f, 1.0f}, {128, 128, 2, 256, 0.6f, 1.15f}};
+constexpr int FB_WIDEST = 2, FB_FAR = 5;
 
 constexpr int64_t FB_FEW_ROWS = 16;       // most rows of a weight, on average, that the few-rows kernel takes
 constexpr int64_t FB_RAW_VALUES = 16384;  // most values of them that its workgroups make codes of, each for itself
@@ -158,21 +162,21 @@ inline Fp8Plan fb_plan(int64_t x_rows, int64_t rows, int64_t experts, int64_t N,
         // [4096, 14336] 20.7 and 17.2
         p.quantize = !codes && (!raw || each * K > FB_RAW_VALUES);
     } else {
-        // the least of: rounds of workgroups, with the time of a block between that of a workgroup alone and of a full
-        // compute unit, or the weight's bytes, and where K is split a launch more and each piece's sums written and read
+        // the least of: rounds of workgroups, with the time of a block between that of few workgroups and of full compute
+        // units; half of the weight's bytes, which these times do not have; where K is split, a launch more and each
+        // piece's sums written and read
         float least = 0.0f;
         const bool beyond = codes ? far : x_rows * K > 1ll << 32;
-        for (int c = 0; c < 4; c++) {
-            if (beyond ? c != FB_FAR : c == FB_FAR || (wide && c == 2)) continue;
+        for (int c = 0; c <= FB_FAR; c++) {
+            if (beyond ? c != FB_FAR : c == FB_FAR || (wide && c == FB_WIDEST)) continue;
             const Fp8Config &f = fb_configs[c];
             const int64_t tiles = fb_ceil(N, f.cols) * (experts > 0 ? busy * fb_ceil(2 * each + f.rows, 2 * f.rows) : fb_ceil(rows, f.rows));
             for (int s = 1; s <= 16; s *= 2) {
                 if (s > 1 && (experts > 0 || KB / s < 4)) break;
                 const int64_t slots = cus * f.held, rounds = fb_ceil(tiles * s, slots);
                 const float load = (float)(tiles * s) / (float)(rounds * slots);
-                float t = (float)(rounds * fb_ceil(KB, s)) * (f.alone + (f.full - f.alone) * load) * (wide ? 1.6f : 1.0f) + 2.0f * (float)rounds;
-                const float bytes = (float)(busy * N) * (float)K / 4.8e6f;
-                if (t < bytes) t = bytes;
+                float t = (float)(rounds * fb_ceil(KB, s)) * (f.alone + (f.full - f.alone) * load) * (wide ? 1.6f : 1.0f) + 2.5f * (float)rounds;
+                t += (float)(busy * N) * (float)K / 9.6e6f;
                 if (s > 1) t += 3.5f + (float)(s * rows) * (float)N * 8.0f / 5e6f;
                 if (least == 0.0f || t < least) {
                     least = t;

@@ -262,7 +262,7 @@ def test_plans_cover_the_product(emu):
         assert p.few == ((-(-rows // experts) if experts else rows) <= 16)
         assert (p.splits - 1) * p.per_split < KB <= p.splits * p.per_split
         assert p.splits == 1 or (not experts and not p.few)
-        bm = 16 if p.few else (64, 128, 256, 128)[p.config]
+        bm = 16 if p.few else (64, 128, 256, 128, 64, 128)[p.config]
         assert p.tiles_m >= -(-rows // bm) and (experts == 0 or p.tiles_m <= rows)
         assert p.part == (-(-p.splits * rows * N * 4 // 256) * 256 if p.splits > 1 else 0)
         assert (p.codes > 0) == (p.scales > 0) == bool(p.quantize) and p.codes >= p.quantize * x_rows * K
@@ -273,7 +273,7 @@ def test_plans_cover_the_product(emu):
             assert p.chunk % (p.depth * p.waves) == 0 and p.chunk > 0
             assert max(p.chunk * min(rows, 16) * 132, p.waves * p.weight_tiles * 1024) <= 65536
         else:
-            assert (p.config == 3) == bool(far if codes else x_rows * K > 2 ** 32) and not (wide and p.config == 2)
+            assert (p.config == 5) == bool(far if codes else x_rows * K > 2 ** 32) and not (wide and p.config == 2)
 
 
 def test_grids_have_each_tile_once(emu):
