@@ -17,6 +17,7 @@ namespace {
 
 typedef __attribute__((address_space(1))) const void *fb_global;
 typedef __attribute__((address_space(3))) void *fb_lds;
+typedef __attribute__((address_space(4))) const float *fb_constant;  // scalar loads where the address is one for all lanes
 
 // LDS holds rows of 128 bytes as eight pieces of 16; piece c of row r lies at c ^ (r / 2 % 8), so that sixteen lanes
 // that read one piece of sixteen rows spread over all banks.
@@ -42,7 +43,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
     constexpr int BN = 16 * WN * TN, BM = 16 * WM * TM, WAVES = WN * WM;
     constexpr int H = TN / 2;  // a wave's tiles are two halves, each within one row of blocks
     constexpr int NW = BN / 8 / WAVES, NX = BM / 8 / WAVES;  // loads to LDS of a wave and block: 8 rows each
-    constexpr int SB = 16, NS = BM / 4 / WAVES;  // blocks whose scales are loaded at a time, 4 rows a load
+    constexpr int SB = FB_DEEP_BLOCKS / 2, NS = BM / 4 / WAVES;  // blocks whose scales are loaded at a time, 4 rows a load
     static_assert(S == 2 || S == 4, "buffers");
     // (arrays of their own, so that reads of one do not wait for loads to the others)
     __shared__ __align__(1024) uint8_t buffer0[(BN + BM) * FB], buffer1[(BN + BM) * FB];
@@ -132,7 +133,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
             __builtin_amdgcn_global_load_lds((fb_global)(w + w_at[i]), (fb_lds)(b + (i * WAVES + wave) * 1024), 16, 0, 0);
         }
     };
-    const auto load_weight_scales = [&](auto &sw, int32_t kb) { sw.v[0] = ws[0][kb], sw.v[1] = ws[1][kb]; };
+    const auto load_weight_scales = [&](auto &sw, int32_t kb) { sw.v[0] = ((fb_constant)ws[0])[kb], sw.v[1] = ((fb_constant)ws[1])[kb]; };
     // Scales of SB blocks from `kb` on, one of two places in turn: [row][block], a row's blocks exchanged by its number so
     // that sixteen rows' scales of a block lie in sixteen banks.
     const auto load_scales = [&](int32_t kb) {
@@ -147,10 +148,11 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
             __builtin_amdgcn_global_load_lds((fb_global)from, (fb_lds)(to + (i * WAVES + wave) * 256), 4, 0, 0);
         }
     };
-    const int p0 = swizzle(j, g) << 4, p1 = swizzle(j, g + 4) << 4;  // (16 rows further the swizzle is the same)
+    // (16 rows further the swizzle is the same; each address is an array and an offset, by which the compiler tells the
+    // buffers apart)
+    const int p0 = j * FB + (swizzle(j, g) << 4), p1 = j * FB + (swizzle(j, g + 4) << 4);
     const auto fetch = [&](const uint8_t *b, int row) {
-        const uint8_t *const at = b + (row + j) * FB;
-        const kv_u4 lo = *(const kv_u4 *)(at + p0), hi = *(const kv_u4 *)(at + p1);
+        const kv_u4 lo = *(const kv_u4 *)(b + (row * FB + p0)), hi = *(const kv_u4 *)(b + (row * FB + p1));
         fb_i8 v;
 #pragma unroll
         for (int i = 0; i < 4; i++) v[i] = (int)lo[i], v[4 + i] = (int)hi[i];
@@ -161,12 +163,16 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
         fb_i8 xf[TM];
         float sx[TM];
         const int at = (kb - kb0) & (SB - 1);
-        const uint8_t *const s = scales + ((kb - kb0) / SB & 1) * BM * SB * 4 + (16 * wm * TM + j) * SB * 4 + ((at ^ (j >> 2 & 3)) << 2);
         fb_i8 wf = fetch(b, 16 * wn * TN);
 #pragma unroll
         for (int k = 0; k < TM; k++) xf[k] = fetch(b, BN + 16 * (wm * TM + k));
+        const int s = ((kb - kb0) / SB & 1) * BM * SB * 4 + (16 * wm * TM + j) * SB * 4 + ((at ^ (j >> 2 & 3)) << 2);
 #pragma unroll
-        for (int k = 0; k < TM; k++) sx[k] = *(const float *)(s + k * 16 * SB * 4);
+        for (int k = 0; k < TM; k++) {
+            int o = s + k * 16 * SB * 4;
+            if (S > 2) asm("" : "+v"(o));  // each by itself: two reads in one instruction would wait for every load to LDS on its way
+            sx[k] = *(const float *)(scales + o);
+        }
         // products of tile i, and beside them the scaling of tile i - 1's
         kv_f4 d[2][TM];
         float f[TM];
@@ -230,12 +236,13 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
         constexpr int I = i(), NEXT = (I + S - 1) % S;
         const int32_t ahead = k + S - 1 < kb1 ? k + S - 1 : kb1 - 1;
         uint8_t *const to = buffer(std::integral_constant<int, NEXT>());
-        if (((k - kb0) & (SB - 1)) == 0 && k + SB < kb1) load_scales(k + SB);
+        // (with four buffers the first loads have all)
+        if (S == 2 && ((k - kb0) & (SB - 1)) == 0 && k + SB < kb1) load_scales(k + SB);
         if (idle)
             load_all(to, w_scale[NEXT], ahead);
         else
             multiply(std::true_type(), buffer(i), w_scale[I], k, to, w_scale[NEXT], ahead);
-        fb_meet<(S - 2) * (LOADS + 2)>();
+        fb_meet<(S - 2) * LOADS>();  // (any other load since makes this wait for more, never for less)
     };
     const auto last = [&](auto i, bool idle, int32_t k) {
         constexpr int I = i();
@@ -246,15 +253,13 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
     typedef std::integral_constant<int, 2> I2;
     typedef std::integral_constant<int, 3> I3;
     load_scales(kb0);
+    if (S > 2) load_scales(kb0 + SB);
     load_all(buffer0, w_scale[0], kb0);
     if constexpr (S > 2) {
-        if (kb0 + 1 < kb1) load_all(buffer1, w_scale[1], kb0 + 1);
-        if (kb0 + 2 < kb1) load_all(buffer2, w_scale[2], kb0 + 2);
+        load_all(buffer1, w_scale[1], kb0 + 1 < kb1 ? kb0 + 1 : kb1 - 1);
+        load_all(buffer2, w_scale[2], kb0 + 2 < kb1 ? kb0 + 2 : kb1 - 1);
     }
-    if (S == 2 || kb0 + 2 < kb1)
-        fb_meet<(S - 2) * (LOADS + 2)>();
-    else
-        fb_meet<0>();
+    fb_meet<(S - 2) * LOADS>();
     const auto blocks = [&](bool idle) {
         int32_t kb = kb0;
         for (; kb + S <= kb1; kb += S) {
@@ -381,6 +386,7 @@ __global__ __launch_bounds__(256) void k_fp8_join(Fp8GemmLaunch a) {
 template <int WN, int WM, int TN, int TM, int S, int OT, bool GATED, typename AT = uint32_t>
 static int rows(Fp8GemmLaunch L, hipStream_t s) {
     constexpr int BN = 16 * WN * TN;
+    if (S > 2 && L.per_split > FB_DEEP_BLOCKS) return 7;  // NQ_ERR_OVERFLOW (the plan makes none)
     const int64_t tiles = fb_ceil(L.N, BN) * L.tiles_m;
     L.span = (int32_t)fb_span(tiles);
     const int64_t round = (int64_t)FB_XCDS * L.span;

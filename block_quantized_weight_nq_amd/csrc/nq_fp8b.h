@@ -95,7 +95,7 @@ inline Fp8Tile fb_find_tile_host(At at, int32_t experts, int64_t rows, int32_t b
 // The tiles of the many-rows kernel: rows of x and of the weight, workgroups that a compute unit holds, their threads, and
 // the time of one block of 128 columns in us, where compute units have few workgroups and where they have all (measured at
 // K = 4096, 1024 to 28672 weight rows, 48 to 8192 rows; times 1.6 for binary32 outputs).  The first and the fourth keep
-// three blocks on their way instead of one, which is what calls of few tiles wait for: 77 rows of [4096, 14336] 21.6 us
+// three blocks on their way instead of one, which is what calls of few tiles wait for: 77 rows of [4096, 14336] 21.4 us
 // with the fourth, 26.0 with the second; 1024 rows of [28672, 4096] 173 and 151 (119 with the third).  The fifth has more
 // workgroups at a time, for many experts of few rows (1800 rows of 64 [2048, 1408] 43 us, 51 with the first).  The last is
 // the second for x beyond 32 bits.
@@ -103,9 +103,10 @@ struct Fp8Config {
     int32_t rows, cols, held, threads;
     float alone, full;
 };
-constexpr Fp8Config fb_configs[6] = {{64, 64, 2, 256, 0.36f, 0.45f}, {128, 128, 2, 256, 0.6f, 1.15f}, {256, 256, 1, 512, 1.4f, 1.84f},
-                                     {128, 128, 1, 512, 0.38f, 0.57f}, {64, 64, 4, 256, 0.42f, 1.0f}, {128, 128, 2, 256, 0.6f, 1.15f}};
+constexpr Fp8Config fb_configs[6] = {{64, 64, 2, 256, 0.30f, 0.42f}, {128, 128, 2, 256, 0.6f, 1.15f}, {256, 256, 1, 512, 1.4f, 1.84f},
+                                     {128, 128, 1, 512, 0.34f, 0.55f}, {64, 64, 4, 256, 0.42f, 1.0f}, {128, 128, 2, 256, 0.6f, 1.15f}};
 constexpr int FB_WIDEST = 2, FB_FAR = 5;
+constexpr int FB_DEEP_BLOCKS = 32;  // most blocks of a piece of K for the first and the fourth: their scales are loaded once
 
 constexpr int64_t FB_FEW_ROWS = 16;       // most rows of a weight, on average, that the few-rows kernel takes
 constexpr int64_t FB_RAW_VALUES = 16384;  // most values of them that its workgroups make codes of, each for itself
@@ -173,6 +174,7 @@ inline Fp8Plan fb_plan(int64_t x_rows, int64_t rows, int64_t experts, int64_t N,
             const int64_t tiles = fb_ceil(N, f.cols) * (experts > 0 ? busy * fb_ceil(2 * each + f.rows, 2 * f.rows) : fb_ceil(rows, f.rows));
             for (int s = 1; s <= 16; s *= 2) {
                 if (s > 1 && (experts > 0 || KB / s < 4)) break;
+                if ((c == 0 || c == 3) && fb_ceil(KB, s) > FB_DEEP_BLOCKS) continue;
                 const int64_t slots = cus * f.held, rounds = fb_ceil(tiles * s, slots);
                 const float load = (float)(tiles * s) / (float)(rounds * slots);
                 float t = (float)(rounds * fb_ceil(KB, s)) * (f.alone + (f.full - f.alone) * load) * (wide ? 1.6f : 1.0f) + 2.5f * (float)rounds;

@@ -273,6 +273,7 @@ def test_plans_cover_the_product(emu):
             assert p.chunk % (p.depth * p.waves) == 0 and p.chunk > 0
             assert max(p.chunk * min(rows, 16) * 132, p.waves * p.weight_tiles * 1024) <= 65536
         else:
+            assert p.config not in (0, 3) or p.per_split <= 32
             assert (p.config == 5) == bool(far if codes else x_rows * K > 2 ** 32) and not (wide and p.config == 2)
 
 
