@@ -319,6 +319,17 @@ def test_layer_in_a_graph(tokens):
             assert torch.equal(captured[k], eager[k]), f"replay {i}, step {k}"
 
 
+@pytest.mark.parametrize("tokens", [5, 64])
+def test_example(tokens):
+    """The example runs; its outputs are bfloat16: two roundings of 2^-8 of a value, and the sums' (fp8_ref.product)."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import experts_layer
+    worst, gradient = experts_layer.main(tokens, 2)
+    assert worst < 4 * 2.0 ** -8 and gradient < 1024 * 2.0 ** -23
+
+
 def test_refusals():
     rng = np.random.default_rng(0)
     plan = plan_of(choices(rng, 6, 2, 4), 4)
