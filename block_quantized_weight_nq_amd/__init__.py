@@ -998,6 +998,9 @@ class MoePlan:
         self.tokens, self.top, self.pairs, self.experts = tokens, top, tokens * top, experts
         self._ref = _PLAN_ARGS.pack(order_at, places_at, offsets_at, tokens, top, experts)
 
+    def __reduce__(self):  # (a copy has addresses of its own)
+        return MoePlan, (self.order, self.places, self.offsets)
+
     @property
     def device(self):
         return self.order.device

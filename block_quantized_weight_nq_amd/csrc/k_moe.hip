@@ -44,12 +44,14 @@ __global__ __launch_bounds__(1024) void k_moe_count(MoeSortLaunch a) {
     const int tid = threadIdx.x;
     for (int e = tid; e < a.experts; e += 1024) count[e] = 0;
     __syncthreads();
-    const int64_t i0 = (int64_t)blockIdx.x * MOE_CHUNK;
+    const int64_t end = ((int64_t)blockIdx.x + 1) * a.chunk;
+    for (int64_t i0 = end - a.chunk; i0 < end; i0 += MOE_CHUNK) {
 #pragma unroll
-    for (int k = 0; k < MOE_CHUNK / 1024; k++) {
-        const int64_t i = i0 + k * 1024 + tid;
-        const int32_t e = i < a.pairs ? moe_id(a, i) : -1;
-        if (e >= 0) atomicAdd(&count[e], 1);
+        for (int k = 0; k < MOE_CHUNK / 1024; k++) {
+            const int64_t i = i0 + k * 1024 + tid;
+            const int32_t e = i < a.pairs ? moe_id(a, i) : -1;
+            if (e >= 0) atomicAdd(&count[e], 1);
+        }
     }
     __syncthreads();
     for (int e = tid; e < a.experts; e += 1024) a.counts[(int64_t)blockIdx.x * a.experts + e] = count[e];
@@ -63,8 +65,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_moe_place(MoeSortLaunch a) {
     constexpr int TB = 64 * WAVES;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, E = a.experts;
     for (int i = tid; i < WAVES * E; i += TB) base[i] = 0;
-    const int64_t chunk0 = ONE ? 0 : (int64_t)blockIdx.x * MOE_CHUNK;
-    const int64_t chunk = ONE ? a.pairs : (a.pairs - chunk0 < MOE_CHUNK ? a.pairs - chunk0 : MOE_CHUNK);
+    const int64_t chunk0 = ONE ? 0 : (int64_t)blockIdx.x * a.chunk;
+    const int64_t chunk = ONE ? a.pairs : (a.pairs - chunk0 < a.chunk ? a.pairs - chunk0 : a.chunk);
     const int64_t per = fb_ceil(fb_ceil(chunk, WAVES), 64) * 64;
     const int64_t i0 = chunk0 + wave * per, end = chunk0 + (wave * per + per < chunk ? wave * per + per : chunk);
     __syncthreads();

@@ -204,11 +204,17 @@ inline Fp8Plan fb_plan(int64_t x_rows, int64_t rows, int64_t experts, int64_t N,
 struct MoeSortLaunch {
     const void *ids;
     int32_t *order, *places, *offsets, *counts;  // counts: [chunks, experts], where there is more than one chunk
-    int64_t pairs;
+    int64_t pairs, chunk;                        // chunk: pairs of a workgroup
     int32_t experts, wide, chunks;               // wide: ids of 64 bits
 };
 
-constexpr int64_t MOE_CHUNK = 4096;  // pairs of a workgroup of the sort
+// Pairs of a workgroup of the sort: MOE_CHUNK, and a multiple of it where there would be more than MOE_CHUNKS workgroups,
+// each of which reads the counts of all.
+constexpr int64_t MOE_CHUNK = 4096, MOE_CHUNKS = 512;
+inline int64_t moe_chunk(int64_t pairs) {
+    const int64_t times = fb_ceil(pairs, MOE_CHUNK * MOE_CHUNKS);
+    return MOE_CHUNK * (times > 1 ? times : 1);
+}
 
 struct MoeRowsLaunch {
     const void *x;        // gather: [tokens], gradient: [tokens] gradients of the tokens, combine: sorted rows

@@ -9,7 +9,7 @@ namespace {
 
 constexpr int64_t MOST = 1ll << 30;        // rows, pairs, N, and scales of rows
 constexpr int64_t MOST_K = 1ll << 23;
-constexpr int64_t MOST_EXPERTS = 1024;
+constexpr int64_t MOST_EXPERTS = 1024, MOST_TOP = 1024;
 constexpr int64_t THREADS = (1ll << 32) - 1;  // of a grid along an axis
 
 int64_t element_size(int32_t dtype) { return dtype == NQ_F32 ? 4 : 2; }
@@ -36,7 +36,7 @@ int check_blocks(int32_t dtype, int64_t matrices, int64_t rows, int64_t cols, in
 int check_plan(const nq_moe_plan *p) {
     if (!p) return NQ_ERR_NULL_ARG;
     if (p->tokens < 0 || p->top < 1 || p->experts < 1) return NQ_ERR_BAD_DIM;
-    if (p->top > MOST || p->tokens > MOST / p->top || p->experts > MOST_EXPERTS) return NQ_ERR_OVERFLOW;
+    if (p->top > MOST_TOP || p->tokens > MOST / p->top || p->experts > MOST_EXPERTS) return NQ_ERR_OVERFLOW;
     if (!p->offsets || (p->tokens > 0 && (!p->order || !p->places))) return NQ_ERR_NULL_ARG;
     if (((uintptr_t)p->order | (uintptr_t)p->places | (uintptr_t)p->offsets) % 4) return NQ_ERR_MISALIGNED;
     return NQ_OK;
@@ -196,8 +196,8 @@ NQ_API int nq_moe_sort_workspace(int64_t tokens, int64_t top, int64_t experts, u
     if (!bytes) return NQ_ERR_NULL_ARG;
     *bytes = 0;
     if (tokens < 0 || top < 1 || experts < 1) return NQ_ERR_BAD_DIM;
-    if (top > MOST || tokens > MOST / top || experts > MOST_EXPERTS) return NQ_ERR_OVERFLOW;
-    const int64_t chunks = nq::fb_ceil(tokens * top, nq::MOE_CHUNK);
+    if (top > MOST_TOP || tokens > MOST / top || experts > MOST_EXPERTS) return NQ_ERR_OVERFLOW;
+    const int64_t chunks = nq::fb_ceil(tokens * top, nq::moe_chunk(tokens * top));
     if (chunks > 1) *bytes = (uint64_t)chunks * experts * 4;
     return NQ_OK;
 }
@@ -218,7 +218,8 @@ NQ_API int nq_moe_sort(const void *ids, int32_t wide, int64_t tokens, int64_t to
     L.counts = (int32_t *)workspace;
     L.pairs = tokens * top;
     L.experts = (int32_t)experts, L.wide = wide;
-    L.chunks = need > 0 ? (int32_t)nq::fb_ceil(L.pairs, nq::MOE_CHUNK) : 1;
+    L.chunk = nq::moe_chunk(L.pairs);
+    L.chunks = need > 0 ? (int32_t)nq::fb_ceil(L.pairs, L.chunk) : 1;
     return nq::launch_moe_sort(L, stream);
 }
 

@@ -517,8 +517,8 @@ int nq_dequantize_fp8_block(const void *codes, const float *scales, int64_t matr
  *   offsets[e]  the first place of expert e, offsets[experts] the number of
  *               places.
  * Pairs of one expert keep their order (a stable sort).  order and places
- * have tokens * top entries, offsets experts + 1.  1 <= experts <= 1024,
- * top >= 1.  The calls below take them as device memory and check them there:
+ * have tokens * top entries, offsets experts + 1.  1 <= experts <= 1024 and
+ * 1 <= top <= 1024 (NQ_ERR_BAD_DIM below, NQ_ERR_OVERFLOW above).  The calls below take them as device memory and check them there:
  * no value leads outside the buffers that the arguments describe.
  *
  * nq_moe_sort: ids [tokens, top], int32, or int64 where `wide` is 1

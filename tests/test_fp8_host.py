@@ -82,7 +82,7 @@ def test_product_refuses_pointers_and_workspace(kw, status):
 
 @pytest.mark.parametrize("plan, kw, status", [
     (dict(), dict(rows=5), 4), (dict(), dict(sorted=1), 4), (dict(tokens=-1), {}, 4), (dict(top=0), {}, 4), (dict(experts=0), {}, 4),
-    (dict(experts=1025), {}, 7), (dict(tokens=2 ** 29, top=4), {}, 7), (dict(offsets=0), {}, 1), (dict(order=0), {}, 1),
+    (dict(experts=1025), {}, 7), (dict(tokens=2 ** 29, top=4), {}, 7), (dict(top=1025), {}, 7), (dict(offsets=0), {}, 1), (dict(order=0), {}, 1),
     (dict(places=0), {}, 1), (dict(order=P + 2), {}, 11), (dict(offsets=P + 1), {}, 11)])
 def test_product_refuses_plans(plan, kw, status):
     assert product(plan=plan, **kw) == status
@@ -95,12 +95,20 @@ def test_empty_plan_launches_nothing():
 
 @pytest.mark.parametrize("kw, status", [
     (dict(tokens=-1), 4), (dict(top=0), 4), (dict(experts=0), 4), (dict(experts=1025), 7), (dict(tokens=2 ** 30, top=2), 7),
-    (dict(wide=2), 8), (dict(ids=0), 1), (dict(order=0), 1), (dict(places=0), 1), (dict(offsets=0), 1), (dict(ids=P + 4, wide=1), 11),
+    (dict(tokens=1, top=1025), 7), (dict(wide=2), 8), (dict(ids=0), 1), (dict(order=0), 1), (dict(places=0), 1), (dict(offsets=0), 1), (dict(ids=P + 4, wide=1), 11),
     (dict(ids=P + 2), 11), (dict(order=P + 2), 11), (dict(ws=P + 1), 11), (dict(tokens=5000), 12), (dict(tokens=5000, ws=P, ws_bytes=12), 12)])
 def test_sort_refuses(kw, status):
     a = dict(ids=P, wide=0, tokens=9, top=2, experts=8, order=P, places=P, offsets=P, ws=0, ws_bytes=0)
     a.update(kw)
     assert nq.library().nq_moe_sort(*a.values(), None) == status
+
+
+@pytest.mark.parametrize("tokens, top, chunks", [(4096, 1, 0), (4097, 1, 2), (2 ** 18, 8, 512), (2 ** 18 + 1, 8, 257), (2 ** 30, 1, 512), (2 ** 20 + 1, 1023, 512)])
+def test_sort_workspace_stays_small(tokens, top, chunks):
+    """At most 512 workgroups, each of which reads the counts of all."""
+    need = ctypes.c_uint64()
+    assert nq.library().nq_moe_sort_workspace(tokens, top, 96, ctypes.byref(need)) == 0
+    assert need.value == chunks * 96 * 4
 
 
 @pytest.mark.parametrize("plan, kw, status", [

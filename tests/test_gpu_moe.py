@@ -53,6 +53,33 @@ def test_sort_uneven(kind, tokens):
     same_plan(plan_of(ids, 60), ids, 60, kind)
 
 
+def test_sort_of_many_pairs():
+    """More than 512 times 4096 pairs: a workgroup takes 8192."""
+    ids = np.random.default_rng(8).integers(-1, 41, (700001, 3))
+    plan = plan_of(ids, 40, wide=True)
+    flat = ids.reshape(-1)
+    live = (flat >= 0) & (flat < 40)
+    order = np.argsort(np.where(live, flat, 40), kind="stable")[:live.sum()]
+    places = np.full(flat.size, -1)
+    places[order] = np.arange(order.size)
+    assert np.array_equal(plan.order.cpu().numpy(), np.concatenate([order, np.full(flat.size - order.size, -1)]))
+    assert np.array_equal(plan.places.cpu().numpy().reshape(-1), places)
+    assert np.array_equal(plan.offsets.cpu().numpy(), np.cumsum([0, *np.bincount(flat[live], minlength=40)]))
+
+
+def test_copies_of_a_plan():
+    """A copy's calls read its own tensors."""
+    import copy
+    ids = choices(np.random.default_rng(2), 30, 2, 5)
+    plan = plan_of(ids, 5)
+    other = copy.deepcopy(plan)
+    same_plan(other, ids, 5, "copy")
+    want = nq.moe_gather(torch.arange(240., device=DEV).view(30, 8), plan)
+    for t in (plan.order, plan.places, plan.offsets):
+        t.zero_()
+    assert torch.equal(nq.moe_gather(torch.arange(240., device=DEV).view(30, 8), other), want)
+
+
 def test_sort_wide_ids_beyond_32_bits():
     ids = np.array([[2 ** 32, 1], [-2 ** 40, 0], [2 ** 33 + 1, 1]])
     plan = nq.moe_sort(torch.as_tensor(ids, device=DEV), 2)
