@@ -12,6 +12,9 @@
 namespace nq {
 
 typedef int fb_i8 __attribute__((ext_vector_type(8)));
+// 16 bytes at any element: rows of odd widths begin anywhere.
+typedef uint32_t fb_any16 __attribute__((ext_vector_type(4), aligned(2)));
+typedef float fb_any32 __attribute__((ext_vector_type(4), aligned(4)));
 
 namespace {
 
@@ -73,8 +76,15 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
     constexpr int OC = GATED ? BN / 2 : BN;
     const int32_t n0 = (int32_t)tile_n * OC;
     if (t.expert < 0) {
-        for (int i = tid; i < t.count * OC; i += 64 * WAVES)
-            if (n0 + i % OC < NO) fb_write1(a.out, (t.first + i / OC) * NO + n0 + i % OC, 0.0f, OT);
+        constexpr int P = WIDE ? 4 : 8;  // outputs of 16 bytes
+        for (int i = tid; i < t.count * (OC / P); i += 64 * WAVES) {
+            const int32_t n = n0 + i % (OC / P) * P;
+            uint8_t *const to = (uint8_t *)a.out + ((t.first + i / (OC / P)) * NO + n) * (16 / P);
+            if (n + P <= NO)
+                *(fb_any16 *)to = fb_any16{0, 0, 0, 0};
+            else
+                for (int q = 0; n + q < NO; q++) fb_write1(to, q, 0.0f, OT);
+        }
         return;
     }
     // weight row of row r of the tile (of a wave's rows, the first half are gates and the second up, where GATED)
@@ -291,8 +301,8 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
 #pragma unroll
             for (int i = 0; i < TN; i++) {
                 const int32_t n = weight_row(16 * (wn * TN + i)) + 4 * g;
-                if (a.N % 4 == 0 && n + 3 < a.N)
-                    *(kv_f4 *)(part + n) = acc[i][k];
+                if (n + 3 < a.N)
+                    *(fb_any32 *)(part + n) = acc[i][k];
                 else
 #pragma unroll
                     for (int q = 0; q < 4; q++)
@@ -301,9 +311,10 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
         }
         return;
     }
-    if (OT != 0 && NO % 8 == 0 && n0 + OC <= NO) {
+    if constexpr (OT != 0) {
         // Rows of V times 16 bytes through LDS, so that a store writes whole rows of the wave's tile (32 bytes of sixteen
-        // rows each otherwise); a row's pieces are exchanged by its number.
+        // rows each otherwise); a row's pieces are exchanged by its number.  (With single stores where N is no multiple of
+        // 8, 10054 rows of 256 [4147, 128] took 253 us instead of 177.)
         constexpr int TILES = GATED ? H : TN, V = 2 * TILES, ROW = 16 * V;
         fb_meet<0>();
         uint8_t *const own = (wave < WAVES / 2 ? buffer0 : buffer1) + wave % (WAVES / 2) * 16 * TM * ROW;
@@ -322,27 +333,35 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
         for (int r0 = 0; r0 < 16 * TM; r0 += RT) {
             const int r = r0 + lane / V, m = 16 * wm * TM + r;
             const kv_u4 v = *(const kv_u4 *)(own + r * ROW + (((lane % V) ^ (r & (V - 1))) << 4));
-            if (m < t.count) *(kv_u4 *)((uint16_t *)a.out + (t.first + m) * NO + n) = v;
-        }
-        return;
-    }
-#pragma unroll
-    for (int k = 0; k < TM; k++) {
-        const int m = 16 * (wm * TM + k) + j;
-        if (m >= t.count) continue;
-#pragma unroll
-        for (int i = 0; i < (GATED ? H : TN); i++) {
-            const int32_t n = weight_row(16 * (wn * TN + i)) + 4 * g;
-            float f[4];
-#pragma unroll
-            for (int q = 0; q < 4; q++) f[q] = GATED ? fb_silu<OT>(acc[i][k][q]) * acc[GATED ? i + H : i][k][q] : acc[i][k][q];
-            const int64_t o = (t.first + m) * NO + n;
-            if (NO % 4 == 0 && n + 3 < NO) {
-                kv_write4<OT>(a.out, o, f);
+            uint16_t *const to = (uint16_t *)a.out + (t.first + m) * NO + n;
+            if (m >= t.count) continue;
+            if (n + 8 <= NO) {
+                *(fb_any16 *)to = v;
             } else {
 #pragma unroll
-                for (int q = 0; q < 4; q++)
-                    if (n + q < NO) fb_write1(a.out, o + q, f[q], OT);
+                for (int q = 0; q < 8; q++)
+                    if (n + q < NO) to[q] = (uint16_t)(v[q >> 1] >> (16 * (q & 1)));
+            }
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < TM; k++) {
+            const int m = 16 * (wm * TM + k) + j;
+            if (m >= t.count) continue;
+#pragma unroll
+            for (int i = 0; i < (GATED ? H : TN); i++) {
+                const int32_t n = weight_row(16 * (wn * TN + i)) + 4 * g;
+                kv_f4 f;
+#pragma unroll
+                for (int q = 0; q < 4; q++) f[q] = GATED ? fb_silu<OT>(acc[i][k][q]) * acc[GATED ? i + H : i][k][q] : acc[i][k][q];
+                float *const to = (float *)a.out + (t.first + m) * NO + n;
+                if (n + 3 < NO) {
+                    *(fb_any32 *)to = f;
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; q++)
+                        if (n + q < NO) to[q] = f[q];
+                }
             }
         }
     }

@@ -153,7 +153,7 @@ def test_types(m, dtype, out):
         run(rng, m, 144, 256, dtype, out, False, codes)
 
 
-@pytest.mark.parametrize("m, n, k", [(65, 1, 128), (65, 130, 2048), (77, 515, 1152), (128, 128, 4096), (129, 256, 384), (257, 130, 640), (300, 384, 128)])
+@pytest.mark.parametrize("m, n, k", [(65, 1, 128), (65, 130, 2048), (77, 515, 1152), (128, 128, 4096), (129, 256, 384), (257, 130, 640), (300, 384, 128), (300, 1027, 256)])
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 def test_many_rows(m, n, k, out):
     rng = np.random.default_rng(m + n)
@@ -167,7 +167,7 @@ def test_many_rows_gated(m, n, k, out):
     run(rng, m, n, k, "f16", out, True, m % 2 == 0)
 
 
-@pytest.mark.parametrize("m, n, gated, out", [(4200, 4100, False, "bf16"), (4111, 8192, True, "bf16"), (4111, 4096, False, "f32")])
+@pytest.mark.parametrize("m, n, gated, out", [(4200, 4100, False, "bf16"), (4200, 4099, False, "f16"), (4111, 8192, True, "bf16"), (4111, 4096, False, "f32")])
 def test_largest_tiles(m, n, gated, out):
     """Sizes that fill the device with the largest tiles; some rows and columns of them are compared."""
     rng = np.random.default_rng(m)

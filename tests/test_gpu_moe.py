@@ -246,6 +246,12 @@ def test_experts_forms(tokens, out, sorted_rows):
         experts_run(rng, tokens, 3, 4, 512, 128, "random", sorted_rows, True, "bf16", out, codes)
 
 
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+def test_experts_odd_widths(out):
+    """Rows that begin at any element, many of them behind the last place."""
+    experts_run(np.random.default_rng(3), 300, 4, 12, 1027, 128, "half", False, False, "bf16", out, False)
+
+
 def test_many_experts():
     experts_run(np.random.default_rng(1), 70, 8, 1024, 20, 128, "random", False, False, "bf16", "bf16", False)
 
