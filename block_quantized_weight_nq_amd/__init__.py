@@ -932,20 +932,24 @@ def dequantize_fp8_block(codes, scales, tile=1, out_dtype=None, stream=None):
     """The values of E4M3 codes and their scales (as quantize_fp8_block returns them) in out_dtype (default float32)."""
     if _I32 is None:
         _torch_names()
-    index = codes.get_device()
     if not codes.is_cuda or codes.dtype is not _F8 or not codes.is_contiguous():
         raise ValueError("codes must be a contiguous float8_e4m3fn CUDA tensor")
+    index = codes.get_device()
     if stream is not None:
         with _on(stream, index):
             return dequantize_fp8_block(codes, scales, tile, out_dtype)
     if _DEVICE() != index:
         with _at(index):
             return dequantize_fp8_block(codes, scales, tile, out_dtype)
-    matrices, rows, cols, scales_shape = _block_shapes(codes.shape, tile)
-    _scales_of("scales", scales, scales_shape, index)
-    out = codes.new_empty(codes.shape, dtype=out_dtype or _F32)
-    st = (_LIB or _lib()).nq_dequantize_fp8_block(codes.data_ptr(), scales.data_ptr(), matrices, rows, cols, tile,
-                                                  _kv_dtype(out.dtype), out.data_ptr(), _STREAM(index))
+    shape = codes.shape
+    matrices, rows, cols, scales_shape = _block_shapes(shape, tile)
+    if scales.dtype is not _F32 or scales.shape != scales_shape or scales.get_device() != index or not scales.is_contiguous():
+        _scales_of("scales", scales, scales_shape, index)
+    out_dtype = out_dtype or _F32
+    code = _kv_dtype(out_dtype)
+    out = codes.new_empty(shape, dtype=out_dtype)
+    st = (_LIB or _lib()).nq_dequantize_fp8_block(codes.data_ptr(), scales.data_ptr(), matrices, rows, cols, tile, code,
+                                                  out.data_ptr(), _STREAM(index))
     if st != NQ_OK:
         raise NqError(st, f"codes {list(codes.shape)} as {out.dtype}")
     return out
@@ -1157,10 +1161,12 @@ def moe_gather(x, plan, stream=None):
     if _DEVICE() != index:
         with _at(index):
             return moe_gather(x, plan)
-    _rows_of("x", x, plan.tokens, None, index)
-    size, cols = x.element_size(), x.shape[1]
+    shape, strides = x.shape, x.stride()
+    if len(shape) != 2 or shape[0] != plan.tokens or x.get_device() != index or strides[1] != 1:
+        _rows_of("x", x, plan.tokens, None, index)
+    size, cols = x.element_size(), shape[1]
     out = x.new_empty((plan.pairs, cols))
-    st = (_LIB or _lib()).nq_moe_gather(plan._ref, x.data_ptr(), cols * size, x.stride(0) * size, out.data_ptr(), _STREAM(index))
+    st = (_LIB or _lib()).nq_moe_gather(plan._ref, x.data_ptr(), cols * size, strides[0] * size, out.data_ptr(), _STREAM(index))
     if st != NQ_OK:
         raise NqError(st, f"x {list(x.shape)} {x.dtype}")
     return out
@@ -1208,17 +1214,25 @@ def moe_combine_grad(grad, rows, plan, weights=None, stream=None):
     if _DEVICE() != index:
         with _at(index):
             return moe_combine_grad(grad, rows, plan, weights)
-    _rows_of("rows", rows, plan.pairs, None, index)
-    cols = rows.shape[1]
-    _rows_of("grad", grad, plan.tokens, cols, index)
-    if grad.dtype is not rows.dtype:
+    pairs, shape, strides, grad_shape, grad_strides = plan.pairs, rows.shape, rows.stride(), grad.shape, grad.stride()
+    if len(shape) != 2 or shape[0] != pairs or rows.get_device() != index or strides[1] != 1:
+        _rows_of("rows", rows, pairs, None, index)
+    cols, dtype = shape[1], rows.dtype
+    if len(grad_shape) != 2 or grad_shape[0] != plan.tokens or grad_shape[1] != cols or grad.get_device() != index or \
+            grad_strides[1] != 1:
+        _rows_of("grad", grad, plan.tokens, cols, index)
+    if grad.dtype is not dtype:
         raise ValueError("grad must have the rows' type")
-    out = rows.new_empty((plan.pairs, cols))
-    pointer = None if weights is None else _weights_of(weights, plan)
-    out_weights = weights.new_empty(weights.shape) if weights is not None else None
-    st = (_LIB or _lib()).nq_moe_combine_grad(plan._ref, grad.data_ptr(), grad.stride(0), rows.data_ptr(), rows.stride(0),
-                                              _kv_dtype(rows.dtype), cols, pointer, out.data_ptr(),
-                                              out_weights.data_ptr() if weights is not None else None, _STREAM(index))
+    out = rows.new_empty((pairs, cols))
+    pointer = out_weights = out_pointer = None
+    if weights is not None:
+        pointer = _weights_of(weights, plan)
+        out_weights = weights.new_empty((plan.tokens, plan.top))
+        out_pointer = out_weights.data_ptr()
+    code = _KV_DTYPES.get(dtype)
+    st = (_LIB or _lib()).nq_moe_combine_grad(plan._ref, grad.data_ptr(), grad_strides[0], rows.data_ptr(), strides[0],
+                                              _dtype_code(dtype) if code is None else code, cols, pointer, out.data_ptr(),
+                                              out_pointer, _STREAM(index))
     if st != NQ_OK:
         raise NqError(st, f"rows {list(rows.shape)} {rows.dtype}")
     return out, out_weights
