@@ -165,16 +165,22 @@ int launch_moe_sort(const MoeSortLaunch &L, hipStream_t s) {
     return L.experts <= 512 ? place<16, true>(L, s) : place<8, true>(L, s);
 }
 
+// The kernels below have G threads a row: a workgroup, a wave or a quarter of one.  Narrow rows would leave most of a
+// workgroup idle, wide ones of a wave's keep less on their way (9834 tokens x 6, bfloat16, combine and gradients, threads a
+// row: 136 values 56 us with 256 and 24 with 16, 512 values 60 and 40 with 64, 1024 values 94 and 89; 8192 x 8, 2048 values
+// 178 and 201), and few tokens would leave compute units idle.
+
 // Rows of bytes to the places of their token's pairs: a row is read once, whatever the number of its places.  Places
 // behind the last get zeros.
 // FAR: more bytes than the L2s hold, which go past them (268 MB 52 us, 64 us through them).
-template <typename V, bool FAR>
+template <typename V, int G, bool FAR>
 __global__ __launch_bounds__(256) void k_moe_gather(MoeRowsLaunch a) {
-    const int64_t n = a.cols / (int64_t)sizeof(V);
+    const int64_t n = a.cols / (int64_t)sizeof(V), row0 = (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G, rows = (int64_t)gridDim.x * (256 / G);
+    const int lane = threadIdx.x % G;
     V *const out = (V *)a.out;
-    for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+    for (int64_t t = row0; t < a.tokens; t += rows) {
         const V *const x = (const V *)((const uint8_t *)a.x + t * a.x_stride);
-        for (int64_t c = threadIdx.x; c < n; c += 256) {
+        for (int64_t c = lane; c < n; c += G) {
             const V v = x[c];
             for (int k = 0; k < a.top; k++) {
                 const int32_t p = a.places[t * a.top + k];
@@ -186,8 +192,8 @@ __global__ __launch_bounds__(256) void k_moe_gather(MoeRowsLaunch a) {
             }
         }
     }
-    for (int64_t p = fb_clamp(a.offsets[a.experts], a.pairs) + blockIdx.x; p < a.pairs; p += gridDim.x)
-        for (int64_t c = threadIdx.x; c < n; c += 256) out[p * n + c] = V{};
+    for (int64_t p = fb_clamp(a.offsets[a.experts], a.pairs) + row0; p < a.pairs; p += rows)
+        for (int64_t c = lane; c < n; c += G) out[p * n + c] = V{};
 }
 
 template <int DT, int N>
@@ -221,10 +227,10 @@ __device__ __forceinline__ void moe_write(void *y, int64_t i, const float (&f)[N
 
 // out[t] = sum over choices of weight * row, in their order, in binary32.  N columns a thread and turn (four
 // or eight rows on their way in each thread: no faster, and slower).
-template <int DT, int N>
+template <int DT, int N, int G>
 __global__ __launch_bounds__(256) void k_moe_combine(MoeRowsLaunch a) {
-    for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-        for (int64_t c = (int64_t)threadIdx.x * N; c < a.cols; c += 256 * N) {
+    for (int64_t t = (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G; t < a.tokens; t += (int64_t)gridDim.x * (256 / G)) {
+        for (int64_t c = (int64_t)(threadIdx.x % G) * N; c < a.cols; c += G * N) {
             float sum[N];
 #pragma unroll
             for (int i = 0; i < N; i++) sum[i] = 0.0f;
@@ -244,18 +250,19 @@ __global__ __launch_bounds__(256) void k_moe_combine(MoeRowsLaunch a) {
 
 // grad_rows[p] = weight * grad[token], grad_weights = <grad[token], rows[p]>; 0 behind the last place and where a pair
 // is left out.
-template <int DT, int N, bool FAR>
+template <int DT, int N, int G, bool FAR>
 __global__ __launch_bounds__(256) void k_moe_combine_grad(MoeRowsLaunch a) {
     __shared__ float part[4];
-    const int tid = threadIdx.x;
-    for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+    const int lane = threadIdx.x % G;
+    const int64_t row0 = (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G, rows = (int64_t)gridDim.x * (256 / G);
+    for (int64_t t = row0; t < a.tokens; t += rows) {
         for (int k = 0; k < a.top; k++) {
             const int32_t p = a.places[t * a.top + k];
             const bool live = p >= 0 && p < a.pairs;
             float dot = 0.0f;
             if (live) {
                 const float w = a.weights ? a.weights[t * a.top + k] : 1.0f;
-                for (int64_t c = (int64_t)tid * N; c < a.cols; c += 256 * N) {
+                for (int64_t c = (int64_t)lane * N; c < a.cols; c += G * N) {
                     float g[N], f[N];
                     moe_read<DT, N>(a.x, t * a.x_stride + c, g);
                     if (a.out_weights) {
@@ -269,58 +276,86 @@ __global__ __launch_bounds__(256) void k_moe_combine_grad(MoeRowsLaunch a) {
                 }
             }
             if (!a.out_weights) continue;
-            for (int d = 1; d < 64; d <<= 1) dot += __shfl_xor(dot, d, 64);
-            if ((tid & 63) == 0) part[tid >> 6] = dot;
-            __syncthreads();
-            if (tid == 0) a.out_weights[t * a.top + k] = live ? part[0] + part[1] + part[2] + part[3] : 0.0f;
-            __syncthreads();
+            for (int d = 1; d < (G < 64 ? G : 64); d <<= 1) dot += __shfl_xor(dot, d, 64);
+            if constexpr (G > 64) {
+                if ((lane & 63) == 0) part[lane >> 6] = dot;
+                __syncthreads();
+                dot = part[0] + part[1] + part[2] + part[3];
+                __syncthreads();
+            }
+            if (lane == 0) a.out_weights[t * a.top + k] = live ? dot : 0.0f;
         }
     }
     float zero[N];
 #pragma unroll
     for (int i = 0; i < N; i++) zero[i] = 0.0f;
-    for (int64_t p = fb_clamp(a.offsets[a.experts], a.pairs) + blockIdx.x; p < a.pairs; p += gridDim.x)
-        for (int64_t c = (int64_t)tid * N; c < a.cols; c += 256 * N) moe_write<DT, N>(a.out, p * a.cols + c, zero);
+    for (int64_t p = fb_clamp(a.offsets[a.experts], a.pairs) + row0; p < a.pairs; p += rows)
+        for (int64_t c = (int64_t)lane * N; c < a.cols; c += G * N) moe_write<DT, N>(a.out, p * a.cols + c, zero);
 }
 
-static dim3 token_grid(const MoeRowsLaunch &L) {
-    const int64_t most = (int64_t)device_compute_units() * 16;
-    return dim3((uint32_t)(L.tokens < most ? (L.tokens > 0 ? L.tokens : 1) : most));
+// Threads of a row of `units` (what a thread takes at a time), and the grid.
+static int row_threads(int64_t tokens, int64_t units) {
+    const int64_t cus = device_compute_units();
+    if (units <= 32 && tokens >= 16 * cus) return 16;
+    return units <= 128 && tokens >= 4 * cus ? 64 : 256;
+}
+static dim3 row_grid(const MoeRowsLaunch &L, int threads) {
+    const int64_t need = fb_ceil(L.tokens, 256 / threads), most = (int64_t)device_compute_units() * 16;
+    return dim3((uint32_t)(need < most ? need : most));
+}
+
+template <typename V, bool FAR>
+static int gather(const MoeRowsLaunch &L, hipStream_t s) {
+    const int threads = row_threads(L.tokens, L.cols / (int64_t)sizeof(V));
+    const dim3 grid = row_grid(L, threads);
+    switch (threads) {
+    case 16: hipLaunchKernelGGL((k_moe_gather<V, 16, FAR>), grid, dim3(256), 0, s, L); break;
+    case 64: hipLaunchKernelGGL((k_moe_gather<V, 64, FAR>), grid, dim3(256), 0, s, L); break;
+    default: hipLaunchKernelGGL((k_moe_gather<V, 256, FAR>), grid, dim3(256), 0, s, L); break;
+    }
+    return hipGetLastError() == hipSuccess ? 0 : 9;  // NQ_ERR_HIP
 }
 
 int launch_moe_gather(const MoeRowsLaunch &L, hipStream_t s) {
     if (L.tokens == 0 || L.cols == 0) return 0;
     const uintptr_t all = (uintptr_t)L.x | (uintptr_t)L.out | (uintptr_t)L.x_stride | (uintptr_t)L.cols;
-    const dim3 grid = token_grid(L);
-    if (all % 16 == 0 && L.pairs * L.cols > FAR_BYTES)
-        hipLaunchKernelGGL((k_moe_gather<kv_u4, true>), grid, dim3(256), 0, s, L);
-    else if (all % 16 == 0)
-        hipLaunchKernelGGL((k_moe_gather<kv_u4, false>), grid, dim3(256), 0, s, L);
-    else if (all % 4 == 0)
-        hipLaunchKernelGGL((k_moe_gather<uint32_t, false>), grid, dim3(256), 0, s, L);
-    else
-        hipLaunchKernelGGL((k_moe_gather<uint8_t, false>), grid, dim3(256), 0, s, L);
+    if (all % 16 == 0) return L.pairs * L.cols > FAR_BYTES ? gather<kv_u4, true>(L, s) : gather<kv_u4, false>(L, s);
+    return all % 4 == 0 ? gather<uint32_t, false>(L, s) : gather<uint8_t, false>(L, s);
+}
+
+template <int DT, int N>
+static int combine_wide(const MoeRowsLaunch &L, hipStream_t s) {
+    const int threads = row_threads(L.tokens, L.cols / N);
+    const dim3 grid = row_grid(L, threads);
+    switch (threads) {
+    case 16: hipLaunchKernelGGL((k_moe_combine<DT, N, 16>), grid, dim3(256), 0, s, L); break;
+    case 64: hipLaunchKernelGGL((k_moe_combine<DT, N, 64>), grid, dim3(256), 0, s, L); break;
+    default: hipLaunchKernelGGL((k_moe_combine<DT, N, 256>), grid, dim3(256), 0, s, L); break;
+    }
+    return hipGetLastError() == hipSuccess ? 0 : 9;  // NQ_ERR_HIP
+}
+
+template <int DT, int N, bool FAR>
+static int grad_wide(const MoeRowsLaunch &L, hipStream_t s) {
+    const int threads = row_threads(L.tokens, L.cols / N);
+    const dim3 grid = row_grid(L, threads);
+    switch (threads) {
+    case 16: hipLaunchKernelGGL((k_moe_combine_grad<DT, N, 16, FAR>), grid, dim3(256), 0, s, L); break;
+    case 64: hipLaunchKernelGGL((k_moe_combine_grad<DT, N, 64, FAR>), grid, dim3(256), 0, s, L); break;
+    default: hipLaunchKernelGGL((k_moe_combine_grad<DT, N, 256, FAR>), grid, dim3(256), 0, s, L); break;
+    }
     return hipGetLastError() == hipSuccess ? 0 : 9;  // NQ_ERR_HIP
 }
 
 template <int DT>
 static int combine_in(const MoeRowsLaunch &L, hipStream_t s) {
-    if (L.vec)
-        hipLaunchKernelGGL((k_moe_combine<DT, 8>), token_grid(L), dim3(256), 0, s, L);
-    else
-        hipLaunchKernelGGL((k_moe_combine<DT, 1>), token_grid(L), dim3(256), 0, s, L);
-    return hipGetLastError() == hipSuccess ? 0 : 9;  // NQ_ERR_HIP
+    return L.vec ? combine_wide<DT, 8>(L, s) : combine_wide<DT, 1>(L, s);
 }
 
 template <int DT>
 static int grad_in(const MoeRowsLaunch &L, hipStream_t s) {
-    if (L.vec && L.pairs * L.cols * (DT == 0 ? 4 : 2) > FAR_BYTES)
-        hipLaunchKernelGGL((k_moe_combine_grad<DT, 8, true>), token_grid(L), dim3(256), 0, s, L);
-    else if (L.vec)
-        hipLaunchKernelGGL((k_moe_combine_grad<DT, 8, false>), token_grid(L), dim3(256), 0, s, L);
-    else
-        hipLaunchKernelGGL((k_moe_combine_grad<DT, 1, false>), token_grid(L), dim3(256), 0, s, L);
-    return hipGetLastError() == hipSuccess ? 0 : 9;  // NQ_ERR_HIP
+    if (!L.vec) return grad_wide<DT, 1, false>(L, s);
+    return L.pairs * L.cols * (DT == 0 ? 4 : 2) > FAR_BYTES ? grad_wide<DT, 8, true>(L, s) : grad_wide<DT, 8, false>(L, s);
 }
 
 int launch_moe_combine(const MoeRowsLaunch &L, hipStream_t s) {

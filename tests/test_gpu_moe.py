@@ -100,12 +100,9 @@ def test_no_tokens():
 
 # --- rows -------------------------------------------------------------------------------------------------------
 
-@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("cols", [1, 7, 8, 64, 2048, 2056, 5000])
-@pytest.mark.parametrize("kind", ["random", "half", "none"])
-def test_gather_combine_and_gradient(dtype, cols, kind):
+def rows_run(tokens, top, cols, dtype, kind):
     rng = np.random.default_rng(cols)
-    tokens, top, experts = 37, 5, 12
+    experts = 12
     ids = choices(rng, tokens, top, experts, kind)
     plan = plan_of(ids, experts)
     order, places, offsets = fp8_ref.sort(ids, experts)
@@ -133,6 +130,20 @@ def test_gather_combine_and_gradient(dtype, cols, kind):
     assert none is None
     want_rows, _, _ = fp8_ref.combine_grad(grad.double().numpy(), r64, places, np.ones(w.shape))
     fp8_ref.check(g_rows, want_rows, 0 * want_rows, "gradient of rows, no weights")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("cols", [1, 7, 8, 64, 2048, 2056, 5000])
+@pytest.mark.parametrize("kind", ["random", "half", "none"])
+def test_gather_combine_and_gradient(dtype, cols, kind):
+    rows_run(37, 5, cols, dtype, kind)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("tokens, cols", [(4100, 8), (4100, 30), (4100, 136), (4111, 256), (1100, 33), (1100, 100), (1031, 264), (1031, 1024)])
+def test_narrow_rows_of_many_tokens(tokens, cols, dtype):
+    """Several rows a workgroup."""
+    rows_run(tokens, 3, cols, dtype, "half")
 
 
 def test_rows_without_columns():
