@@ -157,8 +157,13 @@ __global__ __launch_bounds__(64 * MAX_WAVES) void k_fp8_few(Fp8GemmLaunch a) {
             for (int q = 0; q < 4; q++)
                 d = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb_half8(p.w[i][q >> 1][2 * (q & 1)], p.w[i][q >> 1][2 * (q & 1) + 1]), xc[q], d, 0, 0, 0);
             const float s = sx * p.ws[i];
+            if (__builtin_expect(!__any(!(fabsf(s) <= FB_MOST)), 1)) {
 #pragma unroll
-            for (int k = 0; k < 4; k++) acc[i][k] = __builtin_fmaf(d[k], s, acc[i][k]);
+                for (int k = 0; k < 4; k++) acc[i][k] = __builtin_fmaf(d[k], s, acc[i][k]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; k++) acc[i][k] = fb_scaled(d[k], sx, p.ws[i], s, acc[i][k]);
+            }
         }
     };
     // a.chunk is a multiple of DEPTH * waves

@@ -184,6 +184,20 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
         for (int i = 0; i < 4; i++) v[i] = (int)lo[i], v[4 + i] = (int)hi[i];
         return v;
     };
+    // The sums of a block of a tile's weight rows and rows of x.
+    const auto block_sums = [](const fb_i8 &wf, const fb_i8 &xf) {
+        kv_f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (WIDE) {
+#pragma unroll
+            for (int q = 0; q < 4; q++)
+                v = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb_half8((uint32_t)wf[2 * q], (uint32_t)wf[2 * q + 1]),
+                                                           fb_half8((uint32_t)xf[2 * q], (uint32_t)xf[2 * q + 1]), v, 0, 0, 0);
+        } else {
+            v = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf, v, 0, 0, 0, 0, 0, 0);
+        }
+        return v;
+    };
+    float most = 0.0f;  // the largest sx * sw so far
     constexpr int SPREAD = TN > 8 ? TN / 8 : 1, PER = (NW + NX + SPREAD - 1) / SPREAD;
     const auto multiply = [&](auto more, const uint8_t *b, const auto &sw, int32_t kb, uint8_t *b_next, auto &sw_next, int32_t kb_next) {
         fb_i8 xf[TM];
@@ -215,22 +229,16 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
                 if (i + 1 < TN) wf = fetch(b, 16 * (wn * TN + i + 1));
 #pragma unroll
                 for (int k = 0; k < TM; k++) {
-                    kv_f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-                    if constexpr (WIDE) {
-#pragma unroll
-                        for (int q = 0; q < 4; q++)
-                            v = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb_half8((uint32_t)now[2 * q], (uint32_t)now[2 * q + 1]),
-                                                                       fb_half8((uint32_t)xf[k][2 * q], (uint32_t)xf[k][2 * q + 1]), v, 0, 0, 0);
-                    } else {
-                        v = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(now, xf[k], v, 0, 0, 0, 0, 0, 0);
-                    }
-                    d[i & 1][k] = v;
+                    d[i & 1][k] = block_sums(now, xf[k]);
                 }
             }
             if (i > 0) {
                 if ((i - 1) % H == 0) {
 #pragma unroll
-                    for (int k = 0; k < TM; k++) f[k] = sx[k] * sw.v[(i - 1) / H];
+                    for (int k = 0; k < TM; k++) {
+                        f[k] = sx[k] * sw.v[(i - 1) / H];
+                        most = fmaxf(most, fabsf(f[k]));
+                    }
                 }
 #pragma unroll
                 for (int k = 0; k < TM; k++)
@@ -307,6 +315,31 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
         blocks(true);
     else
         blocks(false);
+    // Where some sx * sw left binary32 (fb_scaled), the wave takes its tiles again, straight from memory.
+    if (__builtin_expect(__any(most > FB_MOST), 0)) {
+#pragma unroll
+        for (int k = 0; k < TM; k++) {
+            const int64_t r = source(16 * (wm * TM + k) + j);
+            const uint8_t *const x = (const uint8_t *)a.x + r * a.x_stride + 16 * g;
+#pragma unroll
+            for (int i = 0; i < TN; i++) {
+                const int32_t n = weight_row(16 * (wn * TN + i) + j);
+                const uint8_t *const w = a.w + ((int64_t)t.expert * a.N + (n < a.N ? n : a.N - 1)) * a.K + 16 * g;
+                acc[i][k] = kv_f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+                for (int32_t kb = kb0; kb < kb1; kb++) {
+                    const auto codes = [&](const uint8_t *p) {
+                        const kv_u4 lo = *(const kv_u4 *)(p + (int64_t)kb * FB), hi = *(const kv_u4 *)(p + (int64_t)kb * FB + 64);
+                        return fb_i8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+                    };
+                    const kv_f4 d = block_sums(codes(w), codes(x));
+                    const float sx = a.x_scales[r * KB + kb], sw = ws[i / H][kb], s = sx * sw;
+#pragma unroll
+                    for (int q = 0; q < 4; q++) acc[i][k][q] = fb_scaled(d[q], sx, sw, s, acc[i][k][q]);
+                }
+            }
+        }
+    }
     // lane (j, g): outputs 4 g .. 4 g + 3 of each tile of weight rows, of row j
     if (a.splits > 1) {
 #pragma unroll

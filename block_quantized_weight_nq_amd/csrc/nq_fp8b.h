@@ -10,6 +10,7 @@ namespace nq {
 
 constexpr int FB = 128;                      // values of a block along a row
 constexpr float FB_TINY = 1.17549435e-38f;   // 2^-126, the least scale
+constexpr float FB_MOST = 3.40282347e+38f;   // the largest binary32 number
 constexpr int FB_CODES = 3;                  // x_type of rows that are codes already; 0 to 2 as nq_dtype
 
 struct Fp8QuantLaunch {

@@ -190,6 +190,13 @@ __device__ __forceinline__ int64_t fb_source_row(const Fp8GemmLaunch &a, int64_t
     return r < a.x_rows ? r : a.x_rows - 1;
 }
 
+// acc + d * sx * sw for a block's sum d, s = sx * sw.  Where s leaves binary32 the value need not: a sum of zero stays
+// zero, one of 2^-18 (the least product of two codes) is finite up to 2^146.  |sw| is above 1 then, so d * sx leaves
+// binary32 only where the value does.
+__device__ __forceinline__ float fb_scaled(float d, float sx, float sw, float s, float acc) {
+    return fabsf(s) <= FB_MOST ? __builtin_fmaf(d, s, acc) : acc + d * sx * sw;
+}
+
 // g / (1 + e^-g).  For 16-bit outputs the hardware's exponential and reciprocal, each within 1 ulp of binary32; the
 // argument's rounding makes the exponential off by |g| * 2^-24 of itself at most, 2^-17 at the ends of binary32.
 template <int OT>

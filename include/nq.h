@@ -543,7 +543,8 @@ int nq_moe_sort(const void *ids, int32_t wide, int64_t tokens, int64_t top, int6
  * rows are gates g and the others u, out is [rows, N / 2] of g / (1 + e^-g) * u,
  * and N % 256 == 0 (NQ_ERR_NOT_BLOCK_ALIGNED).
  * Sums are binary32, and sx sw is rounded to it once (to its subnormals below
- * 2^-126).  Up to 16 rows, and for binary32 outputs, products of
+ * 2^-126); where sx sw is beyond binary32, the block's sum is multiplied by sx
+ * and then by sw.  Up to 16 rows, and for binary32 outputs, products of
  * codes are exact; for 16-bit outputs of more rows the 8-bit matrix
  * instruction adds eight products at a time and drops what lies 2^-13 below
  * the largest of the eight.

@@ -1,0 +1,82 @@
+"""GPU: products of E4M3 blocks at the ends of binary32's range, in every kernel: scales whose product leaves it."""
+import numpy as np
+import pytest
+import torch
+
+import block_quantized_weight_nq_amd as nq
+import fp8_ref
+from gpu_util import announce
+from test_gpu_fp8_block import DEV, DT, up, weight
+
+pytestmark = pytest.mark.gpu
+
+# rows, N: up to 16 rows, and the many-rows kernel's tiles of 64, 128 (four and two buffers) and 256 (16-bit outputs)
+SIZES = [(3, 130), (16, 384), (40, 130), (300, 1027), (370, 5888), (1347, 4100), (2100, 8200)]
+
+
+def sampled(rng, most, count):
+    return np.unique(np.r_[0, most - 1, rng.integers(0, most, count)])
+
+
+@pytest.mark.parametrize("large_x", [False, True])
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("m, n", SIZES)
+def test_scales_whose_product_leaves_binary32(m, n, out, large_x):
+    """The first block's scales are 2^96 and 2^34.  Its codes have one nonzero column: weight rows of 2^-9 where n % 3 is 1
+    and of 448 where it is 2, rows of 2^-9 where m % 2 is 0.  So its sums are 0, 2^-18 (2^112 with the scales) or 448 * 2^-9
+    (0.875 * 2^130, an infinity)."""
+    rng = np.random.default_rng(m + n)
+    k = 640
+    xw = rng.integers(0, 0x40, (m, k), dtype=np.uint8) | rng.integers(0, 2, (m, k), dtype=np.uint8) << 7
+    xs = np.exp(rng.normal(0, 0.5, (m, k // 128))).astype(np.float32)
+    ww, ws = weight(rng, n, k)
+    xw[:, :128], ww[:, :128] = 0, 0
+    xw[::2, 77] = 0x01
+    ww[1::3, 77], ww[2::3, 77] = 0x01, 0x7E
+    xs[:, 0], ws[:, 0] = (2.0 ** 96, 2.0 ** 34) if large_x else (2.0 ** 34, 2.0 ** 96)
+    announce(f"scales beyond binary32 {m} x [{n}, {k}] {out}")
+    y = nq.gemm_fp8_block(nq.Fp8Weight(up(ww), torch.as_tensor(ws, device=DEV)), up(xw), torch.as_tensor(xs, device=DEV),
+                          out_dtype=DT[out])
+    infinite = torch.zeros((m, n), dtype=torch.bool, device=DEV)
+    infinite[::2, 2::3] = True
+    if out == "f16":  # 2^112 is one there as well
+        infinite[::2, 1::3] = True
+    assert torch.equal(torch.isposinf(y), infinite) and not bool(y.isnan().any())
+    rows, cols = sampled(rng, m, 12), sampled(rng, n, 24)
+    parts = [fp8_ref.product(xw[rows], xs[rows], ww[c:c + 1], ws[c // 128:c // 128 + 1], out == "f32" or fp8_ref.few_rows(m))
+             for c in cols]
+    want, bound = (np.concatenate([p[i] for p in parts], 1) for i in range(2))
+    got = y[torch.as_tensor(rows, device=DEV)][:, torch.as_tensor(cols, device=DEV)]
+    high = torch.isinf(got).cpu().numpy()
+    fp8_ref.check(got.masked_fill(torch.isinf(got), 0), np.where(high, 0, want), np.where(high, 0, bound), "beyond binary32")
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_values_whose_scales_leave_binary32(out):
+    """Rows that are values, rounded within the call: weight rows of zeros give zeros, not 0 times an infinity."""
+    rng = np.random.default_rng(5)
+    for m in (2, 60):
+        x = rng.normal(0, 1, (m, 256)).astype(np.float32)
+        x[:, :128] *= np.float32(1e37)
+        ww, ws = weight(rng, 70, 256)
+        ww[::2, :128] = 0
+        ws[:, 0] = 1e9
+        y = nq.gemm_fp8_block(nq.Fp8Weight(up(ww), torch.as_tensor(ws, device=DEV)), torch.as_tensor(x, device=DEV), out_dtype=DT[out])
+        fp8_ref.check(y[:, ::2], *fp8_ref.product(*fp8_ref.quantize(x), ww[::2], ws, out == "f32" or m <= 16), f"{m} rows")
+
+
+def test_experts_whose_scales_leave_binary32():
+    rng = np.random.default_rng(6)
+    for tokens, n in ((10, 130), (150, 130), (500, 4100)):
+        experts, k = 4, 256
+        xw = rng.integers(0, 0x40, (tokens, k), dtype=np.uint8)
+        xs = np.ones((tokens, 2), np.float32)
+        ww, ws = weight(rng, experts, n, k)
+        xw[:, :128] = 0
+        xs[:, 0], ws[1:3, :, 0] = 2.0 ** 100, 2.0 ** 60
+        plan = nq.moe_sort(torch.as_tensor(rng.integers(0, experts, (tokens, 2)), device=DEV), experts)
+        handle = nq.Fp8Weight(up(ww), torch.as_tensor(ws, device=DEV))
+        y = nq.moe_gemm_fp8_block(handle, up(xw), plan, torch.as_tensor(xs, device=DEV), out_dtype=torch.bfloat16)
+        one = np.where(np.arange(2) == 0, 1, xs).astype(np.float32)  # zeros of a block are zeros whatever its scale
+        want = nq.moe_gemm_fp8_block(handle, up(xw), plan, torch.as_tensor(one, device=DEV), out_dtype=torch.bfloat16)
+        assert bool(want.isfinite().all()) and torch.equal(y, want)
