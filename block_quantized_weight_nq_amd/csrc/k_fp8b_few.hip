@@ -204,7 +204,7 @@ __global__ __launch_bounds__(64 * MAX_WAVES) void k_fp8_few(Fp8GemmLaunch a) {
         if constexpr (GATED) {
             const kv_f4 up = total(i + PER);
 #pragma unroll
-            for (int k = 0; k < 4; k++) f[k] = fb_silu<0>(f[k]) * up[k];
+            for (int k = 0; k < 4; k++) f[k] = fb_gate<0>(f[k], up[k]);
         }
         const int m = at & 15, n = n0 + 16 * i + 4 * (at >> 4);
         if (m >= t.count) continue;

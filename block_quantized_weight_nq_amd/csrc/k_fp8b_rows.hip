@@ -373,7 +373,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
             for (int i = 0; i < TILES; i++) {
                 float f[4];
 #pragma unroll
-                for (int q = 0; q < 4; q++) f[q] = GATED ? fb_silu<OT>(acc[i][k][q]) * acc[GATED ? i + H : i][k][q] : acc[i][k][q];
+                for (int q = 0; q < 4; q++) f[q] = GATED ? fb_gate<OT>(acc[i][k][q], acc[GATED ? i + H : i][k][q]) : acc[i][k][q];
                 kv_write4<OT>(own + (16 * k + j) * ROW + (((2 * i + (g >> 1)) ^ (j & (V - 1))) << 4), 4 * (g & 1), f);
             }
         constexpr int RT = 64 / V;  // rows of a store
@@ -402,7 +402,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
                 const int32_t n = weight_row(16 * (wn * TN + i)) + 4 * g;
                 kv_f4 f;
 #pragma unroll
-                for (int q = 0; q < 4; q++) f[q] = GATED ? fb_silu<OT>(acc[i][k][q]) * acc[GATED ? i + H : i][k][q] : acc[i][k][q];
+                for (int q = 0; q < 4; q++) f[q] = GATED ? fb_gate<OT>(acc[i][k][q], acc[GATED ? i + H : i][k][q]) : acc[i][k][q];
                 float *const to = (float *)a.out + (t.first + m) * NO + n;
                 if (n + 3 < NO) {
                     *(fb_any32 *)to = f;
@@ -443,7 +443,7 @@ __global__ __launch_bounds__(256) void k_fp8_join(Fp8GemmLaunch a) {
         }
         if (a.gated)
 #pragma unroll
-            for (int q = 0; q < PER; q++) y[q] = fb_silu<0>(y[q]) * up[q];
+            for (int q = 0; q < PER; q++) y[q] = fb_gate<0>(y[q], up[q]);
         if constexpr (PER == 4)
             fb_write4(a.out, m * NO + n, y, a.out_dtype);
         else

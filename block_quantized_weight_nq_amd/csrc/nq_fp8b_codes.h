@@ -197,14 +197,21 @@ __device__ __forceinline__ float fb_scaled(float d, float sx, float sw, float s,
     return fabsf(s) <= FB_MOST ? __builtin_fmaf(d, s, acc) : acc + d * sx * sw;
 }
 
-// g / (1 + e^-g).  For 16-bit outputs the hardware's exponential and reciprocal, each within 1 ulp of binary32; the
-// argument's rounding makes the exponential off by |g| * 2^-24 of itself at most, 2^-17 at the ends of binary32.
+// g / (1 + e^-g) * u.  For 16-bit outputs the hardware's exponential and reciprocal, each within 1 ulp of binary32; the
+// roundings of the argument make the exponential off by |g| * 2^-23 of itself at most.
+// Below -80 the quotient is g * e^g (to e^-80 of itself).  e^-g leaves binary32 there (from -88.8 on), and the hardware's
+// reciprocal gives no subnormal numbers (from -87.4 on), while the value with u need not be small: the fourth root of e^g
+// is in range as far as u can make up for it.  u comes after the first factor, so that only the value itself underflows.
 template <int OT>
-__device__ __forceinline__ float fb_silu(float g) {
+__device__ __forceinline__ float fb_gate(float g, float u) {
+    if (g < -80.0f) {
+        const float h = OT == 0 ? expf(0.25f * g) : __builtin_amdgcn_exp2f(g * 0.36067376f);
+        return g * h * u * h * h * h;
+    }
     if constexpr (OT == 0)
-        return g / (1.0f + expf(-g));
+        return g / (1.0f + expf(-g)) * u;
     else
-        return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f));
+        return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f)) * u;
 }
 
 // One value of type ot.

@@ -1,4 +1,5 @@
-"""GPU: products of E4M3 blocks at the ends of binary32's range, in every kernel: scales whose product leaves it."""
+"""GPU: products of E4M3 blocks at the ends of binary32's range, in every kernel: scales whose product leaves it, gates far
+below zero."""
 import numpy as np
 import pytest
 import torch
@@ -80,3 +81,40 @@ def test_experts_whose_scales_leave_binary32():
         one = np.where(np.arange(2) == 0, 1, xs).astype(np.float32)  # zeros of a block are zeros whatever its scale
         want = nq.moe_gemm_fp8_block(handle, up(xw), plan, torch.as_tensor(one, device=DEV), out_dtype=torch.bfloat16)
         assert bool(want.isfinite().all()) and torch.equal(y, want)
+
+
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("m", [1, 16, 17, 200, 2100])
+@pytest.mark.parametrize("k", [128, 4096])
+def test_gates_far_below_zero(m, k, out):
+    """Gates of -60 to -196 and ups of 2^30 to 2^127, each one product of two codes and their scales, so exact: what is
+    compared is g / (1 + e^-g) * u alone, e^-g beyond binary32 and e^g below its normal numbers among them.
+
+    The kernels take the fourth root of e^g: a binary32 exponential (1 ulp) in four factors and five roundings for binary32
+    outputs and calls of up to 16 rows, 13 * 2^-24; the hardware's exponential, whose argument carries two roundings,
+    |g| * 2^-23 more, for others."""
+    tiles = 36
+    if m == 2100 and k == 4096:
+        tiles = 64
+    half = 128 * tiles
+    g = -np.concatenate([np.linspace(60, 110, 26), np.linspace(115, 196, tiles - 26)]).round()
+    u = np.full(tiles, 2.0 ** 127)
+    u[:26:2], u[1:26:2] = 2.0 ** 122, 2.0 ** np.arange(30, 121, 7.5).round()  # (silu(-88) is near 2^-120)
+    xw, ww = np.zeros((m, k), np.uint8), np.zeros((2 * half, k), np.uint8)
+    xw[:, 5], ww[:half, 5], ww[half:, 5] = 0x38, 0xB8, 0x38  # 1, -1 and 1
+    ww[:half:5, 5] = 0xB4  # -0.75
+    xs, ws = np.ones((m, k // 128), np.float32), np.ones((2 * tiles, k // 128), np.float32)
+    ws[:tiles, 0], ws[tiles:, 0] = -g, u
+    announce(f"far gates {m} x [{2 * half}, {k}] {out}")
+    y = nq.gemm_fp8_block(nq.Fp8Weight(up(ww), torch.as_tensor(ws, device=DEV)), up(xw), torch.as_tensor(xs, device=DEV), gated=True,
+                          out_dtype=DT[out])
+    gate = np.repeat(g, 128)
+    gate[::5] *= 0.75
+    with np.errstate(over="ignore"):
+        want = gate / (1 + np.exp(-gate)) * np.repeat(u, 128)
+    rel = 13 * 2.0 ** -24 + (0 if out == "f32" or fp8_ref.few_rows(m) else np.abs(gate) * 2.0 ** -23)
+    want, rel = np.broadcast_to(want, (m, half)), np.broadcast_to(np.abs(want) * rel, (m, half))
+    most = {"f32": 3.4e38, "f16": 65504.0, "bf16": 3.38e38}[out]
+    inside = np.abs(want) < most
+    got = y.masked_fill(torch.as_tensor(~inside, device=DEV), 0)
+    fp8_ref.check(got, np.where(inside, want, 0), np.where(inside, rel, 0), "far gates")
