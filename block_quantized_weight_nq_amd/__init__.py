@@ -873,6 +873,7 @@ def kv_attention(cache, q, token_start, lengths, table, scale=None, window=0, ma
 
 # --- E4M3 blocks of 128, and rows sorted by expert ----------------------------------------------------------------
 
+# Types go to the library as _KV_DTYPES' codes, -1 for what it refuses as NQ_ERR_BAD_DTYPE.
 _BLOCK_ARGS, _PLAN_ARGS = struct.Struct("@PqPPPPqqqiiii"), struct.Struct("@PPPqqq")
 assert _BLOCK_ARGS.size == ctypes.sizeof(Fp8BlockArgs) and _PLAN_ARGS.size == ctypes.sizeof(MoePlanDesc)
 _SORT_WORKSPACES = {}
@@ -912,11 +913,10 @@ def quantize_fp8_block(x, tile=1, stream=None):
         matrices, rows, cols, scales_shape = _block_shapes(shape, tile)
     if strides[-1] != 1 and x.numel() or (matrices > 1 and strides[0] != rows * strides[1]):
         raise ValueError("x must have contiguous columns, and matrices must follow each other row by row")
-    code = _KV_DTYPES.get(x.dtype)
     codes = x.new_empty(shape, dtype=_F8)
     scales = x.new_empty(scales_shape, dtype=_F32)
-    st = (_LIB or _lib()).nq_quantize_fp8_block(x.data_ptr(), _dtype_code(x.dtype) if code is None else code, matrices, rows, cols, strides[-2], tile,
-                                                codes.data_ptr(), scales.data_ptr(), _STREAM(index))
+    st = (_LIB or _lib()).nq_quantize_fp8_block(x.data_ptr(), _KV_DTYPES.get(x.dtype, -1), matrices, rows, cols, strides[-2],
+                                                tile, codes.data_ptr(), scales.data_ptr(), _STREAM(index))
     if st != NQ_OK:
         raise NqError(st, f"x {list(shape)} {x.dtype}, tile {tile}")
     return codes, scales
@@ -946,10 +946,9 @@ def dequantize_fp8_block(codes, scales, tile=1, out_dtype=None, stream=None):
     if scales.dtype is not _F32 or scales.shape != scales_shape or scales.get_device() != index or not scales.is_contiguous():
         _scales_of("scales", scales, scales_shape, index)
     out_dtype = out_dtype or _F32
-    code = _kv_dtype(out_dtype)
     out = codes.new_empty(shape, dtype=out_dtype)
-    st = (_LIB or _lib()).nq_dequantize_fp8_block(codes.data_ptr(), scales.data_ptr(), matrices, rows, cols, tile, code,
-                                                  out.data_ptr(), _STREAM(index))
+    st = (_LIB or _lib()).nq_dequantize_fp8_block(codes.data_ptr(), scales.data_ptr(), matrices, rows, cols, tile,
+                                                  _KV_DTYPES.get(out_dtype, -1), out.data_ptr(), _STREAM(index))
     if st != NQ_OK:
         raise NqError(st, f"codes {list(codes.shape)} as {out.dtype}")
     return out
@@ -1038,7 +1037,7 @@ def _block_product(weight, x, x_scales, plan, sorted_rows, gated, out_dtype):
     _rows_of("x", x, wanted, k, index)
     pointer, stride, dtype = x.data_ptr(), x.stride(0), x.dtype
     if x_scales is None:
-        code, xs = _kv_dtype(dtype), 0
+        code, xs = _KV_DTYPES.get(dtype, -1), 0
         out_dtype = out_dtype or dtype
     else:
         if dtype is not _F8:
@@ -1046,7 +1045,7 @@ def _block_product(weight, x, x_scales, plan, sorted_rows, gated, out_dtype):
         _scales_of("x_scales", x_scales, (rows, k // FP8_BLOCK), index)
         code, xs = 3, x_scales.data_ptr()
         out_dtype = out_dtype or _F32
-    out_code = _kv_dtype(out_dtype)
+    out_code = _KV_DTYPES.get(out_dtype, -1)
     out = x.new_empty((out_rows, n // 2 if gated else n), dtype=out_dtype)
     lib, ref = _LIB or _lib(), plan._ref if plan is not None else None
     args = _BLOCK_ARGS.pack(pointer, stride, xs, weight.codes.data_ptr(), weight.scales.data_ptr(), out.data_ptr(), rows, n, k,
@@ -1067,7 +1066,7 @@ def _block_product(weight, x, x_scales, plan, sorted_rows, gated, out_dtype):
         ws = x.new_empty(need, dtype=_U8) if need else None
         st = lib.nq_gemm_fp8_block(args, ref, ws.data_ptr() if need else None, need, _STREAM(index))
     if st != NQ_OK:
-        raise NqError(st, f"x {list(x.shape)} {dtype}, weight {list(weight.codes.shape)}, gated {gated}")
+        raise NqError(st, f"x {list(x.shape)} {dtype}, weight {list(weight.codes.shape)}, gated {gated}, out {out_dtype}")
     return out
 
 
@@ -1192,11 +1191,10 @@ def moe_combine(rows, plan, weights=None, stream=None):
     shape, strides, tokens = rows.shape, rows.stride(), plan.tokens
     if len(shape) != 2 or shape[0] != plan.pairs or rows.get_device() != index or strides[1] != 1:
         _rows_of("rows", rows, plan.pairs, None, index)
-    code = _KV_DTYPES.get(rows.dtype)
     cols = shape[1]
     out = rows.new_empty((tokens, cols))
-    st = (_LIB or _lib()).nq_moe_combine(plan._ref, rows.data_ptr(), strides[0], _dtype_code(rows.dtype) if code is None else code,
-                                         cols, None if weights is None else _weights_of(weights, plan), out.data_ptr(),
+    st = (_LIB or _lib()).nq_moe_combine(plan._ref, rows.data_ptr(), strides[0], _KV_DTYPES.get(rows.dtype, -1), cols,
+                                         None if weights is None else _weights_of(weights, plan), out.data_ptr(),
                                          _STREAM(index))
     if st != NQ_OK:
         raise NqError(st, f"rows {list(rows.shape)} {rows.dtype}")
@@ -1229,10 +1227,9 @@ def moe_combine_grad(grad, rows, plan, weights=None, stream=None):
         pointer = _weights_of(weights, plan)
         out_weights = weights.new_empty((plan.tokens, plan.top))
         out_pointer = out_weights.data_ptr()
-    code = _KV_DTYPES.get(dtype)
     st = (_LIB or _lib()).nq_moe_combine_grad(plan._ref, grad.data_ptr(), grad_strides[0], rows.data_ptr(), strides[0],
-                                              _dtype_code(dtype) if code is None else code, cols, pointer, out.data_ptr(),
-                                              out_pointer, _STREAM(index))
+                                              _KV_DTYPES.get(dtype, -1), cols, pointer, out.data_ptr(), out_pointer,
+                                              _STREAM(index))
     if st != NQ_OK:
         raise NqError(st, f"rows {list(rows.shape)} {rows.dtype}")
     return out, out_weights

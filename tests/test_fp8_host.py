@@ -292,3 +292,26 @@ def test_grids_have_each_tile_once(emu):
         hits = np.zeros(m * n, np.int32)
         assert emu.nq_fp8_emu_grid(m, n, hits.ctypes.data) == 0
         assert (hits == 1).all(), (m, n)
+
+
+# --- types ------------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [torch.int32, torch.float64, torch.uint8, torch.float8_e5m2])
+def test_types_that_no_call_takes_are_refused_as_such(gpus, monkeypatch, dtype):  # noqa: F811
+    """NQ_ERR_BAD_DTYPE of the library itself, for inputs and outputs alike."""
+    monkeypatch.setattr(nq, "_LIB", None)
+    f8 = lambda *shape: Tensor(shape, torch.float8_e4m3fn, 0)  # noqa: E731
+    f32 = lambda *shape: Tensor(shape, torch.float32, 0)  # noqa: E731
+    i32 = lambda *shape: Tensor(shape, torch.int32, 0)  # noqa: E731
+    one, many = nq.Fp8Weight(f8(256, 128), f32(2, 1)), nq.Fp8Weight(f8(4, 256, 128), f32(4, 2, 1))
+    plan = nq.MoePlan(i32(6), i32(3, 2), i32(5))
+    x, other, rows = f32(3, 128), Tensor((3, 128), dtype, 0), Tensor((6, 8), dtype, 0)
+    for call in (lambda: nq.quantize_fp8_block(other), lambda: nq.quantize_fp8_block(Tensor((2, 3, 128), dtype, 0), 128),
+                 lambda: nq.dequantize_fp8_block(f8(3, 128), f32(3, 1), out_dtype=dtype), lambda: nq.gemm_fp8_block(one, other),
+                 lambda: nq.gemm_fp8_block(one, x, out_dtype=dtype), lambda: nq.gemm_fp8_block(one, f8(3, 128), f32(3, 1), out_dtype=dtype),
+                 lambda: nq.moe_gemm_fp8_block(many, other, plan), lambda: nq.moe_gemm_fp8_block(many, x, plan, out_dtype=dtype),
+                 lambda: nq.moe_combine(rows, plan), lambda: nq.moe_combine_grad(Tensor((3, 8), dtype, 0), rows, plan),
+                 lambda: nq.gemm_fp8_block(one, f8(3, 128))):  # codes without their scales
+        with pytest.raises(nq.NqError) as refused:
+            call()
+        assert refused.value.status == 8
