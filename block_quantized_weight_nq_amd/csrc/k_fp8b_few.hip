@@ -21,6 +21,8 @@
 // that multiply: 150 vector instructions a block of 128, which bound it at 3.5 TB/s.)
 #include "nq_fp8b_codes.h"
 
+#include <type_traits>
+
 namespace nq {
 
 namespace {
@@ -40,6 +42,7 @@ template <int XT, int NT, bool GATED>
 __global__ __launch_bounds__(64 * MAX_WAVES) void k_fp8_few(Fp8GemmLaunch a) {
     // codes of x, a block's rows together, and their scales; in the end the waves' sums, [wave][NT][lane]
     extern __shared__ __align__(16) uint8_t lds[];
+    __shared__ bool lost[MAX_WAVES];
     const int tid = threadIdx.x, lane = tid & 63, j = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = a.waves;
     Fp8Tile t;
@@ -82,8 +85,6 @@ __global__ __launch_bounds__(64 * MAX_WAVES) void k_fp8_few(Fp8GemmLaunch a) {
     }
     constexpr int DEPTH = fb_few_depth(NT);
     kv_f4 acc[NT];
-#pragma unroll
-    for (int i = 0; i < NT; i++) acc[i] = kv_f4{0.0f, 0.0f, 0.0f, 0.0f};
 
     struct Part {
         kv_u4 w[NT][2], x[2];
@@ -136,7 +137,8 @@ __global__ __launch_bounds__(64 * MAX_WAVES) void k_fp8_few(Fp8GemmLaunch a) {
         }
         __syncthreads();
     };
-    const auto multiply = [&](const Part &p, int32_t block) {
+    float most = 0.0f;  // the largest sx * sw so far
+    const auto multiply = [&](auto careful, const Part &p, int32_t block) {
         kv_u4 v[2];
         float sx;
         if constexpr (RAW) {
@@ -157,36 +159,49 @@ __global__ __launch_bounds__(64 * MAX_WAVES) void k_fp8_few(Fp8GemmLaunch a) {
             for (int q = 0; q < 4; q++)
                 d = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb_half8(p.w[i][q >> 1][2 * (q & 1)], p.w[i][q >> 1][2 * (q & 1) + 1]), xc[q], d, 0, 0, 0);
             const float s = sx * p.ws[i];
-            if (__builtin_expect(!__any(!(fabsf(s) <= FB_MOST)), 1)) {
+            if constexpr (!careful()) most = fmaxf(most, fabsf(s));
 #pragma unroll
-                for (int k = 0; k < 4; k++) acc[i][k] = __builtin_fmaf(d[k], s, acc[i][k]);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 4; k++) acc[i][k] = fb_scaled(d[k], sx, p.ws[i], s, acc[i][k]);
-            }
+            for (int k = 0; k < 4; k++) acc[i][k] = careful() ? fb_scaled(d[k], sx, p.ws[i], s, acc[i][k]) : __builtin_fmaf(d[k], s, acc[i][k]);
         }
     };
-    // a.chunk is a multiple of DEPTH * waves
+    const auto blocks = [&](auto careful) {
 #pragma unroll
-    for (int d = 0; d < DEPTH; d++)
-        if (wave + d * waves < KB) read(part[d], wave + d * waves);
-    for (int32_t c0 = 0; c0 < KB; c0 += a.chunk) {
-        if constexpr (RAW) refill(c0);
-        const int32_t end = KB - c0 < a.chunk ? KB - c0 : a.chunk;
-        for (int32_t b = wave; b < end; b += DEPTH * waves) {
+        for (int i = 0; i < NT; i++) acc[i] = kv_f4{0.0f, 0.0f, 0.0f, 0.0f};
+        // a.chunk is a multiple of DEPTH * waves
 #pragma unroll
-            for (int d = 0; d < DEPTH; d++) {
-                const int32_t now = b + d * waves, next = c0 + now + DEPTH * waves;
-                if (now < end) multiply(part[d], now);
-                if (next < KB) read(part[d], next);
+        for (int d = 0; d < DEPTH; d++)
+            if (wave + d * waves < KB) read(part[d], wave + d * waves);
+        for (int32_t c0 = 0; c0 < KB; c0 += a.chunk) {
+            if constexpr (RAW) refill(c0);
+            const int32_t end = KB - c0 < a.chunk ? KB - c0 : a.chunk;
+            for (int32_t b = wave; b < end; b += DEPTH * waves) {
+#pragma unroll
+                for (int d = 0; d < DEPTH; d++) {
+                    const int32_t now = b + d * waves, next = c0 + now + DEPTH * waves;
+                    if (now < end) multiply(careful, part[d], now);
+                    if (next < KB) read(part[d], next);
+                }
             }
         }
-    }
-    if constexpr (RAW) __syncthreads();
+        if constexpr (RAW) __syncthreads();
+    };
+    blocks(std::false_type());
+    const bool left = __any(most > FB_MOST);
+    if (lane == 0) lost[wave] = left;
     kv_f4 *const red = (kv_f4 *)lds;
 #pragma unroll
     for (int i = 0; i < NT; i++) red[(wave * NT + i) * 64 + lane] = acc[i];
     __syncthreads();
+    // Where some sx * sw left binary32 (fb_scaled), the workgroup does all again with care (a choice at each block: 1 us of 34
+    // for 4 x 8 pairs on 64 gated [2816, 2048]).
+    bool again = false;
+    for (int v = 0; v < waves; v++) again |= lost[v];
+    if (again) {
+        blocks(std::true_type());
+#pragma unroll
+        for (int i = 0; i < NT; i++) red[(wave * NT + i) * 64 + lane] = acc[i];
+        __syncthreads();
+    }
     constexpr int PER = GATED ? NT / 2 : NT;
     for (int q = tid; q < PER * 64; q += 64 * waves) {
         const int at = q & 63, i = q >> 6;

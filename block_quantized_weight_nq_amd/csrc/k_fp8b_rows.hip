@@ -360,60 +360,76 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
         }
         return;
     }
-    if constexpr (OT != 0) {
-        // Rows of V times 16 bytes through LDS, so that a store writes whole rows of the wave's tile (32 bytes of sixteen
-        // rows each otherwise); a row's pieces are exchanged by its number.  (With single stores where N is no multiple of
-        // 8, 10054 rows of 256 [4147, 128] took 253 us instead of 177.)
-        constexpr int TILES = GATED ? H : TN, V = 2 * TILES, ROW = 16 * V;
-        fb_meet<0>();
-        uint8_t *const own = (wave < WAVES / 2 ? buffer0 : buffer1) + wave % (WAVES / 2) * 16 * TM * ROW;
+    if constexpr (OT != 0) fb_meet<0>();  // the outputs go through the buffers
+    // (one branch for all gates of a wave: one at each costs the large tiles of gated products 5%)
+    const auto write = [&](auto far) {
+        if constexpr (OT != 0) {
+            // Rows of V times 16 bytes through LDS, so that a store writes whole rows of the wave's tile (32 bytes of sixteen
+            // rows each otherwise); a row's pieces are exchanged by its number.  (With single stores where N is no multiple of
+            // 8, 10054 rows of 256 [4147, 128] took 253 us instead of 177.)
+            constexpr int TILES = GATED ? H : TN, V = 2 * TILES, ROW = 16 * V;
+            uint8_t *const own = (wave < WAVES / 2 ? buffer0 : buffer1) + wave % (WAVES / 2) * 16 * TM * ROW;
 #pragma unroll
-        for (int k = 0; k < TM; k++)
+            for (int k = 0; k < TM; k++)
 #pragma unroll
-            for (int i = 0; i < TILES; i++) {
-                float f[4];
+                for (int i = 0; i < TILES; i++) {
+                    float f[4];
 #pragma unroll
-                for (int q = 0; q < 4; q++) f[q] = GATED ? fb_gate<OT>(acc[i][k][q], acc[GATED ? i + H : i][k][q]) : acc[i][k][q];
-                kv_write4<OT>(own + (16 * k + j) * ROW + (((2 * i + (g >> 1)) ^ (j & (V - 1))) << 4), 4 * (g & 1), f);
-            }
-        constexpr int RT = 64 / V;  // rows of a store
-        const int n = weight_row(16 * wn * TN) + 8 * (lane % V);
+                    for (int q = 0; q < 4; q++) f[q] = GATED ? fb_gate<OT, far()>(acc[i][k][q], acc[GATED ? i + H : i][k][q]) : acc[i][k][q];
+                    kv_write4<OT>(own + (16 * k + j) * ROW + (((2 * i + (g >> 1)) ^ (j & (V - 1))) << 4), 4 * (g & 1), f);
+                }
+            constexpr int RT = 64 / V;  // rows of a store
+            const int n = weight_row(16 * wn * TN) + 8 * (lane % V);
 #pragma unroll
-        for (int r0 = 0; r0 < 16 * TM; r0 += RT) {
-            const int r = r0 + lane / V, m = 16 * wm * TM + r;
-            const kv_u4 v = *(const kv_u4 *)(own + r * ROW + (((lane % V) ^ (r & (V - 1))) << 4));
-            uint16_t *const to = (uint16_t *)a.out + (t.first + m) * NO + n;
-            if (m >= t.count) continue;
-            if (n + 8 <= NO) {
-                *(fb_any16 *)to = v;
-            } else {
-#pragma unroll
-                for (int q = 0; q < 8; q++)
-                    if (n + q < NO) to[q] = (uint16_t)(v[q >> 1] >> (16 * (q & 1)));
-            }
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < TM; k++) {
-            const int m = 16 * (wm * TM + k) + j;
-            if (m >= t.count) continue;
-#pragma unroll
-            for (int i = 0; i < (GATED ? H : TN); i++) {
-                const int32_t n = weight_row(16 * (wn * TN + i)) + 4 * g;
-                kv_f4 f;
-#pragma unroll
-                for (int q = 0; q < 4; q++) f[q] = GATED ? fb_gate<OT>(acc[i][k][q], acc[GATED ? i + H : i][k][q]) : acc[i][k][q];
-                float *const to = (float *)a.out + (t.first + m) * NO + n;
-                if (n + 3 < NO) {
-                    *(fb_any32 *)to = f;
+            for (int r0 = 0; r0 < 16 * TM; r0 += RT) {
+                const int r = r0 + lane / V, m = 16 * wm * TM + r;
+                const kv_u4 v = *(const kv_u4 *)(own + r * ROW + (((lane % V) ^ (r & (V - 1))) << 4));
+                uint16_t *const to = (uint16_t *)a.out + (t.first + m) * NO + n;
+                if (m >= t.count) continue;
+                if (n + 8 <= NO) {
+                    *(fb_any16 *)to = v;
                 } else {
 #pragma unroll
-                    for (int q = 0; q < 4; q++)
-                        if (n + q < NO) to[q] = f[q];
+                    for (int q = 0; q < 8; q++)
+                        if (n + q < NO) to[q] = (uint16_t)(v[q >> 1] >> (16 * (q & 1)));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < TM; k++) {
+                const int m = 16 * (wm * TM + k) + j;
+                if (m >= t.count) continue;
+#pragma unroll
+                for (int i = 0; i < (GATED ? H : TN); i++) {
+                    const int32_t n = weight_row(16 * (wn * TN + i)) + 4 * g;
+                    kv_f4 f;
+#pragma unroll
+                    for (int q = 0; q < 4; q++) f[q] = GATED ? fb_gate<OT, far()>(acc[i][k][q], acc[GATED ? i + H : i][k][q]) : acc[i][k][q];
+                    float *const to = (float *)a.out + (t.first + m) * NO + n;
+                    if (n + 3 < NO) {
+                        *(fb_any32 *)to = f;
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; q++)
+                            if (n + q < NO) to[q] = f[q];
+                    }
                 }
             }
         }
+    };
+    float low = 0.0f;
+    if constexpr (GATED) {
+#pragma unroll
+        for (int k = 0; k < TM; k++)
+#pragma unroll
+            for (int i = 0; i < H; i++)
+#pragma unroll
+                for (int q = 0; q < 4; q++) low = fminf(low, acc[i][k][q]);
     }
+    if (GATED && __any(low < FB_FAR_GATE))
+        write(std::true_type());
+    else
+        write(std::false_type());
 }
 
 // The pieces' sums in order, and the epilogue; four columns a thread where they are a multiple of four.
