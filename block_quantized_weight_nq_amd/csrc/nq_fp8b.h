@@ -71,6 +71,8 @@ inline int64_t fb_row_tiles(int64_t rows, int64_t experts, int64_t bm) {
 
 // The segment and rows of row tile `t` of `bm` rows: expert -1 is what lies behind the last expert's rows (they get 0),
 // count 0 that there is no such tile.  `at(i)` reads offset i; whatever it holds, first and count stay within rows.
+// A wave searches, a lane looks at one expert: `Wave` has numbers of its lanes (Lanes, 32 bits, whose sums wrap) and what
+// a wave does with them, each(f) of f(lane), scan, the mask of those above a number, and one lane's.
 struct Fp8Tile {
     int32_t expert;
     int64_t first;
@@ -79,16 +81,35 @@ struct Fp8Tile {
 
 __host__ __device__ inline int64_t fb_clamp(int64_t v, int64_t hi) { return v < 0 ? 0 : v > hi ? hi : v; }
 
-template <typename At>
-inline Fp8Tile fb_find_tile_host(At at, int32_t experts, int64_t rows, int32_t bm, int64_t t) {
-    for (int32_t e = 0; e <= experts; e++) {
-        const int64_t lo = fb_clamp(at(e), rows), hi = e < experts ? fb_clamp(at(e + 1), rows) : rows;
-        const int64_t n = hi > lo ? fb_ceil(hi - lo, bm) : 0;
-        if (t < n) {
-            const int64_t first = lo + t * bm;
-            return {e < experts ? e : -1, first, (int32_t)(hi - first < bm ? hi - first : bm)};
+template <typename Wave, typename At>
+__host__ __device__ inline Fp8Tile fb_find_tile_by(At at, int32_t experts, int64_t rows, int32_t bm, int32_t t) {
+    const int32_t most = (int32_t)rows;  // (at most 2^30)
+    uint32_t left = (uint32_t)t;
+    for (int32_t e0 = 0; e0 <= experts; e0 += 64) {
+        // (two loads that no condition keeps apart)
+        const auto lo = Wave::each([&](int lane) {
+            const int32_t e = e0 + lane, v = (int32_t)fb_clamp(at(e < experts ? e : experts), most);
+            return e <= experts ? v : 0;
+        });
+        const auto hi = Wave::each([&](int lane) {
+            const int32_t e = e0 + lane, v = (int32_t)fb_clamp(at(e < experts ? e + 1 : experts), most);
+            return e < experts ? v : e == experts ? most : 0;
+        });
+        const auto n = Wave::each([&](int lane) {
+            const int32_t rows_of = Wave::own(hi, lane) - Wave::own(lo, lane);
+            return rows_of > 0 ? (int32_t)((uint32_t)(rows_of + bm - 1) / (uint32_t)bm) : 0;
+        });
+        const auto sum = Wave::scan(n);
+        const uint64_t past = Wave::above(sum, (int32_t)left);
+        if (past) {
+            const int i = __builtin_ctzll(past);
+            const int32_t from = Wave::lane(lo, i), end = Wave::lane(hi, i);
+            const int32_t before = (int32_t)((uint32_t)Wave::lane(sum, i) - (uint32_t)Wave::lane(n, i));
+            const int64_t first = from + (int64_t)(int32_t)(left - (uint32_t)before) * bm;
+            if (first < from || first >= end) break;  // offsets that no sort gives: their sum may have left 32 bits
+            return {e0 + i < experts ? e0 + i : -1, first, (int32_t)(end - first < bm ? end - first : bm)};
         }
-        t -= n;
+        left -= (uint32_t)Wave::lane(sum, 63);
     }
     return {-1, 0, 0};
 }

@@ -148,38 +148,29 @@ __device__ __forceinline__ kv_h8 fb_half8(uint32_t lo, uint32_t hi) {
 
 // The sum of the lanes' numbers up to each.
 __device__ __forceinline__ int32_t fb_scan(int32_t v) {
-    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // from 1, 2, 4 and 8 lanes before, in rows of sixteen
-    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // the end of a row to the next, of rows 0 and 2
-    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // the end of row 1 to rows 2 and 3
-    return v;
+    uint32_t s = (uint32_t)v;  // (sums wrap)
+    s += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)s, 0x111, 0xF, 0xF, false);  // from 1, 2, 4 and 8 lanes before, in rows of sixteen
+    s += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)s, 0x112, 0xF, 0xF, false);
+    s += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)s, 0x114, 0xF, 0xF, false);
+    s += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)s, 0x118, 0xF, 0xF, false);
+    s += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)s, 0x142, 0xA, 0xF, false);  // the end of a row to the next, of rows 0 and 2
+    s += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)s, 0x143, 0xC, 0xF, false);  // the end of row 1 to rows 2 and 3
+    return (int32_t)s;
 }
 
-// The row tile of a workgroup (fb_find_tile_host's rule), by a wave: a lane looks at one expert.
-__device__ __forceinline__ Fp8Tile fb_find_tile(const int32_t *offsets, int32_t experts, int64_t rows, int32_t bm, int32_t t) {
-    const int lane = threadIdx.x & 63;
-    const int32_t most = (int32_t)rows;  // (at most 2^30)
-    for (int32_t e0 = 0; e0 <= experts; e0 += 64) {
-        const int32_t e = e0 + lane;
-        int32_t lo = 0, hi = 0;
-        if (e <= experts) {
-            lo = (int32_t)fb_clamp(offsets[e], most);
-            hi = e < experts ? (int32_t)fb_clamp(offsets[e + 1], most) : most;
-        }
-        const int32_t n = hi > lo ? (int32_t)((uint32_t)(hi - lo + bm - 1) / (uint32_t)bm) : 0, sum = fb_scan(n);
-        const uint64_t past = __ballot(sum > t);
-        if (past) {
-            const int at = __builtin_ctzll(past);
-            const int32_t from = __builtin_amdgcn_readlane(lo, at), end = __builtin_amdgcn_readlane(hi, at);
-            const int64_t first = from + (int64_t)(t - (__builtin_amdgcn_readlane(sum, at) - __builtin_amdgcn_readlane(n, at))) * bm;
-            if (first < from || first >= end) break;  // offsets that no sort gives: their sum may have left 32 bits
-            return {e0 + at < experts ? e0 + at : -1, first, (int32_t)(end - first < bm ? end - first : bm)};
-        }
-        t -= __builtin_amdgcn_readlane(sum, 63);
+// The row tile of a workgroup.
+struct FbWave {
+    template <typename F>
+    static __device__ __forceinline__ int32_t each(F f) {
+        return f((int)(threadIdx.x & 63));
     }
-    return {-1, 0, 0};
+    static __device__ __forceinline__ int32_t own(int32_t v, int) { return v; }
+    static __device__ __forceinline__ int32_t scan(int32_t v) { return fb_scan(v); }
+    static __device__ __forceinline__ uint64_t above(int32_t v, int32_t t) { return __ballot(v > t); }
+    static __device__ __forceinline__ int32_t lane(int32_t v, int i) { return __builtin_amdgcn_readlane(v, i); }
+};
+__device__ __forceinline__ Fp8Tile fb_find_tile(const int32_t *offsets, int32_t experts, int64_t rows, int32_t bm, int32_t t) {
+    return fb_find_tile_by<FbWave>([=](int32_t i) { return (int64_t)offsets[i]; }, experts, rows, bm, t);
 }
 
 // The row of x that output row p takes.
@@ -199,12 +190,14 @@ __device__ __forceinline__ float fb_scaled(float d, float sx, float sw, float s,
 
 // g / (1 + e^-g) * u.  For 16-bit outputs the hardware's exponential and reciprocal, each within 1 ulp of binary32; the
 // roundings of the argument make the exponential off by |g| * 2^-23 of itself at most.
-// Below -80 the quotient is g * e^g (to e^-80 of itself).  e^-g leaves binary32 there (from -88.8 on), and the hardware's
-// reciprocal gives no subnormal numbers (from -87.4 on), while the value with u need not be small: the fourth root of e^g
-// is in range as far as u can make up for it.  u comes after the first factor, so that only the value itself underflows.
-template <int OT>
+// Below -80 (FAR: gates may be) the quotient is g * e^g (to e^-80 of itself).  e^-g leaves binary32 there (from -88.8 on),
+// and the hardware's reciprocal gives no subnormal numbers (from -87.4 on), while the value with u need not be small: the
+// fourth root of e^g is in range as far as u can make up for it.  u comes after the first factor, so that only the value
+// itself underflows.
+constexpr float FB_FAR_GATE = -80.0f;
+template <int OT, bool FAR = true>
 __device__ __forceinline__ float fb_gate(float g, float u) {
-    if (g < -80.0f) {
+    if (FAR && g < FB_FAR_GATE) {
         const float h = OT == 0 ? expf(0.25f * g) : __builtin_amdgcn_exp2f(g * 0.36067376f);
         return g * h * u * h * h * h;
     }

@@ -315,3 +315,52 @@ def test_types_that_no_call_takes_are_refused_as_such(gpus, monkeypatch, dtype):
         with pytest.raises(nq.NqError) as refused:
             call()
         assert refused.value.status == 8
+
+
+# --- the wave's search of a tile --------------------------------------------------------------------------------
+
+def search(emu, offsets, rows, bm, t):
+    """What the kernels' wave finds for tile t, and what the rule says: (expert, first, count) each."""
+    o, found, rule = np.array(offsets, np.int32), np.zeros(3, np.int64), np.zeros(3, np.int64)
+    emu.nq_fp8_emu_search.argtypes = [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p]
+    emu.nq_fp8_emu_search(o.ctypes.data, o.size - 1, rows, bm, t, found.ctypes.data, rule.ctypes.data)
+    return found.tolist(), rule.tolist()
+
+
+@pytest.mark.parametrize("bm", [16, 64, 128, 256])
+def test_the_waves_search_follows_the_rule(emu, bm):
+    """Every tile of offsets that a sort gives, and those past the last."""
+    rng = np.random.default_rng(bm)
+    for trial in range(60):
+        experts = int(rng.choice([1, 2, 5, 62, 63, 64, 65, 127, 128, 200, 1024]))
+        counts = rng.choice([0, 0, 1, bm - 1, bm, bm + 1, 3 * bm + 5], experts)
+        offsets = np.concatenate([[0], np.cumsum(counts)])
+        rows = int(offsets[-1]) + int(rng.choice([0, 0, 1, bm, 2 * bm + 3]))
+        tiles = int(sum(-(-c // bm) for c in counts)) + -(-(rows - int(offsets[-1])) // bm)
+        for t in range(tiles + 3) if tiles < 60 else np.unique(np.r_[0, tiles - 1, tiles, tiles + 2, rng.integers(0, tiles, 40)]):
+            found, rule = search(emu, offsets, rows, bm, int(t))
+            assert found == rule if t < tiles else found[2] == rule[2] == 0, (experts, rows, t)
+    # many rows of one expert, and 2^30 rows
+    for offsets, rows in (([0, 2 ** 30], 2 ** 30), ([0] * 900 + [2 ** 30] * 124, 2 ** 30), ([0, 5, 2 ** 30 - 7], 2 ** 30)):
+        for t in np.r_[0, 1, 2 ** 30 // bm - 1, 2 ** 30 // bm, 2 ** 30 // bm + 2, rng.integers(0, 2 ** 30 // bm, 20)]:
+            found, rule = search(emu, offsets, rows, bm, int(t))
+            assert found == rule or (found[2] == rule[2] == 0), (rows, t)
+
+
+def test_the_waves_search_of_any_offsets_stays_inside(emu):
+    """Offsets that no sort gives, sums past 32 bits among them: a tile lies within the rows, and within what its expert's
+    offsets say of them."""
+    rng = np.random.default_rng(1)
+    for trial in range(4000):
+        experts, rows = int(rng.choice([1, 3, 63, 64, 70, 300, 1024])), int(rng.choice([1, 17, 300, 2 ** 20 + 3, 2 ** 30]))
+        bm = int(rng.choice([16, 64, 128, 256]))
+        offsets = rng.choice([-2 ** 31, -5, 0, 1, rows // 2, rows - 1, rows, min(rows + 1, 2 ** 31 - 1), 2 ** 31 - 1], experts + 1)
+        if trial % 3 == 0:  # from 0 to all rows and back: every second segment has them all
+            offsets = np.arange(experts + 1) % 2 * rows
+        t = int(rng.choice([0, 1, 7, rows // bm, rows // bm + experts, 2 ** 26, 2 ** 31 - 1]))
+        (e, first, count), _ = search(emu, offsets, rows, bm, t)
+        assert 0 <= count <= bm and -1 <= e < experts
+        if count:
+            lo = np.clip(offsets[e if e >= 0 else experts], 0, rows)
+            hi = np.clip(offsets[e + 1], 0, rows) if e >= 0 else rows
+            assert lo <= first and first + count <= hi <= rows, (offsets[:8], rows, bm, t)
