@@ -364,3 +364,43 @@ def test_the_waves_search_of_any_offsets_stays_inside(emu):
             lo = np.clip(offsets[e if e >= 0 else experts], 0, rows)
             hi = np.clip(offsets[e + 1], 0, rows) if e >= 0 else rows
             assert lo <= first and first + count <= hi <= rows, (offsets[:8], rows, bm, t)
+
+
+# --- what the GPU tests reach -----------------------------------------------------------------------------------
+
+def test_the_sizes_of_the_gpu_tests_reach_every_instance(emu):
+    """On 256 compute units, which an MI355X has: every tile and form of the many-rows kernel that the plan can choose, each in
+    pieces too where it can be, with more than sixteen blocks of K in a piece (scales of two places in turn where there are
+    two buffers, both halves of them where there are four); the few-rows kernel with each number of weight tiles, and with
+    codes in LDS that are replaced."""
+    from fp8_cases import EXPERTS, FAR, FAR_EXPERTS, FEW, FEW_EXPERTS, PRODUCTS
+    seen, pieces, odd = set(), set(), set()
+    for far, one, several in ((0, PRODUCTS, EXPERTS), (1, FAR, FAR_EXPERTS)):
+        for m, n, kb, gated, wide in one:
+            p = plan(emu, m, m, 0, n, 128 * kb, gated, far, 1, wide, far)
+            key = (p.config, "one", gated, wide)
+            assert not p.few
+            if p.per_split > 16:
+                (seen if p.splits == 1 else pieces).add(key)
+            if p.per_split > 16 and p.per_split % 2:
+                odd.add(key)
+        for tokens, top, experts, n, kb, gated, wide in several:
+            p = plan(emu, tokens, tokens * top, experts, n, 128 * kb, gated, far, 1, wide, far)
+            assert not p.few
+            if p.per_split > 16:
+                seen.add((p.config, "experts", gated, wide))
+    every = {(c, kind, g, w) for c in range(6) for kind in ("one", "experts") for g in (0, 1) for w in (0, 1) if not (c == 2 and w)}
+    assert seen == every
+    assert pieces >= {k for k in every if k[1] == "one" and k[0] != 5}
+    assert odd >= {k for k in every if k[1] == "one" and k[0] in (1, 2, 4, 5)}
+    tiles, refilled = set(), set()
+    for m, n, kb, gated in FEW:
+        p = plan(emu, m, m, 0, n, 128 * kb, gated)
+        tiles.add((p.weight_tiles, gated, "values" if not p.quantize else "codes"))
+        refilled.add(p.few and not p.quantize and kb > p.chunk and ("one", kb % p.chunk > 0))
+    for tokens, top, experts, n, kb, gated in FEW_EXPERTS:
+        p = plan(emu, tokens, tokens * top, experts, n, 128 * kb, gated)
+        tiles.add((p.weight_tiles, gated, "values" if not p.quantize else "codes"))
+        refilled.add(p.few and not p.quantize and kb > p.chunk and ("experts", kb % p.chunk > 0))
+    assert tiles == {(t, g, x) for t, g in ((1, 0), (2, 0), (2, 1), (4, 1)) for x in ("values", "codes")}
+    assert refilled >= {("one", True), ("experts", False)}
