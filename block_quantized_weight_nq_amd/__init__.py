@@ -1076,8 +1076,10 @@ def gemm_fp8_block(weight, x, x_scales=None, gated=False, out_dtype=None, stream
     x: [rows, K] float32, float16 or bfloat16 (any row stride), rounded to E4M3 blocks of one row and 128 columns within
     the call; or codes float8_e4m3fn with x_scales float32 [rows, K / 128], as quantize_fp8_block returns them.
     gated: the weight's first N / 2 rows are gates, the others up (N a multiple of 256); returns silu(gate) * up,
-    [rows, N / 2].  out_dtype: default x's type (float32 for codes).  Sums are binary32; binary32 outputs and calls of up
-    to 16 rows multiply exactly, others on the 8-bit matrix instructions (include/nq.h states the difference).
+    [rows, N / 2].  out_dtype: default x's type (float32 for codes).  float32 outputs and calls of up to 16 rows have
+    exact products and binary32 sums; 16-bit outputs of more rows use the 8-bit matrix instructions, which drop up to
+    2^-10 of the largest of each eight products: less than the output's rounding, unless products cancel.  Ask for
+    float32 where that matters (include/nq.h states the arithmetic).
     """
     if weight.experts:
         raise ValueError("an [experts, N, K] weight takes moe_gemm_fp8_block")

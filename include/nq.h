@@ -518,8 +518,9 @@ int nq_dequantize_fp8_block(const void *codes, const float *scales, int64_t matr
  *               places.
  * Pairs of one expert keep their order (a stable sort).  order and places
  * have tokens * top entries, offsets experts + 1.  1 <= experts <= 1024 and
- * 1 <= top <= 1024 (NQ_ERR_BAD_DIM below, NQ_ERR_OVERFLOW above).  The calls below take them as device memory and check them there:
- * no value leads outside the buffers that the arguments describe.
+ * 1 <= top <= 1024 (NQ_ERR_BAD_DIM below, NQ_ERR_OVERFLOW above).  The calls
+ * below take them as device memory and check them there: no value leads
+ * outside the buffers that the arguments describe.
  *
  * nq_moe_sort: ids [tokens, top], int32, or int64 where `wide` is 1
  * (NQ_ERR_BAD_DTYPE for other values of it).  The workspace
@@ -547,7 +548,11 @@ int nq_moe_sort(const void *ids, int32_t wide, int64_t tokens, int64_t top, int6
  * and then by sw.  Up to 16 rows, and for binary32 outputs, products of
  * codes are exact; for 16-bit outputs of more rows the 8-bit matrix
  * instruction adds eight products at a time and drops what lies 2^-13 below
- * the largest of the eight.
+ * the largest of the eight.  That is at most 7 * 2^-13 of the sum of those
+ * largest products, below a 16-bit output's rounding unless products cancel:
+ * then a result near zero may be off by many of its steps, and differ from
+ * what a call of up to 16 rows gives.  out_dtype NQ_F32 has binary32 sums for
+ * any number of rows.
  * plan NULL: one weight [N, K] for all rows.  Otherwise weight is [experts, N,
  * K] and output row p is the product of the expert whose place p is: of row p
  * of x where `sorted` is 1 (rows = tokens * top), else of row order[p] / top

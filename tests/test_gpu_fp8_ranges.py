@@ -118,3 +118,24 @@ def test_gates_far_below_zero(m, k, out):
     inside = np.abs(want) < most
     got = y.masked_fill(torch.as_tensor(~inside, device=DEV), 0)
     fp8_ref.check(got, np.where(inside, want, 0), np.where(inside, rel, 0), "far gates")
+
+
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("m", [16, 17, 300])
+def test_sums_whose_large_products_cancel(m, out):
+    """Of every eight products one is 448 * 448, one -448 * 448 and one 1: the sum is the number of eights.  Up to 16 rows and
+    in binary32 outputs it is exact (so each partial sum in binary32 is: multiples of 1 below 2^24).  The 8-bit matrix
+    instruction of the others may lose 7 * 2^-13 of the largest product of each eight, here more than the result."""
+    n, k = 130, 1152
+    xw, ww = np.zeros((m, k), np.uint8), np.zeros((n, k), np.uint8)
+    xw[:, 0::8], ww[:, 0::8] = 0x7E, 0x7E
+    xw[:, 3::8], ww[:, 3::8] = 0x7E, 0xFE
+    xw[:, 6::8], ww[:, 6::8] = 0x38, 0x38
+    one = lambda rows: torch.ones((rows, k // 128), device=DEV)  # noqa: E731
+    y = nq.gemm_fp8_block(nq.Fp8Weight(up(ww), one(2)), up(xw), one(m), out_dtype=DT[out]).double()
+    off = float((y - k // 8).abs().max())
+    print(f"{m} rows, {out}: off by {off}")
+    if m <= 16 or out == "f32":
+        assert off == 0  # 144, which every type holds
+    else:
+        assert off <= 7 * 2.0 ** -13 * 448 * 448 * (k // 8)
