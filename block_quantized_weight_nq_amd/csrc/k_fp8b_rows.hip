@@ -203,7 +203,6 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
         return v;
     };
     float most = 0.0f;  // the largest sx * sw so far
-    constexpr int SPREAD = TN > 8 ? TN / 8 : 1, PER = (NW + NX + SPREAD - 1) / SPREAD;
     const auto multiply = [&](auto more, const uint8_t *b, const auto &sw, int32_t kb, uint8_t *b_next, auto &sw_next, int32_t kb_next) {
         fb_i8 xf[TM];
         float sx[TM];
@@ -226,9 +225,11 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
             __builtin_amdgcn_sched_barrier(0);
             if (i < TN) {
                 if constexpr (more()) {
-                    if (i == 0) load_weight_scales(sw_next, kb_next);
+                    if (i == 0) {
+                        load_weight_scales(sw_next, kb_next);
 #pragma unroll
-                    for (int l = PER * i; l < PER * (i + 1) && l < NW + NX; l++) load(b_next, kb_next, l);
+                        for (int l = 0; l < NW + NX; l++) load(b_next, kb_next, l);
+                    }
                 }
                 const fb_i8 now = wf;
                 if (i + 1 < TN) wf = fetch(b, 16 * (wn * TN + i + 1));

@@ -201,7 +201,7 @@ __device__ __forceinline__ void moe_read(const void *x, int64_t i, float (&f)[N]
     if constexpr (N == 1)
         f[0] = kv_read<DT>(x, i);
     else
-        fb_read8<DT, true>(x, i, f);
+        fb_read8<DT>(x, i, f);
 }
 
 // FAR: more bytes than the L2s hold, which go past them.

@@ -6,13 +6,10 @@
 
 namespace nq {
 
-// Eight consecutive elements of type IN as binary32; VEC: the address is a multiple of 16 bytes.
-template <int IN, bool VEC>
+// Eight consecutive elements of type IN as binary32, the address a multiple of 16 bytes.
+template <int IN>
 __device__ __forceinline__ void fb_read8(const void *x, int64_t i, float (&f)[8]) {
-    if constexpr (!VEC) {
-#pragma unroll
-        for (int j = 0; j < 8; j++) f[j] = kv_read<IN>(x, i + j);
-    } else if constexpr (IN == 0) {
+    if constexpr (IN == 0) {
 #pragma unroll
         for (int v = 0; v < 2; v++) {
             const kv_f4 w = *(const kv_f4 *)((const float *)x + i + 4 * v);
