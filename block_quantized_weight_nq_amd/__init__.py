@@ -873,6 +873,8 @@ def kv_attention(cache, q, token_start, lengths, table, scale=None, window=0, ma
 
 # --- E4M3 blocks of 128, and rows sorted by expert ----------------------------------------------------------------
 
+# No call records an autograd graph: results do not require gradients, whatever their inputs do.  moe_combine_grad and
+# moe_combine (for moe_gather) give the gradients that there are; a torch.autograd.Function around them is the caller's.
 # Types go to the library as _KV_DTYPES' codes, -1 for what it refuses as NQ_ERR_BAD_DTYPE.
 _BLOCK_ARGS, _PLAN_ARGS = struct.Struct("@PqPPPPqqqiiii"), struct.Struct("@PPPqqq")
 assert _BLOCK_ARGS.size == ctypes.sizeof(Fp8BlockArgs) and _PLAN_ARGS.size == ctypes.sizeof(MoePlanDesc)
@@ -1079,7 +1081,8 @@ def gemm_fp8_block(weight, x, x_scales=None, gated=False, out_dtype=None, stream
     [rows, N / 2].  out_dtype: default x's type (float32 for codes).  float32 outputs and calls of up to 16 rows have
     exact products and binary32 sums; 16-bit outputs of more rows use the 8-bit matrix instructions, which drop up to
     2^-10 of the largest of each eight products: less than the output's rounding, unless products cancel.  Ask for
-    float32 where that matters (include/nq.h states the arithmetic).
+    float32 where that matters (include/nq.h states the arithmetic).  No autograd graph is recorded, and the product has no
+    gradient.
     """
     if weight.experts:
         raise ValueError("an [experts, N, K] weight takes moe_gemm_fp8_block")
@@ -1096,7 +1099,7 @@ def moe_gemm_fp8_block(weight, x, plan, x_scales=None, sorted_rows=False, gated=
     """Each expert's product with its own rows, in the plan's order: [pairs, N] (gated: [pairs, N / 2]), zeros behind the
     last place.  weight: Fp8Weight [experts, N, K]; x: one row for each token, which the product takes in the plan's
     order, or with sorted_rows one for each place (as a product before this one returned them).  The other arguments
-    are gemm_fp8_block's."""
+    are gemm_fp8_block's; "up to 16 rows" is tokens * top / experts.  No autograd graph is recorded."""
     if not weight.experts:
         raise ValueError("an [N, K] weight takes gemm_fp8_block")
     if stream is not None:
@@ -1154,7 +1157,7 @@ def moe_sort(ids, experts, stream=None):
 
 def moe_gather(x, plan, stream=None):
     """The rows of x [tokens, cols] (any type, columns contiguous) in the plan's order, [pairs, cols], zeros behind the last
-    place.  The gradient of x is moe_combine(gradient of the rows, plan)."""
+    place.  No autograd graph is recorded: the gradient of x is moe_combine(gradient of the rows, plan)."""
     index = plan.index
     if stream is not None:
         with _on(stream, index):
@@ -1182,7 +1185,8 @@ def _weights_of(weights, plan):
 
 def moe_combine(rows, plan, weights=None, stream=None):
     """The sorted rows [pairs, cols] (float32, float16 or bfloat16) back to their tokens: [tokens, cols], each the sum of
-    its rows times weights (float32 [tokens, top], 1 if not given), summed in binary32 in the order of the choices."""
+    its rows times weights (float32 [tokens, top], 1 if not given), summed in binary32 in the order of the choices.  No
+    autograd graph is recorded: moe_combine_grad gives the gradients."""
     index = plan.index
     if stream is not None:
         with _on(stream, index):
@@ -1206,7 +1210,7 @@ def moe_combine(rows, plan, weights=None, stream=None):
 def moe_combine_grad(grad, rows, plan, weights=None, stream=None):
     """The gradients of moe_combine(rows, plan, weights) for its result's gradient grad [tokens, cols] (rows' type):
     (grad_rows [pairs, cols] in that type, 0 behind the last place; grad_weights float32 [tokens, top], 0 for pairs left
-    out, None without weights)."""
+    out, None without weights).  For a torch.autograd.Function of the caller's, since moe_combine records no graph."""
     index = plan.index
     if stream is not None:
         with _on(stream, index):
