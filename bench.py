@@ -16,14 +16,18 @@ reports:
                  same read and write bytes (nq_measure_stream)
   cpu_baseline   the oracle, single-threaded and pinned to one host core, on
                  a bounded sample (the first third of each tensor's blocks)
-  per_format     every format of the step; every one of the 28 formats at
-                 [14336, 4096] -> bf16; the remaining workloads (q8_0/q4_0
+  per_format     every format of the step; the GB/s of every one of the 28
+                 formats at [14336, 4096] -> bf16, of the streaming ceilings
+                 and of the remaining workloads (q8_0/q4_0
                  [64, 4096] -> f32, launch-bound; q4_k/q6_k [4096, 4096];
                  mxfp4/nvfp4 [14336, 4096]; the IQ set [4096, 14336] to f32
                  and bf16), each timed over rotating replicas so no launch
                  reads a payload out of a warm cache
 
-Usage: python bench.py [--gpus 1] [--steps K] [--warmup W]
+The line stays under LINE_CHARS characters; --details FILE has the whole
+record, every workload's bytes, times and ceilings among it.
+
+Usage: python bench.py [--gpus 1] [--steps K] [--warmup W] [--details FILE]
        python bench.py --formats gguf:q6_k,nvfp4 --shapes 14336x4096,4096x4096   (profiling target)
 """
 import argparse
@@ -35,6 +39,7 @@ import time
 
 METRIC = "decode GB/s (payload+output) per format & % of HBM peak, 1×MI355X"
 HBM_PEAK_GBPS = 8000.0  # MI355X HBM3E, vendor figure
+LINE_CHARS = 7500  # a reader that keeps the last 8000 characters of the output has the whole line
 OUT_CODES = {"f32": 0, "f16": 1, "bf16": 2, "f64": 3}
 OUT_SIZE = {"f32": 4, "f16": 2, "bf16": 2, "f64": 8}
 
@@ -592,6 +597,24 @@ def gemv_cpu_baseline(synth, fmt="gguf:q4_k", shape=(14336, 4096), rows=14336, s
             "weights_per_s": round(rows * K / secs, 1)}
 
 
+def short_line(record):
+    """The record that the last line holds: of each workload and ceiling its GB/s (a product's TOP/s) alone.  Where that is
+    still too long, the workloads but the 28 formats go first, then those."""
+    rate = lambda m: m.get("gbps", m.get("tops"))  # noqa: E731
+    line = dict(record)
+    line["roofline"] = {k: v for k, v in record["roofline"].items() if k != "copy_ceiling"}
+    line["roofline"]["copy_ceiling_gbps"] = rate(record["roofline"]["copy_ceiling"])
+    per = record["per_format"]
+    rates = {k: rate(m) for k, m in per["workloads"].items()}
+    formats = {k: v for k, v in rates.items() if k.startswith("all_formats ")}
+    for kept in (rates, formats, {}):
+        line["per_format"] = {"step": per["step"], "ceilings_gbps": {k: rate(m) for k, m in per["ceilings"].items()},
+                              "workloads_gbps": kept}
+        if len(json.dumps(line)) <= LINE_CHARS:
+            break
+    return line
+
+
 def product_cases(cases, args):
     """The (format, M) product cases to measure: all, or those --cases names."""
     if not args.cases:
@@ -677,6 +700,7 @@ def main():
     ap.add_argument("--shapes", default="14336x4096", metavar="RxC,...", help="shapes for --formats")
     ap.add_argument("--dtype", default="bf16", choices=sorted(OUT_CODES), help="output type for --formats")
     ap.add_argument("--launches", type=int, default=60, help="launches per timed replay for --formats")
+    ap.add_argument("--details", default="", metavar="FILE", help="write the whole record there as JSON")
     ap.add_argument("--calibrate-copy", type=int, default=0, metavar="MiB",
                     help="first run a plain device copy of this many MiB (for counter calibration)")
     args = ap.parse_args()
@@ -829,7 +853,7 @@ def main():
         cpu = cpu_baseline(nq, synth, tensors)
         log(f"cpu baseline: {cpu['value']} GB/s ({cpu['sample']}; {cpu['cpu_model']}, nproc {cpu['nproc']})")
 
-    line = {
+    record = {
         "metric": METRIC, "value": round(value, 1), "unit": "GB/s", "n_gpus": 1, "steps": args.steps,
         "warmup": args.warmup, "ms_per_step": round(ms_per_step, 4), "higher_is_better": True, "scaling": "weak",
         "vs_baseline": None, "dtype": "f32", "data": "synthetic",
@@ -849,7 +873,10 @@ def main():
         "cpu_baseline": cpu,
         "per_format": {"step": formats, "ceilings": ceilings, "workloads": extra},
     }
-    print(json.dumps(line), flush=True)
+    if args.details:
+        with open(args.details, "w") as f:
+            json.dump(record, f, indent=1)
+    print(json.dumps(short_line(record)), flush=True)
 
 
 if __name__ == "__main__":
