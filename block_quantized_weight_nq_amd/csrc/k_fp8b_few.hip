@@ -7,8 +7,8 @@
 // lanes that multiply with them, and nothing is staged.  A wave takes 16 * NT weight rows and every W-th block of 128
 // columns; the W waves' sums join through LDS in a fixed order.  Lane (j, g) of 16 x 4 holds columns 16 g .. 16 g + 15
 // and 64 + 16 g .. 64 + 16 g + 15 of a block, for weight row j and for row j of x alike, so the order in which the
-// instruction takes them does not matter.  One row of gated [28672, 4096]: 24.0 us, 4.9 TB/s of the 5.0 that a copy moves;
-// 32 pairs on 64 experts of gated [2816, 2048], 144 MB where 25 of them are busy: 30.4 us, 4.7 TB/s.  (Loads of the weight
+// instruction takes them does not matter.  One row of gated [28672, 4096]: 24.2 us, 4.9 TB/s of the 5.0 that a copy moves;
+// 32 pairs on 64 experts of gated [2816, 2048], 144 MB where 25 of them are busy: 31.2 us, 4.6 TB/s.  (Loads of the weight
 // that go past the L2s are slower; 32 and 64 rows a workgroup take 110 us for 33 to 64 rows of [28672, 4096], the kernel for
 // many rows 32.)
 //

@@ -21,11 +21,11 @@
 // blocks' scales of the tile's rows go there as well, and the weight's scales come by scalar loads, so that the loads to
 // LDS are all that is counted.  Each buffer is an array of its own: reads of one then do not wait for loads to the others.
 //
-// What bounds it: 8192 rows of gated [28672, 4096] 830 to 860 us with their quantisation (20), 2.3 PFLOP/s; matrix pipes
-// are busy in 58% of the cycles, and the clock falls to 1.7 to 1.9 GHz under that load (without its loads the kernel took
-// 640 to 730 us, without its products 480 to 550).  8192 x 8 rows of 64 gated [2816, 2048] 475 us, 1.6
+// What bounds it: 8192 rows of gated [28672, 4096] 810 to 860 us with their quantisation (20), 2.3 PFLOP/s; matrix pipes
+// are busy in 56% of the cycles, and the clock falls to 1.7 to 1.9 GHz under that load (without its loads the kernel took
+// 640 to 730 us, without its products 480 to 550).  8192 x 8 rows of 64 gated [2816, 2048] 455 to 500 us, 1.5 to 1.7
 // PFLOP/s at 2.0 GHz: 16 blocks a tile, between which a workgroup starts and writes its outputs.  77 rows of [4096, 14336]:
-// 16.6 us in four pieces of K and 4.5 for the join: start, 28 blocks at 0.34 us, end.
+// 16.7 us in eight pieces of 14 blocks of K (59 MB of weight read and 10 MB of sums written, 4.1 TB/s) and 4.5 for the join.
 #include "nq_fp8b_codes.h"
 
 #include <type_traits>
@@ -243,7 +243,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_fp8_rows(Fp8GemmLaunch a) {
 #pragma unroll
                     for (int k = 0; k < TM; k++) {
                         f[k] = sx[k] * sw.v[(i - 1) / H];
-                        most = fmaxf(most, fabsf(f[k]));
+                        most = fmaxf(most, fabsf(f[k]));  // (3% more vector instructions, 1 to 2% of the largest calls' time)
                     }
                 }
 #pragma unroll

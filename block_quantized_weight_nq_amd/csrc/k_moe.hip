@@ -10,7 +10,7 @@
 // they only count.
 //
 // Up to 4096 pairs are one launch of one workgroup (40 pairs 2.6 us), where latency is all; more are two (131072 pairs of
-// 256 experts 5.0 + 9.2 us, 16 M pairs 270 us): a workgroup reads the counts of all, which is cheaper than a third launch
+// 256 experts 4.9 + 9.6 us, 16 M pairs 270 us): a workgroup reads the counts of all, which is cheaper than a third launch
 // between them.  The rows' kernels are bound by the bytes they move: 16384 rows of 4 KB to 131072 places 106 us (5.7 TB/s),
 // 65536 rows of 4 KB back to 8192 tokens 61 us (5.0 TB/s), their gradients 119 us (4.8 TB/s).
 #include "nq_fp8b_codes.h"
@@ -20,7 +20,11 @@ namespace nq {
 namespace {
 
 constexpr int MOST_EXPERTS = 1024;
-constexpr int64_t FAR_BYTES = 32 << 20;  // eight L2s of 4 MB
+// Outputs of more bytes than this go past the L2s (eight of 4 MB).  8 choices of 64 experts, 2048 bfloat16 values, us past
+// them / through them, by the outputs' MB: gather 32: 7.6 / 7.8, 64: 14.8 / 12.5, 128: 26.2 / 23.8, 256: 52 / 55, 512: 104 / 125;
+// gradients 16: 11.3 / 12.4, 32: 15.0 / 20.8, 64: 29.7 / 27.6, 128: 58 / 54, 256: 114 / 120, 512: 230 / 236.  Between 64 and
+// 128 MB the last cache would keep them for the next call (gather and combine of 64 MB 30.0 / 25.5, of 512 MB 240 / 272).
+constexpr int64_t FAR_BYTES = 32 << 20;
 
 __device__ __forceinline__ int32_t moe_id(const MoeSortLaunch &a, int64_t i) {
     if (a.wide) {
@@ -168,7 +172,10 @@ int launch_moe_sort(const MoeSortLaunch &L, hipStream_t s) {
 // The kernels below have G threads a row: a workgroup, a wave or a quarter of one.  Narrow rows would leave most of a
 // workgroup idle, wide ones of a wave's keep less on their way (9834 tokens x 6, bfloat16, combine and gradients, threads a
 // row: 136 values 56 us with 256 and 24 with 16, 512 values 60 and 40 with 64, 1024 values 94 and 89; 8192 x 8, 2048 values
-// 178 and 201), and few tokens would leave compute units idle.
+// 178 and 201), and few tokens would leave compute units idle.  The gradient alone with 16, 64 and 256 threads: 16384 x 8
+// pairs, 64 values 13 / 28 / 86 us, 256 values 38 / 46 / 115, 512 values 69 / 59 / 135, 1024 values 129 / 114 / 167, 2048 values
+// 285 / 247 / 230; 4096 x 8, 64 values 10 / 13 / 23, 512 values 41 / 22 / 35, 2048 values 159 / 70 / 58; 1024 x 8, 512 values 26 / 11 /
+// 12, 1024 values 48 / 17 / 13.  (At 4096 x 8 of 256 values the rule's 16 take 17 us, 64 would 14.)
 
 // Rows of bytes to the places of their token's pairs: a row is read once, whatever the number of its places.  Places
 // behind the last get zeros.

@@ -121,6 +121,10 @@ __host__ __device__ inline Fp8Tile fb_find_tile_by(At at, int32_t experts, int64
 // with the fourth, 26.0 with the second; 1024 rows of [28672, 4096] 173 and 151 (119 with the third).  The fifth has more
 // workgroups at a time, for many experts of few rows (1800 rows of 64 [2048, 1408] 43 us, 51 with the first).  The last is
 // the second for x beyond 32 bits.
+//
+// The model takes the mean load of the compute units, while the one with the most workgroups decides: where tiles are a few
+// more than there are units, it is a fifth to a quarter low (1536 rows of gated [2816, 10496], 264 tiles of 82 blocks: 72 us
+// for the blocks, while the eight units with two tiles take 94, and the call 93).
 struct Fp8Config {
     int32_t rows, cols, held, threads;
     float alone, full;
@@ -130,7 +134,13 @@ constexpr Fp8Config fb_configs[6] = {{64, 64, 2, 256, 0.30f, 0.42f}, {128, 128, 
 constexpr int FB_WIDEST = 2, FB_FAR = 5;
 constexpr int FB_DEEP_BLOCKS = 32;  // most blocks of a piece of K for the first and the fourth: their scales are loaded once
 
-constexpr int64_t FB_FEW_ROWS = 16;       // most rows of a weight, on average, that the few-rows kernel takes
+// Most rows of a weight, on average, that the few-rows kernel takes.  One weight: 17 rows are two workgroups' tiles, each of
+// which reads it.  Experts whose pairs fall at random (few-rows kernel / many-rows kernel, us; 8 choices): 64 gated
+// [2816, 2048] 77 / 78 at 8 rows, 73 / 79 at 12, 91 / 79 at 16, 108 / 80 at 20; 64 [2048, 1408] 42 / 44 at 4, 50 / 44 at 14,
+// 55 / 44 at 16; 256 gated [512, 2048] 55 / 62 at 4, 64 / 64 at 14, 71 / 65 at 16.  From 5 to 13 on,
+// by the weight, the many-rows kernel is faster: experts with more than 16 rows are read twice.  The border is also where exact
+// products end, and is the same for one weight.
+constexpr int64_t FB_FEW_ROWS = 16;
 constexpr int64_t FB_RAW_VALUES = 16384;  // most values of them that its workgroups make codes of, each for itself
 
 // Workgroup b's tile in the many-rows kernel.  Workgroups go to the eight XCDs in turn; `span` consecutive tiles stay on
@@ -179,6 +189,10 @@ inline Fp8Plan fb_plan(int64_t x_rows, int64_t rows, int64_t experts, int64_t N,
         if (!gated && fb_ceil(cols, 16) * busy <= cus) p.weight_tiles = 1;
         if (gated && fb_ceil(cols, 32) * busy >= cus + cus / 2) p.weight_tiles = 4;
         const int64_t groups = fb_ceil(cols, fb_few_cols(p.weight_tiles, gated)) * busy;
+        // waves that share K (one row, us with 2, 4 and 8): [4096, 14336], 256 workgroups, 26.8, 17.7, 15.0; [14336, 4096],
+        // 448, 15.1, 14.5, 17.3; gated [28672, 4096], 448, 28.8, 25.8, 32.5; [28672, 4096], 896, 27.0, 27.9, 31.1; gated
+        // [57344, 4096], 896, 51.0, 48.4, 58.2.  (Just above a workgroup a unit eight are late: [9216, 4096], 288, 12.2,
+        // 11.8, 14.8.)
         p.waves = 4 * groups <= 5 * cus ? 8 : groups <= 3 * cus ? 4 : 2;
         while (p.waves > 1 && p.waves > KB) p.waves /= 2;
         // one row of [28672, 4096] 27.1 us with codes made in each workgroup, 28.7 with a launch before; four rows of
