@@ -42,7 +42,7 @@ template <int XT, int NT, bool GATED>
 __global__ __launch_bounds__(64 * MAX_WAVES) void k_fp8_few(Fp8GemmLaunch a) {
     // codes of x, a block's rows together, and their scales; in the end the waves' sums, [wave][NT][lane]
     extern __shared__ __align__(16) uint8_t lds[];
-    __shared__ bool lost[MAX_WAVES];
+    __shared__ __align__(8) uint8_t lost[MAX_WAVES];
     const int tid = threadIdx.x, lane = tid & 63, j = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = a.waves;
     Fp8Tile t;
@@ -194,9 +194,7 @@ __global__ __launch_bounds__(64 * MAX_WAVES) void k_fp8_few(Fp8GemmLaunch a) {
     __syncthreads();
     // Where some sx * sw left binary32 (fb_scaled), the workgroup does all again with care (a choice at each block: 1 us of 34
     // for 4 x 8 pairs on 64 gated [2816, 2048]).
-    bool again = false;
-    for (int v = 0; v < waves; v++) again |= lost[v];
-    if (again) {
+    if (*(const uint64_t *)lost << (64 - 8 * waves)) {
         blocks(std::true_type());
 #pragma unroll
         for (int i = 0; i < NT; i++) red[(wave * NT + i) * 64 + lane] = acc[i];
